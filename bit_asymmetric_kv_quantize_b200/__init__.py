@@ -500,10 +500,10 @@ class PagedKiviCache(KiviCache):
 
 def ragged_lengths(st: torch.Tensor):
     """(n_q, r, status) lists of a ragged device state (copies it to the host)."""
-    v = st.cpu().view(torch.int64).view(-1, 2)
-    n_q = v[:, 0].tolist()
-    rs = v[:, 1].contiguous().view(torch.int32).view(-1, 2)
-    return n_q, rs[:, 0].tolist(), rs[:, 1].tolist()
+    v = st.cpu()
+    n_q = v.view(torch.int64).view(-1, 2)[:, 0].tolist()
+    rs = v.view(torch.int32).view(-1, 4)
+    return n_q, rs[:, 2].tolist(), rs[:, 3].tolist()
 
 
 def set_timing_events(start: Optional[torch.cuda.Event], stop: Optional[torch.cuda.Event]) -> None:
