@@ -37,7 +37,9 @@ EXPORTED = (
     "kivi_append_decode_dev", "kivi_ragged_prefill", "kivi_ragged_append", "kivi_ragged_decode",
     "kivi_ragged_append_decode", "kivi_paged_buffer_sizes", "kivi_paged_cache_init",
     "kivi_outlier_buffer_sizes", "kivi_cache_set_outliers", "kivi_host_step_bytes",
-    "kivi_append_decode_host",
+    "kivi_append_decode_host", "kivi_tree_workspace_bytes", "kivi_tree_decode",
+    "kivi_ragged_tree_decode", "kivi_ragged_tree_commit", "kivi_read_tokens",
+    "kivi_ragged_read_tokens", "kivi_qk_norm_rope",
 )
 OUTLIER_NAMES = ("k_out_idx", "k_out_val", "v_out_idx", "v_out_val")
 
@@ -66,6 +68,13 @@ class KiviCacheC(ctypes.Structure):
                 ("num_pages", ctypes.c_longlong),
                 ("k_out_idx", ctypes.c_void_p), ("k_out_val", ctypes.c_void_p),
                 ("v_out_idx", ctypes.c_void_p), ("v_out_val", ctypes.c_void_p)]
+
+
+class KiviRope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("rot", ctypes.c_int), ("axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
+                ("interleaved", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -111,6 +120,16 @@ def lib() -> ctypes.CDLL:
             L.kivi_paged_cache_init.argtypes = [cp, dp, ctypes.POINTER(vp * NUM_BUFFERS), vp, ci, ll]
             L.kivi_outlier_buffer_sizes.argtypes = [dp, ctypes.POINTER(sz * 4)]
             L.kivi_cache_set_outliers.argtypes = [cp, ctypes.POINTER(vp * 4)]
+            L.kivi_tree_workspace_bytes.argtypes = [cp, ci, ci]
+            L.kivi_tree_workspace_bytes.restype = sz
+            tree = [vp, vp, vp, vp, ci, ci, ctypes.c_float, vp, vp, sz, vp]
+            L.kivi_tree_decode.argtypes = [cp, *tree]
+            L.kivi_ragged_tree_decode.argtypes = [cp, vp, *tree]
+            L.kivi_ragged_tree_commit.argtypes = [cp, vp, vp, vp, ci, vp, vp, ci, vp]
+            L.kivi_read_tokens.argtypes = [cp, ll, ll, vp, vp, vp]
+            L.kivi_ragged_read_tokens.argtypes = [cp, vp, ll, ll, vp, vp, vp]
+            L.kivi_qk_norm_rope.argtypes = [ctypes.POINTER(KiviRope), vp, ll, vp, vp, vp, vp, vp,
+                                            vp, vp, vp]
             L.kivi_set_timing_events.argtypes = [vp, vp]
             L.kivi_set_timing_events.restype = None
             L.kivi_decode_num_splits.argtypes = [cp, ci]
@@ -202,6 +221,7 @@ class KiviCache:
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
         self._staging: Optional[torch.Tensor] = None
+        self._ws_tree: Optional[torch.Tensor] = None
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         self.shapes = {
@@ -442,6 +462,103 @@ class KiviCache:
                    "kivi_ragged_append_decode")
         return out
 
+    # -- drafted tokens (speculative decoding)
+    def _tree_args(self, q, k, v, mask, out):
+        if q.dim() != 4:
+            raise ValueError(f"q: expected shape (B, Hq, N, D), got {tuple(q.shape)}")
+        Hq, N = q.shape[1], q.shape[2]
+        pq = self._arg(q, (self.B, Hq, N, self.D), "q")
+        kv = (self.B, self.Hkv, N, self.D)
+        pk, pv = self._arg(k, kv, "k"), self._arg(v, kv, "v")
+        words = (self.B, N, (N + 31) // 32)
+        if (mask.device != self.device or mask.dtype != torch.int32 or tuple(mask.shape) != words
+                or not mask.is_contiguous()):
+            raise ValueError(f"mask: expected a contiguous int32 tensor of shape {words} on "
+                             f"{self.device}")
+        if out is None:
+            out = torch.empty_like(q)
+        po = self._arg(out, (self.B, Hq, N, self.D), "out")
+        with torch.cuda.device(self.device):
+            need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
+        if self._ws_tree is None or self._ws_tree.numel() < need:
+            self._ws_tree = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+        return (pq, pk, pv, mask.data_ptr(), N, Hq), po, out
+
+    def tree_decode(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor,
+                    softmax_scale: float, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Attention of N drafted tokens over the cache and each other (kivi_tree_decode):
+        q, out [B][Hq][N][D]; k, v [B][Hkv][N][D]; mask int32 [B][N][ceil(N / 32)], bit j of
+        node i's words set where it attends to node j (see tree_mask)."""
+        args, po, out = self._tree_args(q, k, v, mask, out)
+        with torch.cuda.device(self.device):
+            _check(lib().kivi_tree_decode(ctypes.byref(self._c), *args, float(softmax_scale), po,
+                                          self._ws_tree.data_ptr(), self._ws_tree.numel(),
+                                          self._stream()), "kivi_tree_decode")
+        return out
+
+    def ragged_tree_decode(self, st: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                           v: torch.Tensor, mask: torch.Tensor, softmax_scale: float,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """tree_decode of a ragged batch, every sequence over its own tokens."""
+        args, po, out = self._tree_args(q, k, v, mask, out)
+        with torch.cuda.device(self.device):
+            _check(lib().kivi_ragged_tree_decode(ctypes.byref(self._c), self._state_arg(st), *args,
+                                                 float(softmax_scale), po,
+                                                 self._ws_tree.data_ptr(), self._ws_tree.numel(),
+                                                 self._stream()), "kivi_ragged_tree_decode")
+        return out
+
+    def _state_arg(self, st: torch.Tensor) -> int:
+        if (st.device != self.device or st.dtype != torch.uint8 or st.numel() != 16 * self.B
+                or not st.is_contiguous()):
+            raise ValueError(f"st: expected the {16 * self.B}-byte state that ragged_prefill gave")
+        return st.data_ptr()
+
+    def ragged_tree_commit(self, st: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                           path: torch.Tensor, count: torch.Tensor) -> None:
+        """Append the accepted nodes path[b, :count[b]] of k, v [B][Hkv][N][D] to every
+        sequence (kivi_ragged_tree_commit).  path: int32 [B][P], count: int32 [B], on the device."""
+        if k.dim() != 4 or path.dim() != 2:
+            raise ValueError("k: expected shape (B, Hkv, N, D); path: expected shape (B, P)")
+        N, P = k.shape[2], path.shape[1]
+        kv = (self.B, self.Hkv, N, self.D)
+        pk, pv = self._arg(k, kv, "k"), self._arg(v, kv, "v")
+        for t, shape, name in ((path, (self.B, P), "path"), (count, (self.B,), "count")):
+            if (t.device != self.device or t.dtype != torch.int32 or tuple(t.shape) != shape
+                    or not t.is_contiguous()):
+                raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {shape} on "
+                                 f"{self.device}")
+        with torch.cuda.device(self.device):
+            _check(lib().kivi_ragged_tree_commit(ctypes.byref(self._c), self._state_arg(st), pk, pv,
+                                                 N, path.data_ptr(), count.data_ptr(), P,
+                                                 self._stream()), "kivi_ragged_tree_commit")
+
+    def _read_out(self, T: int, K, V):
+        shape = (self.B, self.Hkv, max(int(T), 0), self.D)
+        make = lambda: torch.zeros(shape, dtype=self.dtype, device=self.device)  # noqa: E731
+        K, V = make() if K is None else K, make() if V is None else V
+        return self._arg(K, shape, "K"), self._arg(V, shape, "V"), K, V
+
+    def read_tokens(self, t0: int, T: int, K: Optional[torch.Tensor] = None,
+                    V: Optional[torch.Tensor] = None):
+        """Tokens t0 .. t0+T-1 as numbers: (K, V), each [B][Hkv][T][D] (kivi_read_tokens)."""
+        pk, pv, K, V = self._read_out(T, K, V)
+        with torch.cuda.device(self.device):
+            _check(lib().kivi_read_tokens(ctypes.byref(self._c), t0, T, pk, pv, self._stream()),
+                   "kivi_read_tokens")
+        return K, V
+
+    def ragged_read_tokens(self, st: torch.Tensor, t0: int, T: int,
+                           K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None):
+        """read_tokens of a ragged batch; tokens that a sequence does not have are left as they
+        were in K and V (zeros in those made here)."""
+        pk, pv, K, V = self._read_out(T, K, V)
+        with torch.cuda.device(self.device):
+            _check(lib().kivi_ragged_read_tokens(ctypes.byref(self._c), self._state_arg(st), t0, T,
+                                                 pk, pv, self._stream()),
+                   "kivi_ragged_read_tokens")
+        return K, V
+
 
 class PagedKiviCache(KiviCache):
     """A ragged-batch cache whose quantized store is pages of R tokens from a
@@ -483,6 +600,7 @@ class PagedKiviCache(KiviCache):
                                            pages_per_seq, num_pages), "kivi_paged_cache_init")
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
+        self._ws_tree: Optional[torch.Tensor] = None
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         P = num_pages
@@ -496,6 +614,85 @@ class PagedKiviCache(KiviCache):
             "k_res": ((B, Hkv, R, D), dtype),
             "v_res": ((B, Hkv, R, D), dtype),
         }
+
+
+def tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """The mask of tree_decode for trees given by parents: int [B][N], the parent node of each
+    node (a lower number), or -1 for one that follows the cache's last token.  Each node attends
+    to itself and its ancestors.  Returned on the device of `parents`, made on the host."""
+    p = parents.detach().cpu().to(torch.int64)
+    if p.dim() != 2:
+        raise ValueError(f"parents: expected shape (B, N), got {tuple(p.shape)}")
+    B, N = p.shape
+    if bool((p >= torch.arange(N)).any()) or bool((p < -1).any()):
+        raise ValueError("parents: expected -1 or the number of an earlier node")
+    sees = torch.zeros(B, N, (N + 31) // 32 * 32, dtype=torch.int64)
+    rows = torch.arange(B)
+    for i in range(N):
+        up = p[:, i]
+        sees[:, i] = sees[rows, up.clamp(min=0)] * (up >= 0)[:, None]
+        sees[:, i, i] = 1
+    words = (sees.view(B, N, -1, 32) << torch.arange(32)).sum(-1)
+    return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32).to(parents.device)
+
+
+def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, Hq: int,
+                 Hkv: int, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, sections=None,
+                 interleaved: bool = False, out=None):
+    """Queries and keys normed for each head and turned by their positions, laid out by head
+    (kivi_qk_norm_rope).
+
+    qkv: [B][N][(Hq + 2 Hkv) * D], rows evenly spaced (a slice of a wider projection is taken as
+    it is).  positions: int64 [B][N], or [axes][B][N] with `sections` (pairs of channels that
+    turn by each axis).  inv_freq: float64 [rot / 2].  Weights: [D] of qkv's dtype, or None for
+    no norm.  Returns (q [B][Hq][N][D], k [B][Hkv][N][D], v [B][Hkv][N][D]); `out`: three such
+    tensors to write instead."""
+    if qkv.device.type != "cuda" or qkv.dim() != 3 or Hq < 1 or Hkv < 1 \
+            or qkv.shape[2] % (Hq + 2 * Hkv) != 0:
+        raise ValueError("qkv: expected a CUDA tensor of shape (B, N, (Hq + 2 Hkv) * D)")
+    B, N, width = qkv.shape
+    D = width // (Hq + 2 * Hkv)
+    stride = qkv.stride(1) if N > 1 else (qkv.stride(0) if B > 1 else width)
+    if qkv.stride(2) != 1 or (B > 1 and qkv.stride(0) != N * stride):
+        raise ValueError("qkv: expected evenly spaced rows of adjacent channels")
+    if positions.dim() == 2:
+        positions = positions[None]
+    axes = positions.shape[0] if positions.dim() == 3 else 0
+    if (positions.device != qkv.device or positions.dtype != torch.int64 or not 1 <= axes <= 4
+            or tuple(positions.shape[1:]) != (B, N) or not positions.is_contiguous()):
+        raise ValueError(f"positions: expected a contiguous int64 tensor of shape ({B}, {N}) or "
+                         f"(axes, {B}, {N}) on {qkv.device}")
+    if (inv_freq.device != qkv.device or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
+            or not inv_freq.is_contiguous()):
+        raise ValueError(f"inv_freq: expected a contiguous float64 vector on {qkv.device}")
+    rot = 2 * inv_freq.shape[0]
+    sections = [rot // 2] if sections is None else [int(x) for x in sections]
+    if len(sections) != axes:
+        raise ValueError(f"sections: expected one number for each of the {axes} axes")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.device != qkv.device or w.dtype != qkv.dtype
+                              or tuple(w.shape) != (D,) or not w.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous {qkv.dtype} vector of {D} on "
+                             f"{qkv.device}")
+    shapes = ((B, Hq, N, D), (B, Hkv, N, D), (B, Hkv, N, D))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=qkv.dtype, device=qkv.device) for s in shapes)
+    for t, s in zip(out, shapes):
+        if (t.device != qkv.device or t.dtype != qkv.dtype or tuple(t.shape) != s
+                or not t.is_contiguous()):
+            raise ValueError(f"out: expected contiguous {qkv.dtype} tensors of shapes {shapes} on "
+                             f"{qkv.device}")
+    p = KiviRope(B, N, Hq, Hkv, D, _dtype_code(qkv.dtype), rot, axes,
+                 (ctypes.c_int * 4)(*sections), int(bool(interleaved)), float(eps))
+    with torch.cuda.device(qkv.device):
+        _check(lib().kivi_qk_norm_rope(
+            ctypes.byref(p), qkv.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(),
+            q_weight.data_ptr() if q_weight is not None else None,
+            k_weight.data_ptr() if k_weight is not None else None,
+            *(t.data_ptr() for t in out), torch.cuda.current_stream(qkv.device).cuda_stream),
+            "kivi_qk_norm_rope")
+    return tuple(out)
 
 
 def ragged_lengths(st: torch.Tensor):

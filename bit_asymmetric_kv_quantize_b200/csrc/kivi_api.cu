@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "kivi.h"
+#include "kivi_draft.cuh"
 #include "kivi_internal.cuh"
 
 namespace {
@@ -328,6 +329,71 @@ int noalloc_scratch(void** out) {
 void touch_noalloc_scratch() {
   void* p = nullptr;
   (void)noalloc_scratch(&p);
+}
+
+}  // namespace
+
+namespace {
+
+// Drafted tokens a tree may have (rows of a KV head: Hq / Hkv times as many).
+constexpr int kMaxNodes = 256;
+// Query heads that may share a KV head in the tree calls (the rows of a group
+// are cut into row blocks, so any ratio will do; the bound keeps grids small).
+constexpr int kMaxTreeGq = 64;
+
+// Checks and launch shared by the two tree calls; state null: host counters.
+int tree_decode(const kivi_cache* c, const void* state, const void* q, const void* k,
+                const void* v, const uint32_t* mask, int N, int Hq, float softmax_scale, void* out,
+                void* workspace, size_t ws_bytes, void* stream, bool ragged) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if (ragged && (!state || ((uintptr_t)state & 15))) return KIVI_ERR_ARG;
+  if (!q || !k || !v || !mask || ((uintptr_t)mask & 3) || !out || Hq <= 0 ||
+      Hq % c->dims.Hkv != 0 || N < 1)
+    return KIVI_ERR_ARG;
+  const int gq = Hq / c->dims.Hkv;
+  if (N > kMaxNodes || gq > kMaxTreeGq || sparse(c->dims)) return KIVI_ERR_UNSUPPORTED;
+  if (ragged ? !is_ragged(c) : device_counted(c)) return KIVI_ERR_STATE;
+  const int sms = device_sms();
+  if (sms <= 0) return KIVI_ERR_CUDA;
+  const size_t need =
+      kivi::tree_workspace_bytes(c->dims.B, c->dims.Hkv, gq, c->dims.D, c->dims.dtype, N, sms);
+  if (!workspace || ((uintptr_t)workspace & 15) || ws_bytes < need) return KIVI_ERR_WORKSPACE;
+  touch_noalloc_scratch();
+  kivi::TreeArgs a;
+  a.c = view(c);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.mask = mask;
+  a.out = out;
+  a.part = (float*)workspace;
+  a.B = c->dims.B;
+  a.Hkv = c->dims.Hkv;
+  a.gq = gq;
+  a.D = c->dims.D;
+  a.bits = c->dims.bits;
+  a.dtype = c->dims.dtype;
+  a.meta = c->dims.meta;
+  a.N = N;
+  a.n_q = c->n_q;
+  a.r = c->r;
+  a.st = (const kivi::DevState*)state;
+  a.qscale = softmax_scale * kivi::kLog2e;
+  a.sms = sms;
+  return kivi::launch_tree(a, (cudaStream_t)stream) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
+}
+
+int read_tokens(const kivi_cache* c, const void* state, long long t0, long long T, void* K,
+                void* V, void* stream) {
+  if (T == 0) return KIVI_OK;
+  if (T / kivi::kTile + 2 > (long long)INT_MAX) return KIVI_ERR_UNSUPPORTED;
+  touch_noalloc_scratch();
+  return kivi::launch_read(view(c), c->dims.B * c->dims.Hkv, c->dims.Hkv, c->dims.D, c->dims.bits,
+                           c->dims.dtype, c->n_q, c->r, (const kivi::DevState*)state, t0, T, K, V,
+                           (cudaStream_t)stream) == cudaSuccess
+             ? KIVI_OK
+             : KIVI_ERR_CUDA;
 }
 
 }  // namespace
@@ -769,6 +835,124 @@ const char* kivi_status_string(int status) {
       return "KIVI_ERR_SCRATCH_LIMIT: request exceeds the fixed scratch of the no-allocation call";
   }
   return "unknown kivi status";
+}
+
+size_t kivi_tree_workspace_bytes(const kivi_cache* cache, int N, int Hq) {
+  if (check_cache(cache) != KIVI_OK || Hq <= 0 || Hq % cache->dims.Hkv != 0 || N < 1 ||
+      N > kMaxNodes || Hq / cache->dims.Hkv > kMaxTreeGq)
+    return 0;
+  const int sms = device_sms();
+  if (sms <= 0) return 0;
+  return kivi::tree_workspace_bytes(cache->dims.B, cache->dims.Hkv, Hq / cache->dims.Hkv,
+                                    cache->dims.D, cache->dims.dtype, N, sms);
+}
+
+int kivi_tree_decode(const kivi_cache* cache, const void* q, const void* k, const void* v,
+                     const uint32_t* mask, int N, int Hq, float softmax_scale, void* out,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return tree_decode(cache, nullptr, q, k, v, mask, N, Hq, softmax_scale, out, workspace,
+                     workspace_bytes, stream, false);
+}
+
+int kivi_ragged_tree_decode(const kivi_cache* cache, const void* state, const void* q,
+                            const void* k, const void* v, const uint32_t* mask, int N, int Hq,
+                            float softmax_scale, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return tree_decode(cache, state, q, k, v, mask, N, Hq, softmax_scale, out, workspace,
+                     workspace_bytes, stream, true);
+}
+
+int kivi_ragged_tree_commit(const kivi_cache* cache, void* state, const void* k, const void* v,
+                            int N, const int32_t* path, const int32_t* count, int P,
+                            void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (!state || ((uintptr_t)state & 15) || !k || !v || !path || ((uintptr_t)path & 3) || !count ||
+      ((uintptr_t)count & 3) || N < 1 || P < 1 || P > cache->dims.R)
+    return KIVI_ERR_ARG;
+  if (N > kMaxNodes) return KIVI_ERR_UNSUPPORTED;
+  if (!is_ragged(cache)) return KIVI_ERR_STATE;
+  touch_noalloc_scratch();
+  return kivi::launch_commit(view(cache), cache->dims.B, cache->dims.Hkv, cache->dims.D,
+                             cache->dims.bits, cache->dims.dtype, k, v, path, count, N, P,
+                             (kivi::DevState*)state, (cudaStream_t)stream) == cudaSuccess
+             ? KIVI_OK
+             : KIVI_ERR_CUDA;
+}
+
+int kivi_read_tokens(const kivi_cache* cache, long long t0, long long T, void* K, void* V,
+                     void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (device_counted(cache)) return KIVI_ERR_STATE;
+  const long long n = cache->n_q + cache->r;
+  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V))) return KIVI_ERR_ARG;
+  return read_tokens(cache, nullptr, t0, T, K, V, stream);
+}
+
+int kivi_ragged_read_tokens(const kivi_cache* cache, const void* state, long long t0, long long T,
+                            void* K, void* V, void* stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (!state || ((uintptr_t)state & 15)) return KIVI_ERR_ARG;
+  if (!is_ragged(cache)) return KIVI_ERR_STATE;
+  const long long n = cache->dims.capacity;
+  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V))) return KIVI_ERR_ARG;
+  return read_tokens(cache, state, t0, T, K, V, stream);
+}
+
+int kivi_qk_norm_rope(const kivi_rope* p, const void* qkv, long long stride,
+                      const int64_t* positions, const double* inv_freq, const void* q_weight,
+                      const void* k_weight, void* q, void* k, void* v, void* stream) {
+  if (!p || !qkv || !positions || !inv_freq || !q || !k || !v) return KIVI_ERR_ARG;
+  if (p->B < 1 || p->N < 1 || p->Hq < 1 || p->Hkv < 1 || p->axes < 1 || p->rot < 0 ||
+      !(p->eps >= 0.0f && p->eps <= 3.0e38f))
+    return KIVI_ERR_ARG;
+  if (p->D != 32 && p->D != 64 && p->D != 128) return KIVI_ERR_UNSUPPORTED;
+  if (p->dtype != KIVI_F16 && p->dtype != KIVI_F32) return KIVI_ERR_UNSUPPORTED;
+  if (p->axes > kivi::kRopeMaxAxes || p->rot < 16 || p->rot > p->D || p->rot % 16 != 0)
+    return KIVI_ERR_UNSUPPORTED;
+  const long long row = ((long long)p->Hq + 2LL * p->Hkv) * p->D;
+  const long long tokens = (long long)p->B * p->N;
+  // a block's rows are counted in 32 bits, and so are the blocks
+  if (row > (1LL << 24) || tokens > (long long)INT_MAX) return KIVI_ERR_UNSUPPORTED;
+  const size_t es = elem_bytes(p->dtype);
+  if (stride < row || stride % (long long)(16 / es) != 0) return KIVI_ERR_ARG;
+  const uintptr_t all = (uintptr_t)qkv | (uintptr_t)q | (uintptr_t)k | (uintptr_t)v;
+  if ((all & 15) || (((uintptr_t)positions | (uintptr_t)inv_freq) & 7) ||
+      (((uintptr_t)q_weight | (uintptr_t)k_weight) & (es - 1)))
+    return KIVI_ERR_ARG;
+  kivi::RopeArgs a;
+  int sum = 0;
+  for (int i = 0; i < kivi::kRopeMaxAxes; ++i) {
+    if (i < p->axes) {
+      if (p->sections[i] < 0 || p->sections[i] > p->rot / 2) return KIVI_ERR_ARG;
+      sum += p->sections[i];
+    }
+    a.section_end[i] = sum;
+  }
+  if (sum != p->rot / 2) return KIVI_ERR_ARG;
+  a.qkv = qkv;
+  a.stride = stride;
+  a.pos = (const long long*)positions;
+  a.inv_freq = inv_freq;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.B = p->B;
+  a.N = p->N;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.D = p->D;
+  a.rot = p->rot;
+  a.axes = p->axes;
+  a.interleaved = p->interleaved != 0;
+  a.dtype = p->dtype;
+  a.eps = p->eps;
+  touch_noalloc_scratch();
+  return kivi::launch_rope(a, (cudaStream_t)stream) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -28,6 +28,7 @@
 // even) and the codes are chosen against the rounded pair, so that the
 // stored scale and zero reproduce them as closely as the code grid allows.
 #include "kivi_internal.cuh"
+#include "kivi_draft.cuh"
 #include "kivi_quantize_tile.cuh"
 
 namespace kivi {
@@ -650,6 +651,181 @@ __global__ void advance_ragged_kernel(DevState* st, long long B, long long Tq, i
   }
 }
 
+// ---- commit of accepted paths (ragged batches) ----------------------------
+// The fill of a sequence before and after it takes `cnt` tokens, one flush at
+// most (cnt <= R).  ok = false: nothing may be written (counters that are no
+// valid fill, a count outside [0, P], no room, a page outside the pool).  The
+// path's indices are checked apart (path_ok).
+struct CommitSpan {
+  long long n_q;  // before
+  int r;          // before
+  int cnt;
+  bool flush;
+  bool ok;
+};
+__device__ __forceinline__ CommitSpan commit_span(const CacheView& c, const DevState& s, int cnt,
+                                                  int P, long long b) {
+  CommitSpan o;
+  const SeqLen L = seq_len(s, false, c.Tq, c.R);
+  o.n_q = L.n_q;
+  o.r = L.r;
+  o.cnt = cnt;
+  o.ok = L.ok && cnt >= 0 && cnt <= P && L.n_q + L.r + cnt <= c.Tq + c.R;
+  o.flush = o.ok && L.r + cnt > c.R;
+  if (o.flush && c.bt != nullptr) {
+    const long long lp = L.n_q / c.R;
+    const long long pg = lp < c.pps ? c.bt[b * c.pps + lp] : -1;
+    o.ok = pg >= 0 && pg < c.n_pages;
+  }
+  return o;
+}
+
+// Copies row `i` of the path into a row of D elements, by the block's threads
+// (blockDim.x == D).
+template <int D, typename T>
+__device__ __forceinline__ void commit_rows(T* kr, T* vr, const T* __restrict__ k,
+                                            const T* __restrict__ v, const int* __restrict__ path,
+                                            int slot0, int i0, int n) {
+  const int d = threadIdx.x;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const long long node = path[i0 + j];
+    kr[(long long)(slot0 + j) * D + d] = k[node * D + d];
+    vr[(long long)(slot0 + j) * D + d] = v[node * D + d];
+  }
+}
+
+// Grid (R / 32, units), D threads: sequence b takes tokens path[b][0 .. cnt)
+// of k, v [B][Hkv][N][D] as that many appends would.  Block x owns window
+// slots 32x .. 32x+31: it writes the accepted tokens that fall into them, and
+// when the window overflows it first quantizes those 32 slots (old and new
+// tokens) into the store and then writes the tokens that follow the flush.
+// No slot is touched by two blocks, so no barrier is needed between them.  The
+// counters are only read; advance_commit_kernel moves them afterwards.
+template <int D, int BITS, typename T, typename M, bool STAGED>
+__global__ void __launch_bounds__(D, STAGED ? 8 : 1)
+    commit_kernel(CacheView c, const T* __restrict__ k, const T* __restrict__ v,
+                  const int* __restrict__ path, const int* __restrict__ count, int N, int P,
+                  const DevState* st, int Hkv) {
+  extern __shared__ __align__(16) unsigned char dsm[];
+  const long long unit = blockIdx.y, b = unit / Hkv;
+  const int* pb = path + b * P;
+  const CommitSpan sp = commit_span(c, st[b], count[b], P, b);
+  if (!sp.ok || sp.cnt == 0) return;
+  int bad = 0;
+  for (int i = threadIdx.x; i < sp.cnt; i += D) bad |= pb[i] < 0 || pb[i] >= N;
+  if (__syncthreads_or(bad)) return;
+  const int lo = blockIdx.x * kTile, hi = lo + kTile;  // the block's slots
+  T* kr = reinterpret_cast<T*>(c.k_res) + unit * c.R * D;
+  T* vr = reinterpret_cast<T*>(c.v_res) + unit * c.R * D;
+  const T* ku = k + unit * N * D;
+  const T* vu = v + unit * N * D;
+  // slots r .. r+cnt-1 before the flush, as far as they are this block's
+  const int a0 = max(lo, sp.r), a1 = min(hi, min(sp.r + sp.cnt, c.R));
+  if (a0 < a1) commit_rows<D, T>(kr, vr, ku, vu, pb, a0, a0 - sp.r, a1 - a0);
+  if (!sp.flush) return;
+  // the 32 slots from shared memory: old ones from the window, new ones from k, v
+  T* Ks = reinterpret_cast<T*>(dsm);
+  T* Vs = Ks + kTile * D;
+#pragma unroll 8
+  for (int t = 0; t < kTile; ++t) {
+    const int d = threadIdx.x, s = lo + t;
+    const int at = STAGED ? stage_idx<D, T>(t, d) : t * D + d;
+    if (s < sp.r) {
+      Ks[at] = kr[(long long)s * D + d];
+      Vs[at] = vr[(long long)s * D + d];
+    } else {
+      const long long node = pb[s - sp.r];
+      Ks[at] = ku[node * D + d];
+      Vs[at] = vu[node * D + d];
+    }
+  }
+  if constexpr (STAGED) {
+    using SM = StagedSmem<D, T>;
+    int* vbad = reinterpret_cast<int*>(dsm + SM::O_BAD);
+    if (threadIdx.x < D / kGv) vbad[threadIdx.x] = 0;
+    __syncthreads();
+    quantize_tile_staged<D, BITS, T, M>(c, unit, sp.n_q + lo, Ks, Vs, dsm + SM::O_CK,
+                                        reinterpret_cast<float4*>(dsm + SM::O_VZ),
+                                        reinterpret_cast<float2*>(dsm + SM::O_VS), vbad);
+  } else {
+    __syncthreads();
+    uint8_t* ck = dsm + 2 * kTile * D * sizeof(T);
+    quantize_tile<D, BITS, T, M, 0, true>(c, unit, Ks, Vs, sp.n_q + lo, ck, ck + kTile * D);
+  }
+  // what follows the flush starts the window anew (a block's threads write
+  // other elements of a slot than they read above: the tile is in shared
+  // memory by now, behind a barrier)
+  const int f0 = lo, f1 = min(hi, sp.r + sp.cnt - c.R);
+  if (f0 < f1) commit_rows<D, T>(kr, vr, ku, vu, pb, f0, c.R - sp.r + f0, f1 - f0);
+}
+
+// After commit_kernel: advance every sequence that took its path; one that
+// could not gets status 1.
+__global__ void advance_commit_kernel(CacheView c, const int* __restrict__ path,
+                                      const int* __restrict__ count, int N, int P, DevState* st,
+                                      long long B) {
+  for (long long b = blockIdx.x * (long long)blockDim.x + threadIdx.x; b < B;
+       b += (long long)gridDim.x * blockDim.x) {
+    const CommitSpan sp = commit_span(c, st[b], count[b], P, b);
+    bool ok = sp.ok;
+    if (ok)
+      for (int i = 0; i < sp.cnt; ++i) {
+        const int node = path[b * P + i];
+        ok = ok && node >= 0 && node < N;
+      }
+    if (!ok) {
+      st[b].status = 1;
+    } else {
+      st[b].n_q = sp.flush ? sp.n_q + c.R : sp.n_q;
+      st[b].r = sp.r + sp.cnt - (sp.flush ? c.R : 0);
+    }
+  }
+}
+
+template <int D, int BITS, typename T, typename M>
+cudaError_t commit_t(const CacheView& c, int units, int Hkv, const void* k, const void* v,
+                     const int* path, const int* count, int N, int P, DevState* st,
+                     cudaStream_t s) {
+  const dim3 grid((unsigned)(c.R / kTile), (unsigned)units);
+  if (c.k_out == 0 && c.v_out == 0)
+    commit_kernel<D, BITS, T, M, true><<<grid, D, StagedSmem<D, T>::BYTES, s>>>(
+        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv);
+  else
+    commit_kernel<D, BITS, T, M, false><<<grid, D, 2 * kTile * D * (sizeof(T) + 1), s>>>(
+        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int B = units / Hkv;
+  advance_commit_kernel<<<(B + 127) / 128, 128, 0, s>>>(c, path, count, N, P, st, B);
+  return cudaGetLastError();
+}
+
+template <int BITS, typename T, typename M>
+cudaError_t commit_d(int D, const CacheView& c, int units, int Hkv, const void* k, const void* v,
+                     const int* path, const int* count, int N, int P, DevState* st,
+                     cudaStream_t s) {
+  switch (D) {
+    case 32: return commit_t<32, BITS, T, M>(c, units, Hkv, k, v, path, count, N, P, st, s);
+    case 64: return commit_t<64, BITS, T, M>(c, units, Hkv, k, v, path, count, N, P, st, s);
+    case 128: return commit_t<128, BITS, T, M>(c, units, Hkv, k, v, path, count, N, P, st, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T, typename M>
+cudaError_t commit_b(int bits, int D, const CacheView& c, int units, int Hkv, const void* k,
+                     const void* v, const int* path, const int* count, int N, int P,
+                     DevState* st, cudaStream_t s) {
+  switch (bits) {
+    case 1: return commit_d<1, T, M>(D, c, units, Hkv, k, v, path, count, N, P, st, s);
+    case 2: return commit_d<2, T, M>(D, c, units, Hkv, k, v, path, count, N, P, st, s);
+    case 3: return commit_d<3, T, M>(D, c, units, Hkv, k, v, path, count, N, P, st, s);
+    case 4: return commit_d<4, T, M>(D, c, units, Hkv, k, v, path, count, N, P, st, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 // lens != null: ragged prefill over T_len padded tokens per unit
 template <int D, int BITS, typename T, typename M>
 cudaError_t prefill_t(const CacheView& c, int units, const void* K, const void* V,
@@ -789,6 +965,17 @@ cudaError_t launch_advance_ragged(DevState* st, long long B, long long Tq, int R
   const long long blocks = (B + 255) / 256;
   advance_ragged_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(st, B, Tq, R);
   return cudaGetLastError();
+}
+
+cudaError_t launch_commit(const CacheView& c, int B, int Hkv, int D, int bits, int dtype,
+                          const void* k, const void* v, const int* path, const int* count, int N,
+                          int P, DevState* st, cudaStream_t s) {
+  const int units = B * Hkv;
+  if (dtype == 1)
+    return commit_b<float, float>(bits, D, c, units, Hkv, k, v, path, count, N, P, st, s);
+  if (c.meta == 1)
+    return commit_b<__half, __half>(bits, D, c, units, Hkv, k, v, path, count, N, P, st, s);
+  return commit_b<__half, float>(bits, D, c, units, Hkv, k, v, path, count, N, P, st, s);
 }
 
 cudaError_t launch_set_state(DevState* st, long long n_q, int r, cudaStream_t s) {

@@ -1,0 +1,352 @@
+// kivi_tree_simt.cu -- attention of drafted tokens over the cache on CUDA
+// cores, everything in binary32.
+//
+// For row (query head, node i) of a KV head, over the cache's tokens t and
+// the drafted tokens j whose bit is set in the node's mask:
+//   s = softmax_scale * <q, K^>,  out = sum exp(s - max) V^ / sum exp(s - max).
+// One pass, tile by tile: running maximum and sum of each row, accumulators
+// rescaled when the maximum rises.  A tile of 32 tokens is turned into
+// numbers in shared memory once for all rows of the block; scores and
+// accumulators are register tiles of a matrix product.
+#include <type_traits>
+
+#include "kivi_dequant.cuh"
+#include "kivi_tree.cuh"
+
+namespace kivi {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kTT = 32;  // = one key group
+
+template <int D, int RB>
+struct SimtSmem {
+  static constexpr int LD = D + 4;  // row stride of K: 8 rows on different banks
+  static constexpr int Q = 0;
+  static constexpr int K = Q + RB * D;
+  static constexpr int V = K + kTT * LD;
+  static constexpr int P = V + kTT * D;         // [token][row]
+  static constexpr int PL = RB + 4;
+  static constexpr int SCL = P + kTT * PL;
+  static constexpr int FLOATS = SCL + RB;
+};
+
+template <int D, int BITS, typename T, typename M, int RB>
+__global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePlan p) {
+  using SM = SimtSmem<D, RB>;
+  constexpr int TCN = RB == 64 ? 8 : 16;         // column groups of the scores
+  constexpr int SR = RB / (kThreads / TCN), SC = kTT / TCN;
+  constexpr int PCN = RB == 64 ? 16 : 32;        // column groups of the accumulators
+  constexpr int OR = RB / (kThreads / PCN), OC = D / PCN;
+  constexpr int OV = OC >= 4 ? 4 : OC;           // adjacent channels of a thread
+  constexpr int ON = OC / OV;
+  static_assert(kTT == kTile && kTT == kG, "a tile is a key group");
+  extern __shared__ __align__(16) float sm[];
+  __shared__ TreeAt s_at;
+  const int tid = threadIdx.x;
+  const long long W0 = blockIdx.x;
+  if (tid < 32) {
+    TreeAt at = tree_find(a, p, 0);
+    const long long W = tree_range(p, at.total);
+    const long long total = at.total;
+    at = tree_find(a, p, W0 * W);
+    at.total = total;
+    if (tid == 0) s_at = at;
+  }
+  __syncthreads();
+  const long long total = s_at.total, W = tree_range(p, total);
+  long long x = W0 * W;
+  const long long end = x + W < total ? x + W : total;
+  if (x >= end) return;
+  long long b = s_at.b, rem = s_at.rem;
+  const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
+  const float kInf = __builtin_huge_valf();
+
+  while (x < end) {
+    const TreeSeq q = tree_seq(a, p, b);
+    const long long gpb = (long long)a.Hkv * p.n_rb;
+    if (rem >= gpb * q.ut) {  // next sequence
+      rem -= gpb * q.ut;
+      ++b;
+      continue;
+    }
+    const long long grp = rem / q.ut, tile0 = rem % q.ut;
+    const long long left = end - x;
+    const long long nt = q.ut - tile0 < left ? q.ut - tile0 : left;
+    const int h = (int)(grp / p.n_rb), row0 = (int)(grp % p.n_rb) * RB;
+    const long long unit = b * a.Hkv + h;
+    const long long tq = (q.n_q + kTT - 1) / kTT, tw = (q.r + kTT - 1) / kTT;
+
+    __syncthreads();  // the segment before has read its last tile
+    const T* qp = static_cast<const T*>(a.q) + (unit * rows + row0) * D;
+    for (int i = tid; i < RB * D; i += kThreads)
+      sm[SM::Q + i] = row0 + i / D < rows ? to_f32(qp[i]) * a.qscale : 0.f;
+
+    float m[SR], l[SR], acc[OR][OC];
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+      m[i] = -kInf;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < OR; ++i)
+#pragma unroll
+      for (int j = 0; j < OC; ++j) acc[i][j] = 0.f;
+    bool poison = !q.ok;
+    const int sr0 = tid / TCN * SR, sc0 = tid % TCN;
+    const int or0 = tid / PCN * OR, oc0 = tid % PCN * OV;
+
+    for (long long t = tile0; t < tile0 + nt && !poison; ++t) {
+      const int kind = t < tq ? 0 : (t < tq + tw ? 1 : 2);
+      // ---- the tile as numbers
+      constexpr int COLS = D / 4, TPT = kTT / (kThreads / COLS);  // tokens of a thread
+      const int ch = tid % COLS * 4, tk = tid / COLS * TPT;
+      __syncthreads();  // the tile before is read
+      if (kind == 0) {
+        long long su, stl;
+        if (!store_tile(a.c, unit, t, &su, &stl)) {
+          poison = true;  // the same for the whole block
+          break;
+        }
+        float s[4], z[4];
+        key_meta<D, BITS, M, 4>(a.c, su, stl * kTT, ch, s, z);
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+          float v[4];
+          key_values<D, BITS, M, 4>(a.c, su, stl * kTT + tk + i, ch, s, z, v);
+          *reinterpret_cast<float4*>(sm + SM::K + (tk + i) * SM::LD + ch) =
+              make_float4(v[0], v[1], v[2], v[3]);
+          value_values<D, BITS, M, 4>(a.c, su, stl * kTT + tk + i, ch, v);
+          *reinterpret_cast<float4*>(sm + SM::V + (tk + i) * D + ch) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        }
+      } else {
+        const long long first = (t - (kind == 1 ? tq : tq + tw)) * kTT;
+        const int n = kind == 1 ? q.r : a.N;
+        const T* kp = kind == 1 ? static_cast<const T*>(a.c.k_res) + unit * a.c.R * D
+                                : static_cast<const T*>(a.k) + unit * a.N * D;
+        const T* vp = kind == 1 ? static_cast<const T*>(a.c.v_res) + unit * a.c.R * D
+                                : static_cast<const T*>(a.v) + unit * a.N * D;
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+          const long long tok = first + tk + i;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool in = tok < n;
+            sm[SM::K + (tk + i) * SM::LD + ch + e] = in ? to_f32(kp[tok * D + ch + e]) : 0.f;
+            sm[SM::V + (tk + i) * D + ch + e] = in ? to_f32(vp[tok * D + ch + e]) : 0.f;
+          }
+        }
+      }
+      __syncthreads();
+      // ---- scores
+      float sc[SR][SC];
+#pragma unroll
+      for (int i = 0; i < SR; ++i)
+#pragma unroll
+        for (int j = 0; j < SC; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 qv[SR], kv[SC];
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+          qv[i] = *reinterpret_cast<const float4*>(sm + SM::Q + (sr0 + i) * D + d);
+#pragma unroll
+        for (int j = 0; j < SC; ++j)
+          kv[j] = *reinterpret_cast<const float4*>(sm + SM::K + (sc0 + j * TCN) * SM::LD + d);
+#pragma unroll
+        for (int i = 0; i < SR; ++i)
+#pragma unroll
+          for (int j = 0; j < SC; ++j) {
+            sc[i][j] = fmaf(qv[i].x, kv[j].x, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].y, kv[j].y, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].z, kv[j].z, sc[i][j]);
+            sc[i][j] = fmaf(qv[i].w, kv[j].w, sc[i][j]);
+          }
+      }
+      // ---- masks: window slots from r on, drafted tokens that a node does not see
+      if (kind != 0) {
+        const long long first = (t - (kind == 1 ? tq : tq + tw)) * kTT;
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+          uint32_t sees = 0xffffffffu;
+          const int row = row0 + sr0 + i;
+          if (kind == 2)
+            sees = row < rows ? a.mask[(b * a.N + row % a.N) * mw + first / 32] : 0u;
+#pragma unroll
+          for (int j = 0; j < SC; ++j) {
+            const int tl = sc0 + j * TCN;
+            const bool in = kind == 1 ? first + tl < q.r
+                                      : first + tl < a.N && ((sees >> tl) & 1u);
+            if (!in) sc[i][j] = -kInf;
+          }
+        }
+      }
+      // ---- running maximum and sum (the TCN threads of a row are neighbours)
+#pragma unroll
+      for (int i = 0; i < SR; ++i) {
+        float mx = sc[i][0];
+#pragma unroll
+        for (int j = 1; j < SC; ++j) mx = fmaxf(mx, sc[i][j]);
+#pragma unroll
+        for (int o = 1; o < TCN; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[i], mx);
+        const float base = mn == -kInf ? 0.f : mn;  // nothing seen so far
+        const float f = exp2f(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < SC; ++j) {
+          const float e = exp2f(sc[i][j] - base);
+          sm[SM::P + (sc0 + j * TCN) * SM::PL + sr0 + i] = e;
+          sum += e;
+        }
+#pragma unroll
+        for (int o = 1; o < TCN; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+        if (sc0 == 0) sm[SM::SCL + sr0 + i] = f;
+      }
+      __syncthreads();
+      // ---- accumulators
+#pragma unroll
+      for (int i = 0; i < OR; ++i) {
+        const float f = sm[SM::SCL + or0 + i];
+#pragma unroll
+        for (int j = 0; j < OC; ++j) acc[i][j] *= f;
+      }
+      auto add = [&](auto guard) {
+#pragma unroll 4
+        for (int tk2 = 0; tk2 < kTT; ++tk2) {
+          float pv[OR], vv[OC];
+#pragma unroll
+          for (int i = 0; i < OR; i += 4)
+            *reinterpret_cast<float4*>(pv + i) =
+                *reinterpret_cast<const float4*>(sm + SM::P + tk2 * SM::PL + or0 + i);
+#pragma unroll
+          for (int g = 0; g < ON; ++g)
+#pragma unroll
+            for (int e = 0; e < OV; ++e)
+              vv[g * OV + e] = sm[SM::V + tk2 * D + g * (D / ON) + oc0 + e];
+#pragma unroll
+          for (int i = 0; i < OR; ++i)
+#pragma unroll
+            for (int j = 0; j < OC; ++j) {
+              // a drafted token that the node does not see has weight 0 whatever
+              // its values are: 0 * inf must not reach the sum
+              if (decltype(guard)::value && pv[i] == 0.f) continue;
+              acc[i][j] = fmaf(pv[i], vv[j], acc[i][j]);
+            }
+        }
+      };
+      if (kind == 2)
+        add(std::true_type{});
+      else
+        add(std::false_type{});
+    }
+
+    // ---- the segment's end
+    const bool whole = tile0 == 0 && nt == q.ut;
+    if (poison) {  // refused sequence, or a page outside the pool
+#pragma unroll
+      for (int i = 0; i < SR; ++i) {
+        l[i] = kNaN;
+        m[i] = 0.f;
+      }
+    }
+    __syncthreads();
+    if (sc0 == 0) {
+#pragma unroll
+      for (int i = 0; i < SR; ++i) {
+        sm[SM::P + 2 * (sr0 + i)] = m[i];
+        sm[SM::P + 2 * (sr0 + i) + 1] = l[i];
+      }
+    }
+    __syncthreads();
+    if (whole) {
+      T* op = static_cast<T*>(a.out) + (unit * rows + row0) * D;
+#pragma unroll
+      for (int i = 0; i < OR; ++i) {
+        if (row0 + or0 + i >= rows) continue;
+        const float lr = sm[SM::P + 2 * (or0 + i) + 1];
+        const float inv = 1.f / lr;
+#pragma unroll
+        for (int g = 0; g < ON; ++g)
+#pragma unroll
+          for (int e = 0; e < OV; ++e)
+            op[(or0 + i) * D + g * (D / ON) + oc0 + e] =
+                from_f32<T>(lr == 0.f ? 0.f : acc[i][g * OV + e] * inv);
+      }
+    } else {
+      float* pp = a.part + (2 * W0 + (tile0 == 0)) * tree_part(p, D);
+      for (int i = tid; i < 2 * RB; i += kThreads) pp[i] = sm[SM::P + i];
+#pragma unroll
+      for (int i = 0; i < OR; ++i)
+#pragma unroll
+        for (int g = 0; g < ON; ++g)
+#pragma unroll
+          for (int e = 0; e < OV; ++e)
+            pp[2 * RB + (or0 + i) * D + g * (D / ON) + oc0 + e] = acc[i][g * OV + e];
+    }
+    x += nt;
+    rem += nt;
+  }
+}
+
+template <int D, int BITS, typename T, typename M, int RB>
+cudaError_t tree_r(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  constexpr int bytes = SimtSmem<D, RB>::FLOATS * 4;
+  const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D, BITS, T, M, RB>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  tree_simt_kernel<D, BITS, T, M, RB><<<p.ctas, kThreads, bytes, s>>>(a, p);
+  return cudaGetLastError();
+}
+template <int D, int BITS, typename T, typename M>
+cudaError_t tree_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  return p.rb == 16 ? tree_r<D, BITS, T, M, 16>(a, p, s) : tree_r<D, BITS, T, M, 64>(a, p, s);
+}
+template <int BITS, typename T, typename M>
+cudaError_t tree_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  switch (a.D) {
+    case 32: return tree_t<32, BITS, T, M>(a, p, s);
+    case 64: return tree_t<64, BITS, T, M>(a, p, s);
+    case 128: return tree_t<128, BITS, T, M>(a, p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+template <typename T, typename M>
+cudaError_t tree_b(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  switch (a.bits) {
+    case 1: return tree_d<1, T, M>(a, p, s);
+    case 2: return tree_d<2, T, M>(a, p, s);
+    case 3: return tree_d<3, T, M>(a, p, s);
+    case 4: return tree_d<4, T, M>(a, p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+TreePlan tree_plan_simt(int gq, int N, int sms) {
+  TreePlan p;
+  p.rb = gq * N <= 16 ? 16 : 64;
+  p.tt = kTT;
+  p.n_rb = (gq * N + p.rb - 1) / p.rb;
+  p.ctas = sms * (p.rb == 16 ? 4 : 2);
+  p.min_w = 4;
+  return p;
+}
+
+cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t s) {
+  const TreePlan p = tree_plan_simt(a.gq, a.N, a.sms);
+  cudaError_t e;
+  if (a.dtype == 1)
+    e = tree_b<float, float>(a, p, s);
+  else if (a.c.meta == 1)
+    e = tree_b<__half, __half>(a, p, s);
+  else
+    e = tree_b<__half, float>(a, p, s);
+  return e == cudaSuccess ? launch_tree_merge(a, p, s) : e;
+}
+
+}  // namespace kivi

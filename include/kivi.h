@@ -474,6 +474,138 @@ KIVI_API int kivi_cache_set_outliers(kivi_cache *cache, void *const buffers[4]);
 KIVI_API int kivi_decode_attention_noalloc(const kivi_cache *cache, const void *q, int Hq,
                                            float softmax_scale, void *out, void *stream);
 
+/* ---- drafted tokens (speculative decoding) --------------------------------
+ * A draft model proposes N tokens a sequence, a tree of continuations; one
+ * pass of the large model checks them all, and the path that it accepts joins
+ * the cache.  The calls below are that step's: kivi_qk_norm_rope (the
+ * projections made ready), kivi_tree_decode / kivi_ragged_tree_decode (the
+ * attention), kivi_ragged_tree_commit (the accepted path into the cache), and
+ * kivi_read_tokens / kivi_ragged_read_tokens (the cache's tokens as numbers).
+ * No counterpart on the pages, which decode one token at a time; the cache
+ * they read and write is the pages'. */
+
+/* Bytes of device workspace the two tree calls need for N nodes and Hq query
+ * heads at any fill of this cache (0 on error).  Host arithmetic only.  The
+ * workspace needs no initialization, is scratch between calls, and may serve
+ * calls and captured graphs in any order, one at a time. */
+KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq);
+
+/* Attention of N drafted tokens (nodes) of every sequence over the cache and
+ * over each other.  Node i of sequence b attends to all n_q + r tokens of the
+ * cache and to the nodes j whose bit is set in its mask:
+ *   out[b][h][i] = sum_t p_t Vhat_t / sum_t p_t over those tokens,
+ *   p_t = exp(softmax_scale * <q[b][h][i], Khat_t> - max),
+ * Khat, Vhat and the heads as for kivi_decode_attention.
+ * q, out: device, dims.dtype, [B][Hq][N][D].  k, v: device, dims.dtype,
+ * [B][Hkv][N][D], the nodes' own keys and values, which are not in the cache.
+ * mask: device, uint32 [B][N][ceil(N / 32)], node j in bit j % 32 of word
+ * j / 32; any set is taken (a tree's is the node and its ancestors; a node
+ * may leave itself out).  Bits from N on are ignored.  A token that a node
+ * does not attend to has no part in its result, even where its key or value
+ * is infinite or NaN; a node that attends to nothing (an empty cache and an
+ * empty mask) gets 0.  The cache may be empty.  It is only read: see
+ * kivi_ragged_tree_commit.
+ * Any element alignment of q, k, v and out is accepted.  Two launches,
+ * capturable in a CUDA graph.
+ * Sums, the softmax and its statistics are binary32 for both dtypes; with
+ * fp16 inputs the stored codes' products and the weights p_t pass through
+ * binary16 matrix operands as the kernel's comments say.
+ * Errors: KIVI_ERR_ARG (null or misaligned pointer, N < 1, Hq not a multiple
+ * of Hkv), KIVI_ERR_UNSUPPORTED (N > 256, Hq/Hkv > 64, a dense-and-sparse
+ * cache), KIVI_ERR_STATE (a ragged or paged cache),
+ * KIVI_ERR_WORKSPACE, KIVI_ERR_CUDA. */
+KIVI_API int kivi_tree_decode(const kivi_cache *cache, const void *q, const void *k,
+                              const void *v, const uint32_t *mask, int N, int Hq,
+                              float softmax_scale, void *out, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* The same for a cache filled by kivi_ragged_prefill (contiguous or paged):
+ * every sequence over its own tokens, as `state` has them on the device.  A
+ * sequence with a status, with counters that are no valid fill, or with a
+ * page id outside the pool where it has tokens, gets NaN.
+ * Errors: as kivi_tree_decode; KIVI_ERR_STATE where the cache is not ragged. */
+KIVI_API int kivi_ragged_tree_decode(const kivi_cache *cache, const void *state, const void *q,
+                                     const void *k, const void *v, const uint32_t *mask, int N,
+                                     int Hq, float softmax_scale, void *out, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* Commit of accepted paths: sequence b appends its nodes path[b][0],
+ * path[b][1], .. path[b][count[b] - 1], in this order, with the result (store,
+ * window, counters) of that many kivi_ragged_append calls for it alone,
+ * including the flush of a window that fills up.  k, v: as for the tree calls,
+ * [B][Hkv][N][D].  path: device, int32 [B][P]; entries from count[b] on are
+ * not read.  count: device, int32 [B]; 0 leaves the sequence as it is.  A node
+ * may stand in a path more than once.  P <= R, so at most one flush is due.
+ * A sequence gets status 1 and takes nothing where its count lies outside
+ * [0, P], a node outside [0, N), its tokens find no room, the page that its
+ * flush fills is not in the pool, or its counters are no valid fill.
+ * Two launches (the tokens, then the counters), capturable in a CUDA graph.
+ * Errors: KIVI_ERR_ARG (null or misaligned pointer, N < 1, P outside [1, R]),
+ * KIVI_ERR_UNSUPPORTED (N > 256), KIVI_ERR_STATE (the cache is not ragged),
+ * KIVI_ERR_CUDA. */
+KIVI_API int kivi_ragged_tree_commit(const kivi_cache *cache, void *state, const void *k,
+                                     const void *v, int N, const int32_t *path,
+                                     const int32_t *count, int P, void *stream);
+
+/* Read-back: tokens t0 .. t0+T-1 of every sequence as numbers.  K, V: device,
+ * dims.dtype, [B][Hkv][T][D].  A quantized token is c * s + z (kept entries of
+ * a dense-and-sparse cache: their value), computed in binary32 by one fused
+ * multiply-add and rounded to dims.dtype; a window token is its stored value.
+ * Any element alignment of K and V is accepted.  T = 0 does nothing.
+ * Errors: KIVI_ERR_ARG (null pointer, a range that is not within the
+ * n_q + r tokens), KIVI_ERR_STATE (a ragged or paged cache), KIVI_ERR_CUDA. */
+KIVI_API int kivi_read_tokens(const kivi_cache *cache, long long t0, long long T, void *K,
+                              void *V, void *stream);
+
+/* The same for a cache filled by kivi_ragged_prefill.  The range lies within
+ * [0, capacity); tokens that a sequence does not have (all of them for one
+ * with a status), and those on a page outside the pool, are left as they were
+ * in K and V.
+ * Errors: as kivi_read_tokens; KIVI_ERR_STATE where the cache is not ragged. */
+KIVI_API int kivi_ragged_read_tokens(const kivi_cache *cache, const void *state, long long t0,
+                                     long long T, void *K, void *V, void *stream);
+
+/* Shape and rotary positions of kivi_qk_norm_rope. */
+typedef struct {
+  int B;            /* sequences */
+  int N;            /* tokens of each */
+  int Hq;           /* query heads */
+  int Hkv;          /* key/value heads */
+  int D;            /* head dimension: 32, 64 or 128 */
+  int dtype;        /* kivi_dtype of qkv, the weights, q, k and v */
+  int rot;          /* channels that turn: a multiple of 16 up to D */
+  int axes;         /* position axes, 1 to 4 */
+  int sections[4];  /* pairs that turn by each axis, in order; sum = rot / 2 */
+  int interleaved;  /* pairs: 0 (i, i + rot/2), else (2i, 2i + 1) */
+  float eps;        /* of the norm */
+} kivi_rope;
+
+/* A step's projections made ready for the cache and its attention: each head
+ * of queries and keys normed and turned by its token's positions, and all
+ * heads laid out by head, in one pass.
+ * qkv: device, [B][N] rows of (Hq + 2 Hkv) * D channels (queries, keys, values),
+ * `stride` elements apart.  For a head x of q or k, in binary32, rounded once
+ * at the end:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (weight NULL: y = x),
+ *   pair i (channels as `interleaved` says), a = positions[axis][b][n] * inv_freq[i]:
+ *   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a);
+ * pairs 0 .. sections[0]-1 turn by axis 0, the next sections[1] by axis 1, and
+ * so on; channels from rot on are only normed.  Values are copied.
+ * positions: device, int64 [axes][B][N].  inv_freq: device, binary64 [rot/2],
+ * radians per position (the angle a is formed and reduced in binary64, so far
+ * positions keep their angles, to about |a| 2^-51).  q_weight, k_weight: device [D] or NULL.
+ * q: device, [B][Hq][N][D]; k, v: device, [B][Hkv][N][D] -- what the tree
+ * calls and kivi_quantize_prefill take, and with N = 1 what the decode calls
+ * take.  One launch.
+ * Errors: KIVI_ERR_ARG (null pointer; qkv, q, k or v not 16-byte aligned;
+ * stride below a row or no multiple of 16 bytes; sizes below 1; sections that
+ * do not sum to rot / 2; eps negative), KIVI_ERR_UNSUPPORTED (D, rot, axes,
+ * dtype), KIVI_ERR_CUDA. */
+KIVI_API int kivi_qk_norm_rope(const kivi_rope *p, const void *qkv, long long stride,
+                               const int64_t *positions, const double *inv_freq,
+                               const void *q_weight, const void *k_weight, void *q, void *k,
+                               void *v, void *stream);
+
 /* Human-readable name of a kivi_status. */
 KIVI_API const char *kivi_status_string(int status);
 
