@@ -357,7 +357,7 @@ int tree_decode(const kivi_cache* c, const void* state, const void* q, const voi
   const int sms = device_sms();
   if (sms <= 0) return KIVI_ERR_CUDA;
   const size_t need =
-      kivi::tree_workspace_bytes(c->dims.B, c->dims.Hkv, gq, c->dims.D, c->dims.dtype, N, sms);
+      kivi::tree_workspace_bytes(gq, c->dims.D, c->dims.dtype, N, sms);
   if (!workspace || ((uintptr_t)workspace & 15) || ws_bytes < need) return KIVI_ERR_WORKSPACE;
   touch_noalloc_scratch();
   kivi::TreeArgs a;
@@ -843,8 +843,7 @@ size_t kivi_tree_workspace_bytes(const kivi_cache* cache, int N, int Hq) {
     return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  return kivi::tree_workspace_bytes(cache->dims.B, cache->dims.Hkv, Hq / cache->dims.Hkv,
-                                    cache->dims.D, cache->dims.dtype, N, sms);
+  return kivi::tree_workspace_bytes(Hq / cache->dims.Hkv, cache->dims.D, cache->dims.dtype, N, sms);
 }
 
 int kivi_tree_decode(const kivi_cache* cache, const void* q, const void* k, const void* v,

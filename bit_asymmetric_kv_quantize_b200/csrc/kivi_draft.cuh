@@ -23,7 +23,7 @@ struct TreeArgs {
   float qscale;          // softmax_scale * log2(e)
   int sms;
 };
-size_t tree_workspace_bytes(int B, int Hkv, int gq, int D, int dtype, int N, int sms);
+size_t tree_workspace_bytes(int gq, int D, int dtype, int N, int sms);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 
 // ---- read-back ------------------------------------------------------------

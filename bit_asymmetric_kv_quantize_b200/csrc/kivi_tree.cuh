@@ -52,7 +52,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, const TreePlan& p
     o.ok = true;
   }
   // a refused sequence keeps one tile, which writes its NaNs
-  o.ut = o.ok ? (o.n_q + p.tt - 1) / p.tt + (o.r + p.tt - 1) / p.tt + (a.N + p.tt - 1) / p.tt : 1;
+  o.ut = o.ok ? (o.n_q + p.tt - 1) / p.tt + (o.r + a.N + p.tt - 1) / p.tt : 1;
   return o;
 }
 
@@ -103,8 +103,10 @@ __device__ __forceinline__ long long tree_range(const TreePlan& p, long long tot
   return w < p.min_w ? p.min_w : w;
 }
 
-cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t s);
-TreePlan tree_plan_simt(int gq, int N, int sms);
-cudaError_t launch_tree_merge(const TreeArgs& a, const TreePlan& p, cudaStream_t s);
+// The kernels: binary32 caches on CUDA cores, fp16 ones on the tensor cores
+// (binary32 or binary16 scales and zeros).
+cudaError_t tree_simt(const TreeArgs& a, const TreePlan& p, cudaStream_t s);
+cudaError_t tree_tc_f32(const TreeArgs& a, const TreePlan& p, cudaStream_t s);
+cudaError_t tree_tc_meta16(const TreeArgs& a, const TreePlan& p, cudaStream_t s);
 
 }  // namespace kivi

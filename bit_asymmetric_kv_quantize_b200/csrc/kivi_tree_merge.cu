@@ -95,15 +95,41 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_tree_merge(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  return a.dtype == 1 ? merge_d<float>(a, p, s) : merge_d<__half>(a, p, s);
+// The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all
+// fit.  Tensor cores: up to 128 rows a block, more in blocks of equal size, since
+// each block unpacks the cache again; one block of threads per SM.
+static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
+  const int rows = gq * N;
+  TreePlan p;
+  if (dtype == 1) {
+    p.rb = rows <= 16 ? 16 : 64;
+    p.n_rb = (rows + p.rb - 1) / p.rb;
+    p.tt = 32;
+    p.ctas = sms * (p.rb == 16 ? 4 : 2);
+    p.min_w = 4;
+  } else {
+    p.n_rb = (rows + 127) / 128;
+    p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;
+    p.n_rb = (rows + p.rb - 1) / p.rb;
+    p.tt = 128;
+    p.ctas = sms;
+    p.min_w = 1;
+  }
+  return p;
 }
 
-size_t tree_workspace_bytes(int B, int Hkv, int gq, int D, int dtype, int N, int sms) {
-  const TreePlan p = tree_plan_simt(gq, N, sms);
+size_t tree_workspace_bytes(int gq, int D, int dtype, int N, int sms) {
+  const TreePlan p = tree_plan(gq, N, dtype, sms);
   return (size_t)(tree_slots(p) * tree_part(p, D)) * sizeof(float);
 }
 
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) { return launch_tree_simt(a, s); }
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
+  const TreePlan p = tree_plan(a.gq, a.N, a.dtype, a.sms);
+  const cudaError_t e = a.dtype == 1    ? tree_simt(a, p, s)
+                        : a.meta == 1 ? tree_tc_meta16(a, p, s)
+                                      : tree_tc_f32(a, p, s);
+  if (e != cudaSuccess) return e;
+  return a.dtype == 1 ? merge_d<float>(a, p, s) : merge_d<__half>(a, p, s);
+}
 
 }  // namespace kivi

@@ -1,5 +1,5 @@
-// kivi_tree_simt.cu -- attention of drafted tokens over the cache on CUDA
-// cores, everything in binary32.
+// kivi_tree_simt.cu -- attention of drafted tokens over a binary32 cache on
+// CUDA cores, everything in binary32.
 //
 // For row (query head, node i) of a KV head, over the cache's tokens t and
 // the drafted tokens j whose bit is set in the node's mask:
@@ -31,7 +31,7 @@ struct SimtSmem {
   static constexpr int FLOATS = SCL + RB;
 };
 
-template <int D, int BITS, typename T, typename M, int RB>
+template <int D, int BITS, int RB>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePlan p) {
   using SM = SimtSmem<D, RB>;
   constexpr int TCN = RB == 64 ? 8 : 16;         // column groups of the scores
@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     const long long nt = q.ut - tile0 < left ? q.ut - tile0 : left;
     const int h = (int)(grp / p.n_rb), row0 = (int)(grp % p.n_rb) * RB;
     const long long unit = b * a.Hkv + h;
-    const long long tq = (q.n_q + kTT - 1) / kTT, tw = (q.r + kTT - 1) / kTT;
+    const long long tq = (q.n_q + kTT - 1) / kTT;
 
     __syncthreads();  // the segment before has read its last tile
-    const T* qp = static_cast<const T*>(a.q) + (unit * rows + row0) * D;
+    const float* qp = static_cast<const float*>(a.q) + (unit * rows + row0) * D;
     for (int i = tid; i < RB * D; i += kThreads)
-      sm[SM::Q + i] = row0 + i / D < rows ? to_f32(qp[i]) * a.qscale : 0.f;
+      sm[SM::Q + i] = row0 + i / D < rows ? qp[i] * a.qscale : 0.f;
 
     float m[SR], l[SR], acc[OR][OC];
 #pragma unroll
@@ -97,44 +97,47 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     const int or0 = tid / PCN * OR, oc0 = tid % PCN * OV;
 
     for (long long t = tile0; t < tile0 + nt && !poison; ++t) {
-      const int kind = t < tq ? 0 : (t < tq + tw ? 1 : 2);
+      const bool raw = t >= tq;  // window and drafted tokens, as they are
       // ---- the tile as numbers
       constexpr int COLS = D / 4, TPT = kTT / (kThreads / COLS);  // tokens of a thread
       const int ch = tid % COLS * 4, tk = tid / COLS * TPT;
       __syncthreads();  // the tile before is read
-      if (kind == 0) {
+      if (!raw) {
         long long su, stl;
         if (!store_tile(a.c, unit, t, &su, &stl)) {
           poison = true;  // the same for the whole block
           break;
         }
         float s[4], z[4];
-        key_meta<D, BITS, M, 4>(a.c, su, stl * kTT, ch, s, z);
+        key_meta<D, BITS, float, 4>(a.c, su, stl * kTT, ch, s, z);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
           float v[4];
-          key_values<D, BITS, M, 4>(a.c, su, stl * kTT + tk + i, ch, s, z, v);
+          key_values<D, BITS, float, 4>(a.c, su, stl * kTT + tk + i, ch, s, z, v);
           *reinterpret_cast<float4*>(sm + SM::K + (tk + i) * SM::LD + ch) =
               make_float4(v[0], v[1], v[2], v[3]);
-          value_values<D, BITS, M, 4>(a.c, su, stl * kTT + tk + i, ch, v);
+          value_values<D, BITS, float, 4>(a.c, su, stl * kTT + tk + i, ch, v);
           *reinterpret_cast<float4*>(sm + SM::V + (tk + i) * D + ch) =
               make_float4(v[0], v[1], v[2], v[3]);
         }
       } else {
-        const long long first = (t - (kind == 1 ? tq : tq + tw)) * kTT;
-        const int n = kind == 1 ? q.r : a.N;
-        const T* kp = kind == 1 ? static_cast<const T*>(a.c.k_res) + unit * a.c.R * D
-                                : static_cast<const T*>(a.k) + unit * a.N * D;
-        const T* vp = kind == 1 ? static_cast<const T*>(a.c.v_res) + unit * a.c.R * D
-                                : static_cast<const T*>(a.v) + unit * a.N * D;
+        const long long first = (t - tq) * kTT;
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
           const long long tok = first + tk + i;
+          const float* kp = nullptr;
+          const float* vp = nullptr;
+          if (tok < q.r) {
+            kp = static_cast<const float*>(a.c.k_res) + (unit * a.c.R + tok) * D + ch;
+            vp = static_cast<const float*>(a.c.v_res) + (unit * a.c.R + tok) * D + ch;
+          } else if (tok < q.r + a.N) {
+            kp = static_cast<const float*>(a.k) + (unit * a.N + tok - q.r) * D + ch;
+            vp = static_cast<const float*>(a.v) + (unit * a.N + tok - q.r) * D + ch;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool in = tok < n;
-            sm[SM::K + (tk + i) * SM::LD + ch + e] = in ? to_f32(kp[tok * D + ch + e]) : 0.f;
-            sm[SM::V + (tk + i) * D + ch + e] = in ? to_f32(vp[tok * D + ch + e]) : 0.f;
+            sm[SM::K + (tk + i) * SM::LD + ch + e] = kp ? kp[e] : 0.f;
+            sm[SM::V + (tk + i) * D + ch + e] = vp ? vp[e] : 0.f;
           }
         }
       }
@@ -164,20 +167,20 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
             sc[i][j] = fmaf(qv[i].w, kv[j].w, sc[i][j]);
           }
       }
-      // ---- masks: window slots from r on, drafted tokens that a node does not see
-      if (kind != 0) {
-        const long long first = (t - (kind == 1 ? tq : tq + tw)) * kTT;
+      // ---- masks: drafted tokens that a node does not see, and the end
+      if (raw) {
 #pragma unroll
         for (int i = 0; i < SR; ++i) {
-          uint32_t sees = 0xffffffffu;
           const int row = row0 + sr0 + i;
-          if (kind == 2)
-            sees = row < rows ? a.mask[(b * a.N + row % a.N) * mw + first / 32] : 0u;
+          const uint32_t* mk = a.mask + (b * a.N + row % a.N) * mw;
 #pragma unroll
           for (int j = 0; j < SC; ++j) {
-            const int tl = sc0 + j * TCN;
-            const bool in = kind == 1 ? first + tl < q.r
-                                      : first + tl < a.N && ((sees >> tl) & 1u);
+            const long long tok = (t - tq) * kTT + sc0 + j * TCN;
+            bool in = tok < q.r;
+            if (!in && tok < q.r + a.N && row < rows) {
+              const int node = (int)(tok - q.r);
+              in = (mk[node / 32] >> (node % 32)) & 1u;
+            }
             if (!in) sc[i][j] = -kInf;
           }
         }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
             }
         }
       };
-      if (kind == 2)
+      if (raw)
         add(std::true_type{});
       else
         add(std::false_type{});
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     }
     __syncthreads();
     if (whole) {
-      T* op = static_cast<T*>(a.out) + (unit * rows + row0) * D;
+      float* op = static_cast<float*>(a.out) + (unit * rows + row0) * D;
 #pragma unroll
       for (int i = 0; i < OR; ++i) {
         if (row0 + or0 + i >= rows) continue;
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
 #pragma unroll
           for (int e = 0; e < OV; ++e)
             op[(or0 + i) * D + g * (D / ON) + oc0 + e] =
-                from_f32<T>(lr == 0.f ? 0.f : acc[i][g * OV + e] * inv);
+                lr == 0.f ? 0.f : acc[i][g * OV + e] * inv;
       }
     } else {
       float* pp = a.part + (2 * W0 + (tile0 == 0)) * tree_part(p, D);
@@ -292,61 +295,39 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
   }
 }
 
-template <int D, int BITS, typename T, typename M, int RB>
+template <int D, int BITS, int RB>
 cudaError_t tree_r(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
   constexpr int bytes = SimtSmem<D, RB>::FLOATS * 4;
-  const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D, BITS, T, M, RB>,
+  const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D, BITS, RB>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  tree_simt_kernel<D, BITS, T, M, RB><<<p.ctas, kThreads, bytes, s>>>(a, p);
+  tree_simt_kernel<D, BITS, RB><<<p.ctas, kThreads, bytes, s>>>(a, p);
   return cudaGetLastError();
 }
-template <int D, int BITS, typename T, typename M>
+template <int D, int BITS>
 cudaError_t tree_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  return p.rb == 16 ? tree_r<D, BITS, T, M, 16>(a, p, s) : tree_r<D, BITS, T, M, 64>(a, p, s);
+  return p.rb == 16 ? tree_r<D, BITS, 16>(a, p, s) : tree_r<D, BITS, 64>(a, p, s);
 }
-template <int BITS, typename T, typename M>
+template <int BITS>
 cudaError_t tree_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
   switch (a.D) {
-    case 32: return tree_t<32, BITS, T, M>(a, p, s);
-    case 64: return tree_t<64, BITS, T, M>(a, p, s);
-    case 128: return tree_t<128, BITS, T, M>(a, p, s);
-  }
-  return cudaErrorInvalidValue;
-}
-template <typename T, typename M>
-cudaError_t tree_b(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  switch (a.bits) {
-    case 1: return tree_d<1, T, M>(a, p, s);
-    case 2: return tree_d<2, T, M>(a, p, s);
-    case 3: return tree_d<3, T, M>(a, p, s);
-    case 4: return tree_d<4, T, M>(a, p, s);
+    case 32: return tree_t<32, BITS>(a, p, s);
+    case 64: return tree_t<64, BITS>(a, p, s);
+    case 128: return tree_t<128, BITS>(a, p, s);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-TreePlan tree_plan_simt(int gq, int N, int sms) {
-  TreePlan p;
-  p.rb = gq * N <= 16 ? 16 : 64;
-  p.tt = kTT;
-  p.n_rb = (gq * N + p.rb - 1) / p.rb;
-  p.ctas = sms * (p.rb == 16 ? 4 : 2);
-  p.min_w = 4;
-  return p;
-}
-
-cudaError_t launch_tree_simt(const TreeArgs& a, cudaStream_t s) {
-  const TreePlan p = tree_plan_simt(a.gq, a.N, a.sms);
-  cudaError_t e;
-  if (a.dtype == 1)
-    e = tree_b<float, float>(a, p, s);
-  else if (a.c.meta == 1)
-    e = tree_b<__half, __half>(a, p, s);
-  else
-    e = tree_b<__half, float>(a, p, s);
-  return e == cudaSuccess ? launch_tree_merge(a, p, s) : e;
+cudaError_t tree_simt(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  switch (a.bits) {
+    case 1: return tree_d<1>(a, p, s);
+    case 2: return tree_d<2>(a, p, s);
+    case 3: return tree_d<3>(a, p, s);
+    case 4: return tree_d<4>(a, p, s);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace kivi
