@@ -85,8 +85,12 @@ struct TcGeo {
   static constexpr int S_F = S_M + 128 * 4;               // 2 x [128 rows]
   static constexpr int S_LZ = S_F + 2 * 128 * 4;          // [128 rows][8]
   static constexpr int S_MASK = S_LZ + 128 * 8 * 4;       // [256][8] words
-  static constexpr int S_END = S_MASK + 256 * 8 * 4;
-  static constexpr int BYTES = S_END;
+  // zeros as binary16 in operand order, rows padded against bank conflicts:
+  // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
+  static constexpr int ZLD = 136;
+  static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
+  static constexpr int S_ZV = S_ZH + 8 * ZLD * 2;         // 2 x
+  static constexpr int BYTES = S_ZV + 2 * 8 * ZLD * 2;
 };
 
 // Position of code i of a block of E in the order of the operands: the pair
@@ -115,12 +119,13 @@ __device__ __forceinline__ void tc_expect(uint64_t* b, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
-// Waits for phase `n` (counted from 0) of a barrier; bounded by ~2 s.
-__device__ __forceinline__ void tc_wait(uint64_t* b, long long n, volatile int* dead) {
+// Waits for phase `n` (counted from 0) of a barrier; bounded: each try suspends
+// for up to a microsecond, so some seconds at most.
+__device__ __forceinline__ void tc_wait(uint64_t* b, int n, volatile int* dead) {
   const uint32_t addr = tc_smem(b), par = (uint32_t)(n & 1);
-  uint32_t ok = 0;
-  const long long t0 = clock64();
-  for (;;) {
+#pragma unroll 1
+  for (int tries = 0; tries < (1 << 21); ++tries) {
+    uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
@@ -129,11 +134,8 @@ __device__ __forceinline__ void tc_wait(uint64_t* b, long long n, volatile int* 
         : "r"(addr), "r"(par)
         : "memory");
     if (ok || *dead) return;
-    if (clock64() - t0 > (1LL << 32)) {
-      *dead = 1;
-      return;
-    }
   }
+  *dead = 1;
 }
 __device__ __forceinline__ void tc_copy(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
   asm volatile(
@@ -161,8 +163,7 @@ __device__ __forceinline__ void tc_fence_smem() {
 __device__ __forceinline__ void tc_st8(uint32_t t, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 __device__ __forceinline__ void tc_ld16(uint32_t t, float (&r)[16]) {
   uint32_t u[16];
@@ -172,8 +173,7 @@ __device__ __forceinline__ void tc_ld16(uint32_t t, float (&r)[16]) {
       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
         "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
         "=r"(u[14]), "=r"(u[15])
-      : "r"(t)
-      : "memory");
+      : "r"(t));
   tc_wait_ld();
 #pragma unroll
   for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
@@ -210,6 +210,21 @@ __device__ __forceinline__ void tc_commit(uint64_t* b) {
                    tc_smem(b))
                : "memory");
 }
+// A row of K-slices of one product: 8 columns of A and 256 bytes of B each.
+template <int KS>
+__device__ __forceinline__ void tc_mma_row(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           bool add) {
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) tc_mma(d, a + 8 * ks, b + 16 * ks, idesc, add || ks > 0);
+}
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ float tc_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -242,8 +257,35 @@ __device__ __forceinline__ void tc_sync_segment() {
   asm volatile("bar.sync 3, %0;" ::"n"(kTcThreads - 32) : "memory");
   tc_fence_after();
 }
-__device__ __forceinline__ void tc_named(int id) {
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+template <int ID>
+__device__ __forceinline__ void tc_named() {
+  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+}
+// The same for group `sg` of two (barriers 1 and 2).
+__device__ __forceinline__ void tc_group(int sg) {
+  if (sg == 0)
+    tc_named<1>();
+  else
+    tc_named<2>();
+}
+// Barrier of the group that tells whether any of its threads has `x`.
+__device__ __forceinline__ bool tc_group_any(int sg, bool x) {
+  uint32_t r;
+  if (sg == 0)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+  return r != 0;
 }
 
 // ---- codes as binary16 ---------------------------------------------------------
@@ -290,34 +332,34 @@ __device__ __forceinline__ uint32_t tc_pair(const uint32_t* w) {
     return tc_code<e>((sh ? w[0] >> sh : w[0]) & m);
   }
 }
-// 16 codes of a lane: registers 8 CHUNK .. of its operand row; `word(i)` gives
-// word i of the lane's row of words.
-template <int BITS, int CHUNK, typename F>
-__device__ __forceinline__ void tc_codes16(F word, uint32_t (&c)[8]) {
+// What a loop over a lane's words takes at a time: kUnit codes in kUnitW words.
+template <int BITS>
+struct TcUnit {
+  static constexpr int E = BITS == 3 ? 32 : 32 / BITS, WB = BITS == 3 ? 3 : 1;
+  static constexpr int kUnit = E < 16 ? 16 : E;
+  static constexpr int kUnitW = kUnit / E * WB;
+};
+// 16 of a unit's codes, registers 8 HALF .. of its part of the operand row.
+template <int BITS, int HALF>
+__device__ __forceinline__ void tc_codes16(const uint32_t* w, uint32_t (&c)[8]) {
   if constexpr (BITS == 4) {
-    const uint32_t a = word(2 * CHUNK), b = word(2 * CHUNK + 1);
-    c[0] = tc_pair<4, 0>(&a);
-    c[1] = tc_pair<4, 1>(&a);
-    c[2] = tc_pair<4, 2>(&a);
-    c[3] = tc_pair<4, 3>(&a);
-    c[4] = tc_pair<4, 0>(&b);
-    c[5] = tc_pair<4, 1>(&b);
-    c[6] = tc_pair<4, 2>(&b);
-    c[7] = tc_pair<4, 3>(&b);
+    c[0] = tc_pair<4, 0>(w);
+    c[1] = tc_pair<4, 1>(w);
+    c[2] = tc_pair<4, 2>(w);
+    c[3] = tc_pair<4, 3>(w);
+    c[4] = tc_pair<4, 0>(w + 1);
+    c[5] = tc_pair<4, 1>(w + 1);
+    c[6] = tc_pair<4, 2>(w + 1);
+    c[7] = tc_pair<4, 3>(w + 1);
   } else {
-    constexpr int E = BITS == 3 ? 32 : 32 / BITS, WB = BITS == 3 ? 3 : 1;
-    constexpr int blk = 16 * CHUNK / E, i0 = 16 * CHUNK % E / 2;
-    uint32_t w[WB];
-#pragma unroll
-    for (int p = 0; p < WB; ++p) w[p] = word(blk * WB + p);
-    c[0] = tc_pair<BITS, i0 + 0>(w);
-    c[1] = tc_pair<BITS, i0 + 1>(w);
-    c[2] = tc_pair<BITS, i0 + 2>(w);
-    c[3] = tc_pair<BITS, i0 + 3>(w);
-    c[4] = tc_pair<BITS, i0 + 4>(w);
-    c[5] = tc_pair<BITS, i0 + 5>(w);
-    c[6] = tc_pair<BITS, i0 + 6>(w);
-    c[7] = tc_pair<BITS, i0 + 7>(w);
+    c[0] = tc_pair<BITS, 8 * HALF + 0>(w);
+    c[1] = tc_pair<BITS, 8 * HALF + 1>(w);
+    c[2] = tc_pair<BITS, 8 * HALF + 2>(w);
+    c[3] = tc_pair<BITS, 8 * HALF + 3>(w);
+    c[4] = tc_pair<BITS, 8 * HALF + 4>(w);
+    c[5] = tc_pair<BITS, 8 * HALF + 5>(w);
+    c[6] = tc_pair<BITS, 8 * HALF + 6>(w);
+    c[7] = tc_pair<BITS, 8 * HALF + 7>(w);
   }
 }
 // Half of s in two binary16 parts: its leading 7 bits, and the rest.
@@ -353,12 +395,49 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-template <int N, typename F>
-__device__ __forceinline__ void tc_static_for(F f) {
-  if constexpr (N > 0) {
-    tc_static_for<N - 1>(f);
-    f(std::integral_constant<int, N - 1>{});
+// A lane's words (`stride` words apart) into its row of the two planes, N codes; sc:
+// their scales' parts, hi[N] and lo[N].  The loop stays a loop: the kernel's roles
+// share the instruction cache.
+template <int BITS, int N>
+__device__ __forceinline__ void tc_unpack(uint32_t t_hi, uint32_t t_lo, const uint32_t* words,
+                                          int stride, const __half* sc) {
+  using U = TcUnit<BITS>;
+  const uint4* hi = reinterpret_cast<const uint4*>(sc);
+  const uint4* lo = reinterpret_cast<const uint4*>(sc + N);
+#pragma unroll(N / U::kUnit >= 4 ? 2 : 1)
+  for (int u = 0; u < N / U::kUnit; ++u) {
+    uint32_t w[U::kUnitW], c[8];
+#pragma unroll
+    for (int i = 0; i < U::kUnitW; ++i) w[i] = words[(u * U::kUnitW + i) * stride];
+    constexpr int H = U::kUnit / 16;
+    tc_codes16<BITS, 0>(w, c);
+    tc_put16(t_hi + 8 * H * u, t_lo + 8 * H * u, c, hi + 2 * H * u, lo + 2 * H * u);
+    if constexpr (H == 2) {
+      tc_codes16<BITS, 1>(w, c);
+      tc_put16(t_hi + 16 * u + 8, t_lo + 16 * u + 8, c, hi + 4 * u + 2, lo + 4 * u + 2);
+    }
   }
+}
+// Eight adjacent raw elements; aligned: by one 16-byte load.
+__device__ __forceinline__ uint4 tc_raw8(const __half* p, bool aligned) {
+  if (aligned) return *reinterpret_cast<const uint4*>(p);
+  uint16_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __half_as_ushort(p[i]);
+  return make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
+                    v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+}
+
+// Whether rows row0 .. row0 + 15 see drafted token `node`, one bit each.
+__device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, int row0, int N) {
+  uint32_t bits = 0;
+  int q = row0 % N;
+#pragma unroll 1
+  for (int e = 0; e < 16; ++e) {
+    bits |= ((mask_s[q * 8 + (node >> 5)] >> (node & 31)) & 1u) << e;
+    if (++q == N) q = 0;
+  }
+  return bits;
 }
 
 // Tensor-memory columns.
@@ -374,10 +453,10 @@ struct TcBars {
 
 // One segment: tiles [t0, t0 + nt) of a group.
 struct TcSeg {
-  long long b, unit, t0, nt, tq, ut, n_q;
+  long long b, unit, n_q;
+  int t0, nt, tq;      // first tile, tiles, tiles of quantized tokens
   int r, row0, nrows;  // nrows: rows of this block that exist
-  int h, whole;
-  bool ok;
+  bool whole, ok;
 };
 
 template <int D, int BITS, typename M>
@@ -391,10 +470,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
   __shared__ int s_poison[2];   // [segment parity]
-  __shared__ int s_need[2][2];  // [softmax group][tile parity]: a row's reference has to rise
   __shared__ int s_resc[2][8];  // [tile parity][16 rows]: rows were rescaled
   volatile int* dead = &s_dead;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // what a whole warp shares is broadcast, so that it lives in uniform registers
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // ---- set-up
   if (warp == 20) {
@@ -412,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   }
   if (tid == 32) {
     s_dead = 0;
-    for (int i = 0; i < 2; ++i) s_poison[i] = s_need[0][i] = s_need[1][i] = 0;
+    for (int i = 0; i < 2; ++i) s_poison[i] = 0;
     for (int i = 0; i < 3; ++i) {
       tc_bar_init(&bars.raw_full[i], 1);
       tc_bar_init(&bars.raw_empty[i], 12);
@@ -430,10 +509,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  for (int i = tid; i < 2 * 8 * Ge::ZLD; i += kTcThreads)
+    reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 8 == 4 ? 1.0f : 0.0f);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   const long long total = s_at.total, W = tree_range(p, total);
   long long x = blockIdx.x * W;
   const long long end = x + W < total ? x + W : total;
@@ -450,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
 
   // counters of this block: tiles, and tiles that went through the ring; the
   // copying warp runs ahead of the others, over its own walk of the segments
-  long long it0 = 0, st0 = 0;
+  int it0 = 0, st0 = 0;
 
   auto next_seg = [&](long long& xx, long long& bb, long long& rr, TcSeg& g) {
     TreeSeq q = tree_seq(a, p, bb);
@@ -460,38 +541,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       ++bb;
       q = tree_seq(a, p, bb);
     }
-    const long long grp = rr / q.ut;
-    g.t0 = rr % q.ut;
-    g.nt = q.ut - g.t0 < end - xx ? q.ut - g.t0 : end - xx;
+    const int ut = (int)q.ut, grp = (int)(rr / ut), left = (int)min(end - xx, 1LL << 30);
+    g.t0 = (int)(rr - (long long)grp * ut);
+    g.nt = ut - g.t0 < left ? ut - g.t0 : left;
     g.b = bb;
-    g.h = (int)(grp / p.n_rb);
-    g.unit = bb * a.Hkv + g.h;
-    g.row0 = (int)(grp % p.n_rb) * p.rb;
+    g.unit = bb * a.Hkv + grp / p.n_rb;
+    g.row0 = grp % p.n_rb * p.rb;
     g.nrows = rows - g.row0 < nr ? rows - g.row0 : nr;
     g.n_q = q.n_q;
     g.r = q.r;
     g.ok = q.ok;
-    g.tq = q.ok ? (q.n_q + kTcTile - 1) / kTcTile : 0;
-    g.ut = q.ut;
-    g.whole = g.t0 == 0 && g.nt == q.ut;
+    g.tq = q.ok ? (int)((q.n_q + kTcTile - 1) / kTcTile) : 0;
+    g.whole = g.t0 == 0 && g.nt == ut;
     xx += g.nt;
     rr += g.nt;
   };
 
   if (warp == 21) {
     // ==== copies: runs ahead over all segments; the ring alone holds it back
-    long long xx = x, bb = sb, rr = rem, st = 0;
+    long long xx = x, bb = sb, rr = rem;
+    int st = 0;
     if (lane == 0) {
       while (xx < end) {
         TcSeg g;
         next_seg(xx, bb, rr, g);
         if (!g.ok) continue;
-        for (long long t = g.t0; t < g.t0 + g.nt && t < g.tq; ++t, ++st) {
-          const int s = (int)(st % Ge::NST);
+        for (int t = g.t0; t < g.t0 + g.nt && t < g.tq; ++t, ++st) {
+          const int s = st % Ge::NST;
           if (st >= Ge::NST) tc_wait(&bars.raw_empty[s], st / Ge::NST - 1, dead);
           if (*dead) break;
           unsigned char* dst = sm + Ge::S_RING + s * Ge::STAGE;
-          const long long left = (g.n_q - t * kTcTile) / kTile;
+          const long long left = (g.n_q - (long long)t * kTcTile) / kTile;
           const int ns = left < 4 ? (int)left : 4;
           const long long Ts = store_tokens(a.c);
           uint32_t bytes = 0;
@@ -500,7 +580,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             const int step = a.c.bt ? 1 : ns;
             for (int i = 0; i < ns; i += step) {
               long long su, stl;
-              if (!store_tile(a.c, g.unit, t * 4 + i, &su, &stl)) continue;
+              if (!store_tile(a.c, g.unit, t * 4LL + i, &su, &stl)) continue;
               if (pass == 0) {
                 bytes += step * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM);
                 continue;
@@ -526,7 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       }
       // no copy may still be under way when the block ends (bounded again)
       int never = 0;
-      for (long long i = st > Ge::NST ? st - Ge::NST : 0; i < st; ++i)
+      for (int i = st > Ge::NST ? st - Ge::NST : 0; i < st; ++i)
         tc_wait(&bars.raw_full[i % Ge::NST], i / Ge::NST, &never);
     }
     __syncwarp();
@@ -541,8 +621,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     if (!g.ok) s_poison[seg & 1] = 1;
     if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
       const long long i1 =
-          (g.t0 + g.nt) * 4 < g.n_q / kTile ? (g.t0 + g.nt) * 4 : g.n_q / kTile;
-      for (long long i = g.t0 * 4 + tid; i < i1; i += kTcThreads - 32) {
+          (g.t0 + g.nt) * 4LL < g.n_q / kTile ? (g.t0 + g.nt) * 4LL : g.n_q / kTile;
+      for (long long i = g.t0 * 4LL + tid; i < i1; i += kTcThreads - 32) {
         long long su, stl;
         if (!store_tile(a.c, g.unit, i, &su, &stl)) s_poison[seg & 1] = 1;
       }
@@ -568,10 +648,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         // ==== keys: lane = token of subtile `warp`
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
         __half* sc = reinterpret_cast<__half*>(sm + Ge::S_KSC + warp * D * 4);  // hi[D], lo[D]
-        long long it = it0, st = st0;
-        for (long long t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
+        int it = it0, st = st0;
+        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
           if (t < g.tq) {
-            const int s = (int)(st % Ge::NST);
+            const int s = st % Ge::NST;
             tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
             const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
             const M* ks = reinterpret_cast<const M*>(stg + Ge::O_KS + warp * Ge::KM);
@@ -584,18 +664,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
               sc[D + tc_pos<E>(c)] = lo;
             }
             __syncwarp();
-            const uint32_t* kw =
-                reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + warp * Ge::KC) + lane * WK;
             if (it > 0) tc_wait(&bars.s_full[(it - 1) & 1], (it - 1) >> 1, dead);
             tc_fence_after();
-            tc_static_for<D / 16>([&](auto ci) {
-              constexpr int C = decltype(ci)::value;
-              uint32_t c[8];
-              tc_codes16<BITS, C>([&](int i) { return kw[i]; }, c);
-              tc_put16(t_lane + kTKhi + 8 * C, t_lane + kTKlo + 8 * C, c,
-                       reinterpret_cast<const uint4*>(sc) + 2 * C,
-                       reinterpret_cast<const uint4*>(sc + D) + 2 * C);
-            });
+            tc_unpack<BITS, D>(
+                t_lane + kTKhi, t_lane + kTKlo,
+                reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + warp * Ge::KC) + lane * WK, 1, sc);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -606,26 +679,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             ++st;
           } else {
             // raw tokens: the window, then the drafted ones; halved like s
-            const long long i = (t - g.tq) * kTcTile + warp * 32 + lane;
+            const int i = (t - g.tq) * kTcTile + warp * 32 + lane;
             const __half* src = nullptr;
             if (i < g.r)
               src = static_cast<const __half*>(a.c.k_res) + (g.unit * a.c.R + i) * D;
             else if (i < g.r + a.N)
               src = static_cast<const __half*>(a.k) + (g.unit * a.N + (i - g.r)) * D;
+            const bool al = ((uintptr_t)src & 15) == 0;
             if (it > 0) tc_wait(&bars.s_full[(it - 1) & 1], (it - 1) >> 1, dead);
             tc_fence_after();
-#pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t r[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t lo =
-                    src ? __half_as_ushort(src[tc_elem<E>(c0 + 2 * j)]) : (uint16_t)0;
-                const uint32_t hi =
-                    src ? __half_as_ushort(src[tc_elem<E>(c0 + 2 * j + 1)]) : (uint16_t)0;
-                r[j] = tc_hmul2(lo | (hi << 16), 0x38003800u);
+            // 16 places of the operand order: two runs of 8 channels, E / 2 apart (or
+            // two blocks of 8 channels)
+#pragma unroll 2
+            for (int c = 0; c < D / 16; ++c) {
+              const int e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
+              uint4 x = make_uint4(0, 0, 0, 0), y = x;
+              if (src != nullptr) {
+                x = tc_raw8(src + e0, al);
+                y = tc_raw8(src + e0 + (E >= 16 ? E / 2 : 8), al);
               }
-              tc_st8(t_lane + kTKhi + c0 / 2, r);
+              uint32_t r[8];
+              if constexpr (E >= 16) {  // (x_j, y_j)
+                r[0] = __byte_perm(x.x, y.x, 0x5410);
+                r[1] = __byte_perm(x.x, y.x, 0x7632);
+                r[2] = __byte_perm(x.y, y.y, 0x5410);
+                r[3] = __byte_perm(x.y, y.y, 0x7632);
+                r[4] = __byte_perm(x.z, y.z, 0x5410);
+                r[5] = __byte_perm(x.z, y.z, 0x7632);
+                r[6] = __byte_perm(x.w, y.w, 0x5410);
+                r[7] = __byte_perm(x.w, y.w, 0x7632);
+              } else {  // (x_j, x_j+4), then y
+                r[0] = __byte_perm(x.x, x.z, 0x5410);
+                r[1] = __byte_perm(x.x, x.z, 0x7632);
+                r[2] = __byte_perm(x.y, x.w, 0x5410);
+                r[3] = __byte_perm(x.y, x.w, 0x7632);
+                r[4] = __byte_perm(y.x, y.z, 0x5410);
+                r[5] = __byte_perm(y.x, y.z, 0x7632);
+                r[6] = __byte_perm(y.y, y.w, 0x5410);
+                r[7] = __byte_perm(y.y, y.w, 0x7632);
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
+              tc_st8(t_lane + kTKhi + 8 * c, r);
             }
             tc_wait_st();
             tc_fence_before();
@@ -639,15 +734,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         const int ch = vw * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(vw * 32) << 16);
         __half* sc = reinterpret_cast<__half*>(sm + Ge::S_VSC + vw * 128 * 4);  // hi[128], lo[128]
-        long long it = it0, st = st0;
-        for (long long t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
+        int it = it0, st = st0;
+        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
           if (t < g.tq) {
-            const int s = (int)(st % Ge::NST);
+            const int s = st % Ge::NST;
             tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
             if (vw < NJ) {
               const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
               const M* vs = reinterpret_cast<const M*>(stg + Ge::O_VS);
-              const long long n = g.n_q - t * kTcTile;  // tokens that exist
+              const long long n = g.n_q - (long long)t * kTcTile;  // tokens that exist
               __syncwarp();
 #pragma unroll
               for (int k = lane; k < 128; k += 32) {
@@ -657,17 +752,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 sc[128 + tc_pos<E>(k)] = lo;
               }
               __syncwarp();
-              const uint32_t* vwp = reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + ch;
               if (it > 0) tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
               tc_fence_after();
-              tc_static_for<8>([&](auto ci) {
-                constexpr int C = decltype(ci)::value;
-                uint32_t c[8];
-                tc_codes16<BITS, C>([&](int i) { return vwp[i * D]; }, c);
-                tc_put16(t_lane + kTVhi + 8 * C, t_lane + kTVlo + 8 * C, c,
-                         reinterpret_cast<const uint4*>(sc) + 2 * C,
-                         reinterpret_cast<const uint4*>(sc + 128) + 2 * C);
-              });
+              tc_unpack<BITS, 128>(t_lane + kTVhi, t_lane + kTVlo,
+                                   reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + ch, D, sc);
               tc_wait_st();
               tc_fence_before();
             } else if (it > 0) {
@@ -683,34 +771,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             if (it > 0) tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
             tc_fence_after();
             if (vw < NJ) {
-              const long long first = (t - g.tq) * kTcTile;
+              const int first = (t - g.tq) * kTcTile, n = g.r + a.N;
               const __half* wp = static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D + ch;
               const __half* dp = static_cast<const __half*>(a.v) + g.unit * a.N * D + ch;
-              bool odd = false;
-#pragma unroll 2
+              uint32_t odd = 0;
+#pragma unroll 1
               for (int c0 = 0; c0 < 128; c0 += 16) {
+                uint16_t v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const int i = first + tc_elem<E>(c0 + k);
+                  v[k] = i < n ? __half_as_ushort(i < g.r ? wp[i * D] : dp[(i - g.r) * D]) : 0;
+                }
                 uint32_t r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  uint32_t u[2];
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int k = c0 + 2 * j + e;
-                    const long long i = first + k / E * E + (k % E >> 1) + (k & 1) * (E / 2);
-                    uint16_t v = 0;
-                    if (i < g.r)
-                      v = __half_as_ushort(wp[i * D]);
-                    else if (i < g.r + a.N)
-                      v = __half_as_ushort(dp[(i - g.r) * D]);
-                    // infinities and NaN join at the segment's end, for the rows
-                    // that attend to them
-                    if ((v & 0x7C00u) == 0x7C00u) {
-                      odd = true;
-                      v = 0;
-                    }
-                    u[e] = v;
-                  }
-                  r[j] = tc_hmul2(u[0] | (u[1] << 16), 0x38003800u);
+                  uint32_t u = v[2 * j] | (uint32_t)v[2 * j + 1] << 16;
+                  // infinities and NaN join at the segment's end, for the rows that
+                  // attend to them
+                  const uint32_t x = (((u & 0x7C007C00u) + 0x04000400u) & 0x80008000u);
+                  odd |= x;
+                  u &= ~((x >> 15) * 0xFFFFu);
+                  r[j] = tc_hmul2(u, 0x38003800u);
                 }
                 tc_st8(t_lane + kTVhi + c0 / 2, r);
               }
@@ -730,25 +812,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + sw * 128;
         const float c1 = 2.0f * a.qscale;
         const int pk = tc_pos<E>(sw * 32 + lane);  // the token's place in the second product
-        long long it = it0;
-        for (long long t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          const int par = (int)(it & 1);
+        int it = it0;
+        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
+          const int par = it & 1;
           const bool raw = t >= g.tq;
           const uint32_t t_s = t_lane + kTS + (s2 ? 64 * par : 0);
           // the token of this lane: in the cache (all rows see it), drafted, or none
-          long long i = (raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
+          const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
           bool in = raw ? i < g.r : i < g.n_q;
           const int node = raw && i >= g.r && i < g.r + a.N ? (int)(i - g.r) : -1;
           auto seen = [&](int ch) -> uint32_t {  // 16 bits, one for each row of chunk ch
-            if (in) return 0xFFFFu;
-            if (node < 0) return 0u;
-            uint32_t bits = 0;
-            int q = (g.row0 + ch * 16) % a.N;
-            for (int e = 0; e < 16; ++e) {
-              bits |= ((mask_s[q * 8 + (node >> 5)] >> (node & 31)) & 1u) << e;
-              if (++q == a.N) q = 0;
-            }
-            return bits;
+            return in ? 0xFFFFu : (node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + ch * 16, a.N));
           };
           // what the products two tiles ago read (weights, factors) may be written again
           if (it >= 2) {
@@ -758,8 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           tc_wait(&bars.z_full[par], it >> 1, dead);
           for (int e = lane; e < nr; e += 32)
             if (((e >> 4) & 1) == sg) off_s[e] = m_s[e] - zk_s[(par * 4 + sw) * 128 + e];
-          tc_named(1 + sg);
-          if (lane == 0 && sw == 0) s_need[sg][par ^ 1] = 0;  // the next tile's
+          __syncwarp();
           tc_wait(&bars.s_full[par], it >> 1, dead);
           tc_fence_after();
           // ---- does any score exceed its row's reference by too much?
@@ -767,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           for (int ch = sg; ch < nch; ch += 2) {
             float v[16];
             tc_ld16(t_s + ch * 16, v);
-            const uint32_t sees = raw ? seen(ch) : (in ? 0xFFFFu : 0u);
+            const uint32_t sees = seen(ch);
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
               const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
@@ -779,16 +852,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
               }
             }
           }
-          const bool need_w = __any_sync(0xffffffffu, over > kTcSlack);
-          if (need_w && lane == 0) s_need[sg][par] = 1;
-          tc_named(1 + sg);
-          const bool need = s_need[sg][par] != 0;
+          const bool need = tc_group_any(sg, over > kTcSlack);
           if (need) {
             // ---- new references: each warp's maxima, joined
             for (int ch = sg; ch < nch; ch += 2) {
               float v[16];
               tc_ld16(t_s + ch * 16, v);
-              const uint32_t sees = raw ? seen(ch) : (in ? 0xFFFFu : 0u);
+              const uint32_t sees = seen(ch);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int row = ch * 16 + e;
@@ -797,7 +867,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 if (lane == e) wmax_s[row] = d;
               }
             }
-            tc_named(1 + sg);
+            tc_group(sg);
             const float* wm = reinterpret_cast<const float*>(sm + Ge::S_WMAX);
             for (int e = (sw * 32 + lane); e < nr; e += 128) {
               if (((e >> 4) & 1) != sg) continue;
@@ -806,7 +876,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
               f_s[par * 128 + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
               m_s[e] = mn;
             }
-            tc_named(1 + sg);
+            tc_group(sg);
             for (int e = lane; e < nr; e += 32)
               if (((e >> 4) & 1) == sg) off_s[e] = m_s[e] - zk_s[(par * 4 + sw) * 128 + e];
             if (t > g.t0) {
@@ -831,7 +901,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           for (int ch = sg; ch < nch; ch += 2) {
             float v[16];
             tc_ld16(t_s + ch * 16, v);
-            const uint32_t sees = raw ? seen(ch) : (in ? 0xFFFFu : 0u);
+            const uint32_t sees = seen(ch);
             uint32_t w[8];
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
@@ -867,56 +937,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-        const int n8 = lane >> 2, kq = (lane & 3) * 2;
-        // z of the tile for the values' sums, kept until the weights are there
-        auto zv_pair = [&](const unsigned char* stg, long long n, int ks, int up) -> uint32_t {
-          // tokens at operand places 16 ks + kq + up, + 1; column n8: group n8's zero, or (4) a one
-          if (n8 > 4) return 0u;
-          const int k = 16 * ks + kq + up;
-          uint32_t o = 0;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = tc_elem<E>(k + e);
-            __half z = __ushort_as_half(0);
-            if (n8 == 4)
-              z = __float2half_rn(1.0f);
-            else if (stg != nullptr && n8 < NJ && tok < n)
-              z = __float2half_rn(to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[tok * NJ + n8]));
-            o |= (uint32_t)__half_as_ushort(z) << (16 * e);
-          }
-          return o;
-        };
-        long long it = it0, st = st0;
-        for (long long t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          const int par = (int)(it & 1);
+        const int n8 = lane >> 2, kq = (lane & 3) * 2, ht = hw * 32 + lane;
+        __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
+        int st = st0;
+        // the zeros' part of tile t: their products with the queries for its scores,
+        // and the values' zeros set out for its sums
+        auto zeros = [&](int t, int it) {
+          const int par = it & 1;
+          __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
           const bool raw = t >= g.tq;
-          const int s = (int)(st % Ge::NST);
-          const unsigned char* stg = raw ? nullptr : sm + Ge::S_RING + s * Ge::STAGE;
-          const long long n = raw ? 0 : g.n_q - t * kTcTile;
-          if (!raw) tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+          if (!raw) {
+            const int s = st % Ge::NST;
+            const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+            const long long n = g.n_q - (long long)t * kTcTile;
+            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+            const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
+            const M* vz = reinterpret_cast<const M*>(stg + Ge::O_VZ);
+#pragma unroll 2
+            for (int i = ht; i < 4 * D; i += 128)
+              zh[i / D * Ge::ZLD + tc_pos<E>(i % D)] = __float2half_rn(to_f32(kz[i]));
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              zv[j * Ge::ZLD + tc_pos<E>(ht)] =
+                  ht < n ? __float2half_rn(to_f32(vz[ht * NJ + j])) : __ushort_as_half(0);
+            tc_named<4>();
+            if (lane == 0) tc_arrive(&bars.raw_empty[s]);
+            ++st;
+          } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ht] = __ushort_as_half(0);
+            tc_named<4>();
+          }
           if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
-          // ---- sum_d q_d z_gd of the four groups
           float zc[2][4];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) zc[k][e] = 0.f;
-          if (!raw) {
-            const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
-#pragma unroll
+          if (!raw && hw < nch) {
+#pragma unroll 2
             for (int ks = 0; ks < KS; ++ks) {
-              uint32_t bz[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint32_t o = 0;
-                if (n8 < 4 && n8 * 32 < n) {
-                  const int k = 16 * ks + kq + 8 * u;
-                  const __half z0 = __float2half_rn(to_f32(kz[n8 * D + tc_elem<E>(k)]));
-                  const __half z1 = __float2half_rn(to_f32(kz[n8 * D + tc_elem<E>(k + 1)]));
-                  o = __half_as_ushort(z0) | ((uint32_t)__half_as_ushort(z1) << 16);
-                }
-                bz[u] = o;
-              }
+              // rows 4 .. 7 of the table are not there: columns that nothing reads
+              const __half* zr = zh + (n8 & 3) * Ge::ZLD + 16 * ks + kq;
+              const uint32_t b0 = *reinterpret_cast<const uint32_t*>(zr);
+              const uint32_t b1 = *reinterpret_cast<const uint32_t*>(zr + 8);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int ch = hw + 4 * k;
@@ -926,7 +990,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                   const int row = 16 * ch + (lane & 15);
                   tc_ldm<false>(av, tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) +
                                         (2 * ks + (lane >> 4)) * 128 + row % 8 * 16);
-                  tc_mma16816(zc[k], av, bz[0], bz[1]);
+                  tc_mma16816(zc[k], av, b0, b1);
                 }
               }
             }
@@ -947,19 +1011,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           }
           __syncwarp();
           if (lane == 0) tc_arrive(&bars.z_full[par]);
+          tc_named<4>();  // the keys' table may be written again
+        };
+        int it = it0;
+        zeros(g.t0, it);
+        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
+          const int par = it & 1;
+          if (t + 1 < g.t0 + g.nt) zeros(t + 1, it + 1);
           // ---- sums over the tile's tokens
-          uint32_t bz[8][2];
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            bz[ks][0] = zv_pair(stg, n, ks, 0);
-            bz[ks][1] = zv_pair(stg, n, ks, 8);
-          }
-          __syncwarp();
-          if (!raw) {
-            if (lane == 0) tc_arrive(&bars.raw_empty[s]);
-            ++st;
-          }
           tc_wait(&bars.p_full[par], it >> 1, dead);
+          const __half* zv = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
+          const uint32_t pbase = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int ch = hw + 4 * k;
@@ -971,8 +1033,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 acc[k][2] *= f1;
                 acc[k][3] *= f1;
               }
-              const uint32_t pbase = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2);
-#pragma unroll
+#pragma unroll 2
               for (int ks = 0; ks < 8; ++ks) {
                 // 8 x 8 blocks (tokens x rows), transposed on the way: rows 16 ch + 0 / 8,
                 // tokens 16 ks + 0 / 8
@@ -980,7 +1041,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 uint32_t av[4];
                 tc_ldm<true>(av, pbase + (2 * ch + (blk & 1)) * 2048 + (2 * ks + (blk >> 1)) * 128 +
                                      (lane & 7) * 16);
-                tc_mma16816(acc[k], av, bz[ks][0], bz[ks][1]);
+                tc_mma16816(acc[k], av, *reinterpret_cast<const uint32_t*>(zv + 16 * ks),
+                            *reinterpret_cast<const uint32_t*>(zv + 16 * ks + 8));
               }
             }
           }
@@ -1000,54 +1062,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         }
       } else if (warp == 20) {
         // ==== matrix instructions
-        if (lane == 0) {
-          const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
-          auto scores = [&](long long t, long long it) {
-            const int par = (int)(it & 1);
-            tc_wait(&bars.k_full, it, dead);
-            if (s2) {
-              if (it >= 2) tc_wait(&bars.s_empty[par], (it >> 1) - 1, dead);
-            } else if (it >= 1) {
-              tc_wait(&bars.s_empty[(it - 1) & 1], (it - 1) >> 1, dead);
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + kTS + (s2 ? 64 * par : 0);
-            const uint32_t q = tc_smem(sm + Ge::S_Q);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-              tc_mma(d, tmem + kTKhi + 8 * ks, tc_desc(q + ks * 256, 128, D * 16), id_s, ks > 0);
-            if (t < g.tq) {
-#pragma unroll
-              for (int ks = 0; ks < KS; ++ks)
-                tc_mma(d, tmem + kTKlo + 8 * ks, tc_desc(q + ks * 256, 128, D * 16), id_s, true);
-            }
+        const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
+        const uint64_t q_desc = tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
+        const uint64_t p_desc = tc_desc(tc_smem(sm + Ge::S_P), 128, 2048);
+        const bool one = tc_elect();
+        auto scores = [&](int t, int it) {
+          const int par = __shfl_sync(0xffffffffu, it & 1, 0);
+          tc_wait(&bars.k_full, it, dead);
+          if (s2) {
+            if (it >= 2) tc_wait(&bars.s_empty[par], (it >> 1) - 1, dead);
+          } else if (it >= 1) {
+            tc_wait(&bars.s_empty[par ^ 1], (it - 1) >> 1, dead);
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + kTS + (s2 ? 64 * par : 0);
+          const bool lo = t < g.tq;
+          if (one) {
+            tc_mma_row<KS>(d, tmem + kTKhi, q_desc, id_s, false);
+            if (lo) tc_mma_row<KS>(d, tmem + kTKlo, q_desc, id_s, true);
             tc_commit(&bars.s_full[par]);
-          };
-          long long it = it0;
-          scores(g.t0, it);
-          for (long long t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-            const int par = (int)(it & 1);
-            if (t + 1 < g.t0 + g.nt) scores(t + 1, it + 1);
-            tc_wait(&bars.v_full, it, dead);
-            tc_wait(&bars.p_full[par], it >> 1, dead);
-            tc_fence_after();
-            const uint32_t pa = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              tc_mma(tmem + kTO, tmem + kTVhi + 8 * ks, tc_desc(pa + ks * 256, 128, 2048), id_o,
-                     ks > 0 || t > g.t0);
-            if (t < g.tq) {
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc_mma(tmem + kTO, tmem + kTVlo + 8 * ks, tc_desc(pa + ks * 256, 128, 2048), id_o,
-                       true);
-            }
+          }
+          __syncwarp();
+        };
+        int it = it0;
+        scores(g.t0, it);
+        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
+          const int par = __shfl_sync(0xffffffffu, it & 1, 0);
+          if (t + 1 < g.t0 + g.nt) scores(t + 1, it + 1);
+          tc_wait(&bars.v_full, it, dead);
+          tc_wait(&bars.p_full[par], it >> 1, dead);
+          tc_fence_after();
+          const uint64_t pd = p_desc + (par ? 128 * 128 * 2 / 16 : 0);
+          const bool lo = t < g.tq, add = t > g.t0;
+          if (one) {
+            tc_mma_row<8>(tmem + kTO, tmem + kTVhi, pd, id_o, add);
+            if (lo) tc_mma_row<8>(tmem + kTO, tmem + kTVlo, pd, id_o, true);
             tc_commit(&bars.pv_done[par]);
           }
-          it = it0 + g.nt - 1;
-          tc_wait(&bars.pv_done[it & 1], it >> 1, dead);
+          __syncwarp();
         }
-        __syncwarp();
+        it = it0 + g.nt - 1;
+        tc_wait(&bars.pv_done[it & 1], it >> 1, dead);
       }
     }
     tc_sync_segment();
@@ -1061,42 +1116,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       float* part = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
       for (int ch = sg; ch < nch; ch += 2) {
         float v[16];
-        if (g.ok)
-          tc_ld16(t_lane + kTO + ch * 16, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+        if (g.ok) tc_ld16(t_lane + kTO + ch * 16, v);
         if (ch_d >= D) continue;
+        // infinite or NaN raw values, of the tokens that a row attends to
+        const int i1 = s_odd ? min((g.t0 + g.nt - g.tq) * kTcTile, g.r + a.N) : 0;
+#pragma unroll 1
+        for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
+          const __half w = i < g.r ? static_cast<const __half*>(a.c.v_res)[(g.unit * a.c.R + i) * D + ch_d]
+                                   : static_cast<const __half*>(a.v)[(g.unit * a.N + i - g.r) * D + ch_d];
+          if ((__half_as_ushort(w) & 0x7C00u) != 0x7C00u) continue;
+          const uint32_t sees = i < g.r ? 0xFFFFu : tc_seen(mask_s, i - g.r, g.row0 + ch * 16, a.N);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if ((sees >> e) & 1u) v[e] += __half2float(w);
+        }
+        __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0 + ch * 16) * (long long)D + ch_d;
+        const float* lz = lz_s + ch * 128;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int row = ch * 16 + e;
+          const float l = poison ? kNaN : lz[8 * e + 4];
+          const float o = fmaf(2.0f, v[e], lz[8 * e + sw]);
           if (row >= g.nrows) continue;
-          float l = lz_s[row * 8 + 4], o = 0.f;
-          if (poison) {
-            l = kNaN;
-          } else {
-            o = fmaf(2.0f, v[e], lz_s[row * 8 + sw]);
-            if (s_odd) {
-              // infinite or NaN raw values of tokens that the row attends to
-              const long long i0 = g.t0 > g.tq ? (g.t0 - g.tq) * kTcTile : 0;
-              long long i1 = (g.t0 + g.nt - g.tq) * kTcTile;
-              if (i1 > g.r + a.N) i1 = g.r + a.N;
-              for (long long i = i0; i < i1; ++i) {
-                bool att = i < g.r;
-                __half w;
-                if (att) {
-                  w = static_cast<const __half*>(a.c.v_res)[(g.unit * a.c.R + i) * D + ch_d];
-                } else {
-                  const int node = (int)(i - g.r);
-                  att = (mask_s[(g.row0 + row) % a.N * 8 + (node >> 5)] >> (node & 31)) & 1u;
-                  w = static_cast<const __half*>(a.v)[(g.unit * a.N + node) * D + ch_d];
-                }
-                if (att && (__half_as_ushort(w) & 0x7C00u) == 0x7C00u) o += __half2float(w);
-              }
-            }
-          }
           if (g.whole) {
-            static_cast<__half*>(a.out)[(g.unit * rows + g.row0 + row) * (long long)D + ch_d] =
-                __float2half_rn(l == 0.f ? 0.f : o / l);
+            out[e * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(poison ? 0.f : o, l));
           } else {
-            part[2 * nr + row * D + ch_d] = o;
+            part[2 * nr + row * D + ch_d] = poison ? 0.f : o;
             if (ch_d == 0) {
               part[2 * row] = poison ? 0.f : m_s[row];
               part[2 * row + 1] = l;
@@ -1108,7 +1155,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     if (tid == 0) s_poison[(seg & 1) ^ 1] = 0;  // the next segment's
     if (g.ok) {
       it0 += g.nt;
-      const long long q1 = g.t0 + g.nt < g.tq ? g.t0 + g.nt : g.tq;
+      const int q1 = min(g.t0 + g.nt, g.tq);
       if (q1 > g.t0) st0 += q1 - g.t0;
     }
     tc_sync_segment();
