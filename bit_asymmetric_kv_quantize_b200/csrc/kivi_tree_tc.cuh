@@ -34,11 +34,16 @@
 // nothing; that is checked for all rows by one vote, and the rare tile that
 // needs it rescales O^T in tensor memory.
 //
-// Warps: 4 unpack keys, 4 unpack values, 8 softmax (two groups of four, 16
-// rows at a time in turn), 4 for the zeros' products and the sums, one issues
-// the matrix instructions, one the copies (cp.async.bulk of each tile's six
-// ranges into a ring).  All waits are bounded: one that runs out marks the
-// block dead, whose further waits return at once and whose results are NaN.
+// Warps: 4 unpack keys and 4 values (one code), 2 groups of 4 softmax, 2 the
+// zeros' products with the queries, 4 the sums over tokens, one issues the score
+// products, one the value products, one the copies (cp.async.bulk of each
+// tile's ranges into a ring).  With up to 64 rows the two softmax groups take
+// every other tile, each with its own references and accumulators (two
+// streams, joined at the end of a segment); with more rows they share a tile,
+// 16 rows each in turn.  A role's code is a small loop: together they have to
+// fit the instruction cache (unrolled, the kernel took three times as long).
+// All waits are bounded: one that runs out marks the block dead, whose further
+// waits return at once and whose results are NaN.
 #pragma once
 
 #include <type_traits>
@@ -49,7 +54,7 @@ namespace kivi {
 namespace {
 
 constexpr int kTcTile = 128;        // tokens
-constexpr int kTcWarps = 22;
+constexpr int kTcWarps = 25;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr float kTcSlack = 8.0f;    // log2 units a score may exceed m by
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
@@ -89,7 +94,7 @@ struct TcGeo {
   // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
   static constexpr int ZLD = 136;
   static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
-  static constexpr int S_ZV = S_ZH + 8 * ZLD * 2;         // 2 x
+  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;     // 2 x (both tables)
   static constexpr int BYTES = S_ZV + 2 * 8 * ZLD * 2;
 };
 
@@ -178,14 +183,20 @@ __device__ __forceinline__ void tc_ld16(uint32_t t, float (&r)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
-__device__ __forceinline__ void tc_st16(uint32_t t, const float (&r)[16]) {
-  uint32_t u[8];
+// Four columns, for the loops that run seldom.
+__device__ __forceinline__ void tc_ld4(uint32_t t, float (&r)[4]) {
+  uint32_t u[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+               : "r"(t));
+  tc_wait_ld();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(r[8 * h + i]);
-    tc_st8(t + 8 * h, u);
-  }
+  for (int i = 0; i < 4; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tc_st4(uint32_t t, const float (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t),
+               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])),
+               "r"(__float_as_uint(r[2])), "r"(__float_as_uint(r[3])));
 }
 // Instruction descriptor of kind::f16: D binary32, A and B binary16, A K-major.
 __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_mn) {
@@ -214,7 +225,7 @@ __device__ __forceinline__ void tc_commit(uint64_t* b) {
 template <int KS>
 __device__ __forceinline__ void tc_mma_row(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            bool add) {
-#pragma unroll
+#pragma unroll 2
   for (int ks = 0; ks < KS; ++ks) tc_mma(d, a + 8 * ks, b + 16 * ks, idesc, add || ks > 0);
 }
 // One lane of the warp, the same each time.
@@ -257,17 +268,16 @@ __device__ __forceinline__ void tc_sync_segment() {
   asm volatile("bar.sync 3, %0;" ::"n"(kTcThreads - 32) : "memory");
   tc_fence_after();
 }
-template <int ID>
-__device__ __forceinline__ void tc_named() {
-  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
-}
-// The same for group `sg` of two (barriers 1 and 2).
+// Barrier of softmax group `sg` (barriers 1 and 2).
 __device__ __forceinline__ void tc_group(int sg) {
   if (sg == 0)
-    tc_named<1>();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
   else
-    tc_named<2>();
+    asm volatile("bar.sync 2, 128;" ::: "memory");
 }
+// Barriers of the two warps of the zeros' products and the four of the sums.
+__device__ __forceinline__ void tc_pair_sync() { asm volatile("bar.sync 4, 64;" ::: "memory"); }
+__device__ __forceinline__ void tc_sums_sync() { asm volatile("bar.sync 5, 128;" ::: "memory"); }
 // Barrier of the group that tells whether any of its threads has `x`.
 __device__ __forceinline__ bool tc_group_any(int sg, bool x) {
   uint32_t r;
@@ -395,27 +405,31 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-// A lane's words (`stride` words apart) into its row of the two planes, N codes; sc:
-// their scales' parts, hi[N] and lo[N].  The loop stays a loop: the kernel's roles
-// share the instruction cache.
-template <int BITS, int N>
-__device__ __forceinline__ void tc_unpack(uint32_t t_hi, uint32_t t_lo, const uint32_t* words,
-                                          int stride, const __half* sc) {
+// A lane's words (`stride` words apart) into its row of the two planes, n codes (n
+// a multiple of 32); sc: their scales' parts, hi[n] and lo[n].  The loop stays a
+// loop: the kernel's roles share the instruction cache.
+template <int BITS>
+__device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, int stride,
+                                          const __half* sc, int n) {
   using U = TcUnit<BITS>;
+  constexpr int H = U::kUnit / 16;
   const uint4* hi = reinterpret_cast<const uint4*>(sc);
-  const uint4* lo = reinterpret_cast<const uint4*>(sc + N);
-#pragma unroll(N / U::kUnit >= 4 ? 2 : 1)
-  for (int u = 0; u < N / U::kUnit; ++u) {
+  const uint4* lo = reinterpret_cast<const uint4*>(sc + n);
+#pragma unroll 1
+  for (int u = n / U::kUnit; u > 0; --u) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
-    for (int i = 0; i < U::kUnitW; ++i) w[i] = words[(u * U::kUnitW + i) * stride];
-    constexpr int H = U::kUnit / 16;
+    for (int i = 0; i < U::kUnitW; ++i) w[i] = words[i * stride];
+    words += U::kUnitW * stride;
     tc_codes16<BITS, 0>(w, c);
-    tc_put16(t_hi + 8 * H * u, t_lo + 8 * H * u, c, hi + 2 * H * u, lo + 2 * H * u);
+    tc_put16(t_hi, t_hi + 64, c, hi, lo);
     if constexpr (H == 2) {
       tc_codes16<BITS, 1>(w, c);
-      tc_put16(t_hi + 16 * u + 8, t_lo + 16 * u + 8, c, hi + 4 * u + 2, lo + 4 * u + 2);
+      tc_put16(t_hi + 8, t_hi + 72, c, hi + 2, lo + 2);
     }
+    hi += 2 * H;
+    lo += 2 * H;
+    t_hi += 8 * H;
   }
 }
 // Eight adjacent raw elements; aligned: by one 16-byte load.
@@ -426,6 +440,86 @@ __device__ __forceinline__ uint4 tc_raw8(const __half* p, bool aligned) {
   for (int i = 0; i < 8; ++i) v[i] = __half_as_ushort(p[i]);
   return make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
                     v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+}
+
+// Two runs of eight raw elements, halved, in operand order: pairs (x_j, y_j), or
+// for blocks of 8 (x_j, x_j+4), then y.  (Halving keeps infinities and NaN.)
+template <int E>
+__device__ __forceinline__ void tc_raw_pairs(const uint4& x, const uint4& y, uint32_t (&r)[8]) {
+  if constexpr (E >= 16) {
+    r[0] = __byte_perm(x.x, y.x, 0x5410);
+    r[1] = __byte_perm(x.x, y.x, 0x7632);
+    r[2] = __byte_perm(x.y, y.y, 0x5410);
+    r[3] = __byte_perm(x.y, y.y, 0x7632);
+    r[4] = __byte_perm(x.z, y.z, 0x5410);
+    r[5] = __byte_perm(x.z, y.z, 0x7632);
+    r[6] = __byte_perm(x.w, y.w, 0x5410);
+    r[7] = __byte_perm(x.w, y.w, 0x7632);
+  } else {
+    r[0] = __byte_perm(x.x, x.z, 0x5410);
+    r[1] = __byte_perm(x.x, x.z, 0x7632);
+    r[2] = __byte_perm(x.y, x.w, 0x5410);
+    r[3] = __byte_perm(x.y, x.w, 0x7632);
+    r[4] = __byte_perm(y.x, y.z, 0x5410);
+    r[5] = __byte_perm(y.x, y.z, 0x7632);
+    r[6] = __byte_perm(y.y, y.w, 0x5410);
+    r[7] = __byte_perm(y.y, y.w, 0x7632);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
+}
+// A lane's raw key row, halved, into its operand row: 16 places are two runs of 8
+// channels E / 2 apart (or two blocks of 8 channels).  src null: zeros.
+template <int D, int E>
+__device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* src) {
+  const bool al = ((uintptr_t)src & 15) == 0;
+#pragma unroll 2
+  for (int c = 0; c < D / 16; ++c) {
+    const int e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (src != nullptr) {
+      x = tc_raw8(src + e0, al);
+      y = tc_raw8(src + e0 + (E >= 16 ? E / 2 : 8), al);
+    }
+    uint32_t r[8];
+    tc_raw_pairs<E>(x, y, r);
+    tc_st8(t_hi + 8 * c, r);
+  }
+}
+// A lane's channel of 128 raw tokens from `first` on (the window's r tokens at wp,
+// then the drafted ones at dp up to n), halved, into its operand row.  Infinities
+// and NaN are left out (they join at the segment's end, for the rows that attend
+// to them); returns whether there were any.
+template <int D, int E>
+__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* wp, const __half* dp,
+                                              int first, int r, int n) {
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    const int e0 = first + (E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c);
+    uint16_t v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int i = e0 + k % 8 + (k / 8) * (E >= 16 ? E / 2 : 8);
+      const __half* src = i < r ? wp + i * D : dp + (i - r) * D;
+      v[k] = 0;
+      if (i < n) v[k] = __half_as_ushort(*src);
+    }
+    const uint4 x = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
+                               v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+    const uint4 y = make_uint4(v[8] | (uint32_t)v[9] << 16, v[10] | (uint32_t)v[11] << 16,
+                               v[12] | (uint32_t)v[13] << 16, v[14] | (uint32_t)v[15] << 16);
+    uint32_t q[8];
+    tc_raw_pairs<E>(x, y, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // exponent bits all set
+      const uint32_t f = ((q[j] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+      odd |= f;
+      q[j] &= ~((f >> 15) * 0xFFFFu);
+    }
+    tc_st8(t_hi + 8 * c, q);
+  }
+  return odd != 0;
 }
 
 // Whether rows row0 .. row0 + 15 see drafted token `node`, one bit each.
@@ -458,6 +552,11 @@ struct TcSeg {
   int r, row0, nrows;  // nrows: rows of this block that exist
   bool whole, ok;
 };
+// A block's walk over its range: sequence, KV head, row block, tile, tiles left.
+struct TcWalk {
+  long long b, left;
+  int h, rb, t;
+};
 
 template <int D, int BITS, typename M>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, TreePlan p) {
@@ -466,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   constexpr int KS = D / 16;  // k-slices of the scores
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ TcBars bars;
-  __shared__ TreeAt s_at;
+  __shared__ TcWalk s_walk;
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
   __shared__ int s_poison[2];   // [segment parity]
@@ -474,9 +573,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   volatile int* dead = &s_dead;
   // what a whole warp shares is broadcast, so that it lives in uniform registers
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
+  const int nr = p.rb, nch = nr / 16;
+  const bool two = nr <= 64;  // two streams: tiles in turn, each its S and O
 
   // ---- set-up
-  if (warp == 20) {
+  if (warp == 22) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      tc_smem(&s_tmem))
                  : "memory");
@@ -484,28 +586,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   }
   if (warp == 0) {
     TreeAt at = tree_find(a, p, 0);
-    const long long total = at.total;
-    at = tree_find(a, p, blockIdx.x * tree_range(p, total));
-    at.total = total;
-    if (lane == 0) s_at = at;
+    const long long total = at.total, W = tree_range(p, total), x = blockIdx.x * W;
+    at = tree_find(a, p, x);
+    if (lane == 0) {
+      s_walk.left = x < total ? min(W, total - x) : 0;
+      s_walk.b = at.b;
+      if (x < total) {
+        const long long ut = tree_seq(a, p, at.b).ut, grp = at.rem / ut;
+        s_walk.t = (int)(at.rem - grp * ut);
+        s_walk.h = (int)(grp / p.n_rb);
+        s_walk.rb = (int)(grp - (long long)s_walk.h * p.n_rb);
+      }
+    }
   }
   if (tid == 32) {
     s_dead = 0;
     for (int i = 0; i < 2; ++i) s_poison[i] = 0;
     for (int i = 0; i < 3; ++i) {
       tc_bar_init(&bars.raw_full[i], 1);
-      tc_bar_init(&bars.raw_empty[i], 12);
+      tc_bar_init(&bars.raw_empty[i], 14);
     }
     tc_bar_init(&bars.k_full, 4);
     tc_bar_init(&bars.v_full, 4);
+    const int soft = two ? 4 : 8;  // softmax warps of a tile
     for (int i = 0; i < 2; ++i) {
       tc_bar_init(&bars.s_full[i], 1);
-      tc_bar_init(&bars.s_empty[i], 8);
-      tc_bar_init(&bars.p_full[i], 8);
+      tc_bar_init(&bars.s_empty[i], soft);
+      tc_bar_init(&bars.p_full[i], soft);
       tc_bar_init(&bars.pv_done[i], 1);
       tc_bar_init(&bars.h_done[i], 4);
-      tc_bar_init(&bars.z_full[i], 4);
-      tc_bar_init(&bars.z_empty[i], 8);
+      tc_bar_init(&bars.z_full[i], 2);
+      tc_bar_init(&bars.z_empty[i], soft);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -515,113 +626,95 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-  const long long total = s_at.total, W = tree_range(p, total);
-  long long x = blockIdx.x * W;
-  const long long end = x + W < total ? x + W : total;
-  long long sb = s_at.b, rem = s_at.rem;
-  const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
-  const int nr = p.rb, nch = nr / 16;
-  const bool s2 = nr <= 64;  // two S buffers
+  TcWalk walk = s_walk;
 
-  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);
-  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);
-  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);
-  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);
+  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // [stream][64] or [128]
+  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // [tile parity][128]
+  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [tile parity][group][128]
+  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // rows as m_s, 8 each
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
-  // counters of this block: tiles, and tiles that went through the ring; the
-  // copying warp runs ahead of the others, over its own walk of the segments
-  int it0 = 0, st0 = 0;
-
-  auto next_seg = [&](long long& xx, long long& bb, long long& rr, TcSeg& g) {
-    TreeSeq q = tree_seq(a, p, bb);
-    const long long gpb = (long long)a.Hkv * p.n_rb;
-    while (rr >= gpb * q.ut) {
-      rr -= gpb * q.ut;
-      ++bb;
-      q = tree_seq(a, p, bb);
-    }
-    const int ut = (int)q.ut, grp = (int)(rr / ut), left = (int)min(end - xx, 1LL << 30);
-    g.t0 = (int)(rr - (long long)grp * ut);
-    g.nt = ut - g.t0 < left ? ut - g.t0 : left;
-    g.b = bb;
-    g.unit = bb * a.Hkv + grp / p.n_rb;
-    g.row0 = grp % p.n_rb * p.rb;
-    g.nrows = rows - g.row0 < nr ? rows - g.row0 : nr;
+  // A range ends within a group at most at its own end: segments after the first
+  // begin with a group.
+  auto next_seg = [&](TcWalk& w) -> TcSeg {
+    const TreeSeq q = tree_seq(a, p, w.b);
+    TcSeg g;
+    g.t0 = w.t;
+    g.nt = (int)min(q.ut - w.t, w.left);
+    g.b = w.b;
+    g.unit = w.b * a.Hkv + w.h;
+    g.row0 = w.rb * nr;
+    g.nrows = min(rows - g.row0, nr);
     g.n_q = q.n_q;
     g.r = q.r;
     g.ok = q.ok;
     g.tq = q.ok ? (int)((q.n_q + kTcTile - 1) / kTcTile) : 0;
-    g.whole = g.t0 == 0 && g.nt == ut;
-    xx += g.nt;
-    rr += g.nt;
+    g.whole = w.t == 0 && g.nt == q.ut;
+    w.left -= g.nt;
+    w.t = 0;
+    if (++w.rb == p.n_rb) {
+      w.rb = 0;
+      if (++w.h == a.Hkv) {
+        w.h = 0;
+        ++w.b;
+      }
+    }
+    return g;
   };
 
-  if (warp == 21) {
-    // ==== copies: runs ahead over all segments; the ring alone holds it back
-    long long xx = x, bb = sb, rr = rem;
+  if (warp == 24) {
+    // ==== copies: runs ahead over all segments; the ring alone holds it back.
+    // Lane i < 4 copies subtile i.
     int st = 0;
-    if (lane == 0) {
-      while (xx < end) {
-        TcSeg g;
-        next_seg(xx, bb, rr, g);
-        if (!g.ok) continue;
-        for (int t = g.t0; t < g.t0 + g.nt && t < g.tq; ++t, ++st) {
-          const int s = st % Ge::NST;
-          if (st >= Ge::NST) tc_wait(&bars.raw_empty[s], st / Ge::NST - 1, dead);
-          if (*dead) break;
+    const long long Ts = store_tokens(a.c);
+    while (walk.left > 0) {
+      const TcSeg g = next_seg(walk);
+      for (int t = g.t0; t < min(g.t0 + g.nt, g.tq); ++t, ++st) {
+        const int s = st % Ge::NST;
+        if (st >= Ge::NST) tc_wait(&bars.raw_empty[s], st / Ge::NST - 1, dead);
+        const long long tile = t * 4LL + lane;
+        long long su = 0, stl = 0;
+        const bool have = lane < 4 && tile < g.n_q / kTile && store_tile(a.c, g.unit, tile, &su, &stl);
+        const int n = __popc(__ballot_sync(0xffffffffu, have));
+        uint64_t* fb = &bars.raw_full[s];
+        if (lane == 0) tc_expect(fb, n * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM));
+        __syncwarp();
+        if (have && !*dead) {
+          using Lt = Layout<D, BITS>;
           unsigned char* dst = sm + Ge::S_RING + s * Ge::STAGE;
-          const long long left = (g.n_q - (long long)t * kTcTile) / kTile;
-          const int ns = left < 4 ? (int)left : 4;
-          const long long Ts = store_tokens(a.c);
-          uint32_t bytes = 0;
-          for (int pass = 0; pass < 2; ++pass) {
-            // contiguous stores: all subtiles at once; paged: one by one
-            const int step = a.c.bt ? 1 : ns;
-            for (int i = 0; i < ns; i += step) {
-              long long su, stl;
-              if (!store_tile(a.c, g.unit, t * 4LL + i, &su, &stl)) continue;
-              if (pass == 0) {
-                bytes += step * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM);
-                continue;
-              }
-              using Lt = Layout<D, BITS>;
-              const unsigned char* kc = (const unsigned char*)(a.c.k_codes + su * Lt::k_codes_unit(Ts)) + stl * Ge::KC;
-              const unsigned char* ks = (const unsigned char*)a.c.k_scale + su * Lt::k_meta_unit(Ts) * sizeof(M) + stl * Ge::KM;
-              const unsigned char* kz = (const unsigned char*)a.c.k_zero + su * Lt::k_meta_unit(Ts) * sizeof(M) + stl * Ge::KM;
-              const unsigned char* vc = (const unsigned char*)(a.c.v_codes + su * Lt::v_codes_unit(Ts)) + stl * Ge::VC;
-              const unsigned char* vs = (const unsigned char*)a.c.v_scale + su * Lt::v_meta_unit(Ts) * sizeof(M) + stl * Ge::VM;
-              const unsigned char* vz = (const unsigned char*)a.c.v_zero + su * Lt::v_meta_unit(Ts) * sizeof(M) + stl * Ge::VM;
-              uint64_t* fb = &bars.raw_full[s];
-              tc_copy(dst + Ge::O_KC + i * Ge::KC, kc, step * Ge::KC, fb);
-              tc_copy(dst + Ge::O_KS + i * Ge::KM, ks, step * Ge::KM, fb);
-              tc_copy(dst + Ge::O_KZ + i * Ge::KM, kz, step * Ge::KM, fb);
-              tc_copy(dst + Ge::O_VC + i * Ge::VC, vc, step * Ge::VC, fb);
-              tc_copy(dst + Ge::O_VS + i * Ge::VM, vs, step * Ge::VM, fb);
-              tc_copy(dst + Ge::O_VZ + i * Ge::VM, vz, step * Ge::VM, fb);
-            }
-            if (pass == 0) tc_expect(&bars.raw_full[s], bytes);
-          }
+          const long long km = su * Lt::k_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::KM;
+          const long long vm = su * Lt::v_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::VM;
+          tc_copy(dst + Ge::O_KC + lane * Ge::KC,
+                  (const char*)(a.c.k_codes + su * Lt::k_codes_unit(Ts)) + stl * Ge::KC, Ge::KC, fb);
+          tc_copy(dst + Ge::O_KS + lane * Ge::KM, (const char*)a.c.k_scale + km, Ge::KM, fb);
+          tc_copy(dst + Ge::O_KZ + lane * Ge::KM, (const char*)a.c.k_zero + km, Ge::KM, fb);
+          tc_copy(dst + Ge::O_VC + lane * Ge::VC,
+                  (const char*)(a.c.v_codes + su * Lt::v_codes_unit(Ts)) + stl * Ge::VC, Ge::VC, fb);
+          tc_copy(dst + Ge::O_VS + lane * Ge::VM, (const char*)a.c.v_scale + vm, Ge::VM, fb);
+          tc_copy(dst + Ge::O_VZ + lane * Ge::VM, (const char*)a.c.v_zero + vm, Ge::VM, fb);
         }
       }
-      // no copy may still be under way when the block ends (bounded again)
-      int never = 0;
-      for (int i = st > Ge::NST ? st - Ge::NST : 0; i < st; ++i)
-        tc_wait(&bars.raw_full[i % Ge::NST], i / Ge::NST, &never);
     }
+    // no copy may still be under way when the block ends (bounded again; a dead
+    // block has stages without copies, whose waits run out)
+    int never = 0;
+    for (int i = max(st - Ge::NST, 0); i < st; ++i)
+      tc_wait(&bars.raw_full[i % Ge::NST], i / Ge::NST, &never);
     __syncwarp();
   }
 
   // ==== segments
-  for (int seg = 0; warp < 21 && x < end; ++seg) {
-    TcSeg g;
-    next_seg(x, sb, rem, g);
+  // counters of this block: tiles, and tiles that went through the ring
+  int it0 = 0, st0 = 0;
+  for (int seg = 0; warp < 24 && walk.left > 0; ++seg) {
+    const TcSeg g = next_seg(walk);
+    const int t1 = g.t0 + g.nt;
     // ---- start of a segment: queries, mask, references, pages
     if (tid == 0) s_odd = 0;
     if (!g.ok) s_poison[seg & 1] = 1;
     if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
-      const long long i1 =
-          (g.t0 + g.nt) * 4LL < g.n_q / kTile ? (g.t0 + g.nt) * 4LL : g.n_q / kTile;
+      const long long i1 = min(t1 * 4LL, g.n_q / kTile);
+#pragma unroll 1
       for (long long i = g.t0 * 4LL + tid; i < i1; i += kTcThreads - 32) {
         long long su, stl;
         if (!store_tile(a.c, g.unit, i, &su, &stl)) s_poison[seg & 1] = 1;
@@ -629,523 +722,461 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     }
     {
       const __half* qp = static_cast<const __half*>(a.q) + (g.unit * rows + g.row0) * D;
+      const bool al = ((uintptr_t)qp & 15) == 0;
       // operand order along channels; rows that do not exist are 0
-      for (int i = tid; i < nr * D; i += kTcThreads - 32) {
-        const int row = i / D, ch = i % D, k = tc_pos<E>(ch);
-        const __half v = row < g.nrows ? qp[(long long)row * D + ch] : __ushort_as_half(0);
-        *reinterpret_cast<__half*>(sm + Ge::S_Q + row / 8 * (D * 16) + k / 8 * 128 + row % 8 * 16 +
-                                   k % 8 * 2) = v;
+#pragma unroll 1
+      for (int i = tid; i < nr * (D / 8); i += kTcThreads - 32) {
+        const int row = i / (D / 8), c0 = i % (D / 8) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < g.nrows) x = tc_raw8(qp + row * D + c0, al);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        unsigned char* q = sm + Ge::S_Q + row / 8 * (D * 16) + row % 8 * 16;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = tc_pos<E>(c0 + e);
+          *reinterpret_cast<uint16_t*>(q + k / 8 * 128 + k % 8 * 2) = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+        }
       }
+#pragma unroll 1
       for (int i = tid; i < a.N * mw; i += kTcThreads - 32)
-        mask_s[i / mw * 8 + i % mw] = a.mask[(g.b * a.N) * mw + i];
-      for (int i = tid; i < 128; i += kTcThreads - 32) m_s[i] = kTcNone;
+        mask_s[i / mw * 8 + i % mw] = a.mask[g.b * a.N * mw + i];
+      if (tid < 128) m_s[tid] = kTcNone;
     }
     tc_fence_smem();
     tc_sync_segment();
 
-    if (g.ok) {
-      if (warp < 4) {
-        // ==== keys: lane = token of subtile `warp`
-        const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
-        __half* sc = reinterpret_cast<__half*>(sm + Ge::S_KSC + warp * D * 4);  // hi[D], lo[D]
-        int it = it0, st = st0;
-        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          if (t < g.tq) {
-            const int s = st % Ge::NST;
-            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-            const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-            const M* ks = reinterpret_cast<const M*>(stg + Ge::O_KS + warp * Ge::KM);
-            __syncwarp();
-#pragma unroll
-            for (int c = lane; c < D; c += 32) {
-              __half hi, lo;
-              tc_split(to_f32(ks[c]), &hi, &lo);
-              sc[tc_pos<E>(c)] = hi;
-              sc[D + tc_pos<E>(c)] = lo;
-            }
-            __syncwarp();
-            if (it > 0) tc_wait(&bars.s_full[(it - 1) & 1], (it - 1) >> 1, dead);
-            tc_fence_after();
-            tc_unpack<BITS, D>(
-                t_lane + kTKhi, t_lane + kTKlo,
-                reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + warp * Ge::KC) + lane * WK, 1, sc);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              tc_arrive(&bars.raw_empty[s]);
-              tc_arrive(&bars.k_full);
-            }
-            ++st;
-          } else {
-            // raw tokens: the window, then the drafted ones; halved like s
-            const int i = (t - g.tq) * kTcTile + warp * 32 + lane;
-            const __half* src = nullptr;
-            if (i < g.r)
-              src = static_cast<const __half*>(a.c.k_res) + (g.unit * a.c.R + i) * D;
-            else if (i < g.r + a.N)
-              src = static_cast<const __half*>(a.k) + (g.unit * a.N + (i - g.r)) * D;
-            const bool al = ((uintptr_t)src & 15) == 0;
-            if (it > 0) tc_wait(&bars.s_full[(it - 1) & 1], (it - 1) >> 1, dead);
-            tc_fence_after();
-            // 16 places of the operand order: two runs of 8 channels, E / 2 apart (or
-            // two blocks of 8 channels)
-#pragma unroll 2
-            for (int c = 0; c < D / 16; ++c) {
-              const int e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
-              uint4 x = make_uint4(0, 0, 0, 0), y = x;
-              if (src != nullptr) {
-                x = tc_raw8(src + e0, al);
-                y = tc_raw8(src + e0 + (E >= 16 ? E / 2 : 8), al);
-              }
-              uint32_t r[8];
-              if constexpr (E >= 16) {  // (x_j, y_j)
-                r[0] = __byte_perm(x.x, y.x, 0x5410);
-                r[1] = __byte_perm(x.x, y.x, 0x7632);
-                r[2] = __byte_perm(x.y, y.y, 0x5410);
-                r[3] = __byte_perm(x.y, y.y, 0x7632);
-                r[4] = __byte_perm(x.z, y.z, 0x5410);
-                r[5] = __byte_perm(x.z, y.z, 0x7632);
-                r[6] = __byte_perm(x.w, y.w, 0x5410);
-                r[7] = __byte_perm(x.w, y.w, 0x7632);
-              } else {  // (x_j, x_j+4), then y
-                r[0] = __byte_perm(x.x, x.z, 0x5410);
-                r[1] = __byte_perm(x.x, x.z, 0x7632);
-                r[2] = __byte_perm(x.y, x.w, 0x5410);
-                r[3] = __byte_perm(x.y, x.w, 0x7632);
-                r[4] = __byte_perm(y.x, y.z, 0x5410);
-                r[5] = __byte_perm(y.x, y.z, 0x7632);
-                r[6] = __byte_perm(y.y, y.w, 0x5410);
-                r[7] = __byte_perm(y.y, y.w, 0x7632);
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
-              tc_st8(t_lane + kTKhi + 8 * c, r);
-            }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc_arrive(&bars.k_full);
-          }
-        }
-      } else if (warp < 8) {
-        // ==== values: lane = channel of group `vw`
-        const int vw = warp - 4;
-        const int ch = vw * 32 + lane;
-        const uint32_t t_lane = tmem + ((uint32_t)(vw * 32) << 16);
-        __half* sc = reinterpret_cast<__half*>(sm + Ge::S_VSC + vw * 128 * 4);  // hi[128], lo[128]
-        int it = it0, st = st0;
-        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          if (t < g.tq) {
-            const int s = st % Ge::NST;
-            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-            if (vw < NJ) {
-              const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-              const M* vs = reinterpret_cast<const M*>(stg + Ge::O_VS);
-              const long long n = g.n_q - (long long)t * kTcTile;  // tokens that exist
-              __syncwarp();
-#pragma unroll
-              for (int k = lane; k < 128; k += 32) {
-                __half hi = __ushort_as_half(0), lo = hi;
-                if (k < n) tc_split(to_f32(vs[k * NJ + vw]), &hi, &lo);
-                sc[tc_pos<E>(k)] = hi;
-                sc[128 + tc_pos<E>(k)] = lo;
-              }
-              __syncwarp();
-              if (it > 0) tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
-              tc_fence_after();
-              tc_unpack<BITS, 128>(t_lane + kTVhi, t_lane + kTVlo,
-                                   reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + ch, D, sc);
-              tc_wait_st();
-              tc_fence_before();
-            } else if (it > 0) {
-              tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
-            }
-            __syncwarp();
-            if (lane == 0) {
-              tc_arrive(&bars.raw_empty[s]);
-              tc_arrive(&bars.v_full);
-            }
-            ++st;
-          } else {
-            if (it > 0) tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
-            tc_fence_after();
-            if (vw < NJ) {
-              const int first = (t - g.tq) * kTcTile, n = g.r + a.N;
-              const __half* wp = static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D + ch;
-              const __half* dp = static_cast<const __half*>(a.v) + g.unit * a.N * D + ch;
-              uint32_t odd = 0;
-#pragma unroll 1
-              for (int c0 = 0; c0 < 128; c0 += 16) {
-                uint16_t v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const int i = first + tc_elem<E>(c0 + k);
-                  v[k] = i < n ? __half_as_ushort(i < g.r ? wp[i * D] : dp[(i - g.r) * D]) : 0;
-                }
-                uint32_t r[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  uint32_t u = v[2 * j] | (uint32_t)v[2 * j + 1] << 16;
-                  // infinities and NaN join at the segment's end, for the rows that
-                  // attend to them
-                  const uint32_t x = (((u & 0x7C007C00u) + 0x04000400u) & 0x80008000u);
-                  odd |= x;
-                  u &= ~((x >> 15) * 0xFFFFu);
-                  r[j] = tc_hmul2(u, 0x38003800u);
-                }
-                tc_st8(t_lane + kTVhi + c0 / 2, r);
-              }
-              if (odd) s_odd = 1;
-              tc_wait_st();
-              tc_fence_before();
-            }
-            __syncwarp();
-            if (lane == 0) tc_arrive(&bars.v_full);
-          }
-        }
-      } else if (warp < 16) {
-        // ==== softmax: group sg takes the 16-row chunks sg, sg + 2, ..; lane = token
-        const int sg = (warp - 8) >> 2, sw = warp & 3;
-        const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16);
-        float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + sw * 128;
-        float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + sw * 128;
-        const float c1 = 2.0f * a.qscale;
-        const int pk = tc_pos<E>(sw * 32 + lane);  // the token's place in the second product
-        int it = it0;
-        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          const int par = it & 1;
-          const bool raw = t >= g.tq;
-          const uint32_t t_s = t_lane + kTS + (s2 ? 64 * par : 0);
-          // the token of this lane: in the cache (all rows see it), drafted, or none
-          const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
-          bool in = raw ? i < g.r : i < g.n_q;
-          const int node = raw && i >= g.r && i < g.r + a.N ? (int)(i - g.r) : -1;
-          auto seen = [&](int ch) -> uint32_t {  // 16 bits, one for each row of chunk ch
-            return in ? 0xFFFFu : (node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + ch * 16, a.N));
-          };
-          // what the products two tiles ago read (weights, factors) may be written again
-          if (it >= 2) {
-            tc_wait(&bars.pv_done[par], (it >> 1) - 1, dead);
-            tc_wait(&bars.h_done[par], (it >> 1) - 1, dead);
-          }
-          tc_wait(&bars.z_full[par], it >> 1, dead);
-          for (int e = lane; e < nr; e += 32)
-            if (((e >> 4) & 1) == sg) off_s[e] = m_s[e] - zk_s[(par * 4 + sw) * 128 + e];
+    if (!g.ok) {
+    } else if (warp < 8) {
+      // ==== keys (lane = token of subtile w) and values (lane = channel of group w),
+      // by one code
+      const bool vals = warp >= 4;
+      const int w = warp & 3, n_codes = vals ? 128 : D;
+      const uint32_t t_hi = tmem + ((uint32_t)(w * 32) << 16) + (vals ? kTVhi : kTKhi);
+      __half* sc = reinterpret_cast<__half*>(vals ? sm + Ge::S_VSC + w * 512 : sm + Ge::S_KSC + w * D * 4);
+      const int o_sc = vals ? Ge::O_VS + w * (int)sizeof(M) : Ge::O_KS + w * Ge::KM;
+      const int o_w = vals ? Ge::O_VC + (w * 32 + lane) * 4 : Ge::O_KC + w * Ge::KC + lane * WK * 4;
+      const int s_str = vals ? NJ : 1, w_str = vals ? D : 1;
+      uint64_t* done = vals ? bars.pv_done : bars.s_full;
+      uint64_t* full = vals ? &bars.v_full : &bars.k_full;
+      const bool act = !vals || w < NJ;
+      int it = it0, st = st0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int s = st % Ge::NST;
+        const bool raw = t >= g.tq;
+        const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+        if (!raw) {
+          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+          const M* src = reinterpret_cast<const M*>(stg + o_sc);
+          // tokens that exist (values of others must not be NaN: weight 0 times them)
+          const int n = vals ? (int)min(g.n_q - (long long)t * kTcTile, 128LL) : D;
           __syncwarp();
-          tc_wait(&bars.s_full[par], it >> 1, dead);
-          tc_fence_after();
-          // ---- does any score exceed its row's reference by too much?
-          float over = -__builtin_huge_valf();
-          for (int ch = sg; ch < nch; ch += 2) {
-            float v[16];
-            tc_ld16(t_s + ch * 16, v);
-            const uint32_t sees = seen(ch);
+#pragma unroll 2
+          for (int c = lane; c < n_codes; c += 32) {
+            __half hi = __ushort_as_half(0), lo = hi;
+            if (act && c < n) tc_split(to_f32(src[c * s_str]), &hi, &lo);
+            sc[tc_pos<E>(c)] = hi;
+            sc[n_codes + tc_pos<E>(c)] = lo;
+          }
+          __syncwarp();
+        }
+        if (it > 0) tc_wait(&done[(it - 1) & 1], (it - 1) >> 1, dead);
+        tc_fence_after();
+        if (!act) {
+        } else if (!raw) {
+          tc_unpack<BITS>(t_hi, reinterpret_cast<const uint32_t*>(stg + o_w), w_str, sc, n_codes);
+        } else if (!vals) {
+          // raw tokens: the window, then the drafted ones; halved like s
+          const int i = (t - g.tq) * kTcTile + w * 32 + lane;
+          const __half* src = nullptr;
+          if (i < g.r)
+            src = static_cast<const __half*>(a.c.k_res) + (g.unit * a.c.R + i) * D;
+          else if (i < g.r + a.N)
+            src = static_cast<const __half*>(a.k) + (g.unit * a.N + (i - g.r)) * D;
+          tc_raw_keys<D, E>(t_hi, src);
+        } else {
+          const int ch = w * 32 + lane;
+          const bool odd = tc_raw_values<D, E>(
+              t_hi, static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D + ch,
+              static_cast<const __half*>(a.v) + g.unit * a.N * D + ch, (t - g.tq) * kTcTile, g.r,
+              g.r + a.N);
+          if (odd) s_odd = 1;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!raw) tc_arrive(&bars.raw_empty[s]);
+          tc_arrive(full);
+        }
+        st += !raw;
+      }
+    } else if (warp < 16) {
+      // ==== softmax: lane = token.  Two streams: group sg takes the tiles of parity
+      // sg, all rows; else 16-row chunks sg, sg + 2, .. of each tile
+      const int sg = (warp - 8) >> 2, sw = warp & 3;
+      const int ch0 = two ? 0 : sg, chs = two ? 1 : 2, ro = two ? 64 * sg : 0;
+      const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16);
+      float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + sw * 128 + ro;
+      float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + ro;  // + 128 warp
+      float* mr_s = m_s + ro;
+      const float c1 = 2.0f * a.qscale;
+      const int pk = tc_pos<E>(sw * 32 + lane);  // the token's place in the second product
+      int it = it0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int par = it & 1;
+        if (two && par != sg) continue;
+        const bool raw = t >= g.tq;
+        const uint32_t t_s = t_lane + kTS + (two ? 64 * par : 0);
+        const float* zk = zk_s + (par * 4 + sw) * 128;
+        // the token of this lane: in the cache (all rows see it), drafted, or none
+        const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
+        const bool in = raw ? i < g.r : i < g.n_q;
+        const int node = raw && i >= g.r && i < g.r + a.N ? (int)(i - g.r) : -1;
+        auto seen = [&](int ch) -> uint32_t {  // 16 bits, one for each row of chunk ch
+          return in ? 0xFFFFu : (node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + ch * 16, a.N));
+        };
+        // what the products two tiles ago read (weights, factors) may be written again
+        if (it >= 2) {
+          tc_wait(&bars.pv_done[par], (it >> 1) - 1, dead);
+          tc_wait(&bars.h_done[par], (it >> 1) - 1, dead);
+        }
+        tc_wait(&bars.z_full[par], it >> 1, dead);
+        auto offsets = [&]() {
+          for (int e = lane; e < nr; e += 32)
+            if (two || ((e >> 4) & 1) == sg) off_s[e] = mr_s[e] - zk[e];
+          __syncwarp();
+        };
+        offsets();
+        tc_wait(&bars.s_full[par], it >> 1, dead);
+        tc_fence_after();
+        // ---- does any score exceed its row's reference by too much?
+        float over = -__builtin_huge_valf();
+        for (int ch = ch0; ch < nch; ch += chs) {
+          float v[16];
+          tc_ld16(t_s + ch * 16, v);
+          const uint32_t sees = seen(ch);
 #pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
-              const float oo[4] = {o.x, o.y, o.z, o.w};
+          for (int e4 = 0; e4 < 4; ++e4) {
+            const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
+            const float oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float d = fmaf(v[4 * e4 + e], c1, -oo[e]);
+              over = fmaxf(over, (sees >> (4 * e4 + e)) & 1u ? d : over);
+            }
+          }
+        }
+        const bool need = tc_group_any(sg, over > kTcSlack);
+        if (need) {
+          // ---- new references: each warp's maxima, joined
+#pragma unroll 1
+          for (int ch = ch0; ch < nch; ch += chs) {
+            const uint32_t sees = seen(ch);
+#pragma unroll 1
+            for (int e4 = 0; e4 < 16; e4 += 4) {
+              float v[4];
+              tc_ld4(t_s + ch * 16 + e4, v);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float d = fmaf(v[4 * e4 + e], c1, -oo[e]);
-                over = fmaxf(over, (sees >> (4 * e4 + e)) & 1u ? d : over);
+                const int row = ch * 16 + e4 + e;
+                const float d =
+                    warp_max((sees >> (e4 + e)) & 1u ? fmaf(v[e], c1, zk[row]) : kTcNone);
+                if (lane == 0) wmax_s[sw * 128 + row] = d;
               }
             }
           }
-          const bool need = tc_group_any(sg, over > kTcSlack);
-          if (need) {
-            // ---- new references: each warp's maxima, joined
-            for (int ch = sg; ch < nch; ch += 2) {
-              float v[16];
-              tc_ld16(t_s + ch * 16, v);
-              const uint32_t sees = seen(ch);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int row = ch * 16 + e;
-                float d = (sees >> e) & 1u ? fmaf(v[e], c1, zk_s[(par * 4 + sw) * 128 + row]) : kTcNone;
-                d = warp_max(d);
-                if (lane == e) wmax_s[row] = d;
-              }
-            }
-            tc_group(sg);
-            const float* wm = reinterpret_cast<const float*>(sm + Ge::S_WMAX);
-            for (int e = (sw * 32 + lane); e < nr; e += 128) {
-              if (((e >> 4) & 1) != sg) continue;
-              const float old = m_s[e];
-              const float mn = fmaxf(fmaxf(fmaxf(wm[e], wm[128 + e]), fmaxf(wm[256 + e], wm[384 + e])), old);
-              f_s[par * 128 + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
-              m_s[e] = mn;
-            }
-            tc_group(sg);
-            for (int e = lane; e < nr; e += 32)
-              if (((e >> 4) & 1) == sg) off_s[e] = m_s[e] - zk_s[(par * 4 + sw) * 128 + e];
-            if (t > g.t0) {
-              // ---- accumulators so far, once the product before this one is done
-              tc_wait(&bars.pv_done[(it - 1) & 1], (it - 1) >> 1, dead);
-              tc_fence_after();
-              for (int ch = sg; ch < nch; ch += 2) {
-                float v[16];
-                tc_ld16(t_lane + kTO + ch * 16, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= f_s[par * 128 + ch * 16 + e];
-                tc_st16(t_lane + kTO + ch * 16, v);
-              }
-              tc_wait_st();
-            }
-            __syncwarp();
+          tc_group(sg);
+          const int e = sw * 32 + lane;  // a row of each thread
+          if (e < nr && (two || ((e >> 4) & 1) == sg)) {
+            const float old = mr_s[e];
+            const float mn = fmaxf(fmaxf(fmaxf(wmax_s[e], wmax_s[128 + e]),
+                                         fmaxf(wmax_s[256 + e], wmax_s[384 + e])),
+                                   old);
+            f_s[par * 128 + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
+            mr_s[e] = mn;
           }
-          if (lane == 0 && sw == 0)
-            for (int ch = sg; ch < nch; ch += 2) s_resc[par][ch] = need;
-          // ---- weights
-          unsigned char* pb = sm + Ge::S_P + par * 128 * 128 * 2 + pk / 8 * 128 + pk % 8 * 16;
-          for (int ch = sg; ch < nch; ch += 2) {
-            float v[16];
-            tc_ld16(t_s + ch * 16, v);
-            const uint32_t sees = seen(ch);
-            uint32_t w[8];
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
-              const float oo[4] = {o.x, o.y, o.z, o.w};
-              float e[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                e[k] = tc_ex2(fmaf(v[4 * e4 + k], c1, -oo[k]));
-                if (!((sees >> (4 * e4 + k)) & 1u)) e[k] = 0.0f;
+          tc_group(sg);
+          offsets();
+          if (t - g.t0 >= (two ? 2 : 1)) {
+            // ---- accumulators so far, once the product before this one is done (the
+            // stream's last one was waited for above)
+            if (!two) tc_wait(&bars.pv_done[par ^ 1], (it - 1) >> 1, dead);
+            tc_fence_after();
+#pragma unroll 1
+            for (int ch = ch0; ch < nch; ch += chs)
+#pragma unroll 1
+              for (int e4 = ch * 16; e4 < ch * 16 + 16; e4 += 4) {
+                const uint32_t t_o = t_lane + kTO + (two ? 64 * par : 0) + e4;
+                const float4 f = *reinterpret_cast<const float4*>(f_s + par * 128 + e4);
+                float v[4];
+                tc_ld4(t_o, v);
+                v[0] *= f.x;
+                v[1] *= f.y;
+                v[2] *= f.z;
+                v[3] *= f.w;
+                tc_st4(t_o, v);
               }
-              const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
-              w[2 * e4] = *reinterpret_cast<const uint32_t*>(&h0);
-              w[2 * e4 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-            }
-            *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+            tc_wait_st();
           }
-          tc_fence_before();
-          tc_fence_smem();
           __syncwarp();
-          if (lane == 0) {
-            tc_arrive(&bars.s_empty[par]);
-            tc_arrive(&bars.z_empty[par]);
-            tc_arrive(&bars.p_full[par]);
-          }
         }
-      } else if (warp < 20) {
-        // ==== zeros' products and the sums: chunks hw, hw + 4 of 16 rows
-        const int hw = warp - 16;
-        float acc[2][4];
+        if (lane == 0 && sw == 0)
+          for (int ch = ch0; ch < nch; ch += chs) s_resc[par][ch] = need;
+        // ---- weights
+        unsigned char* pb = sm + Ge::S_P + par * 128 * 128 * 2 + pk / 8 * 128 + pk % 8 * 16;
+        for (int ch = ch0; ch < nch; ch += chs) {
+          float v[16];
+          tc_ld16(t_s + ch * 16, v);
+          const uint32_t sees = seen(ch);
+          uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int e4 = 0; e4 < 4; ++e4) {
+            const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
+            const float oo[4] = {o.x, o.y, o.z, o.w};
+            float e[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-        const int n8 = lane >> 2, kq = (lane & 3) * 2, ht = hw * 32 + lane;
-        __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
-        int st = st0;
-        // the zeros' part of tile t: their products with the queries for its scores,
-        // and the values' zeros set out for its sums
-        auto zeros = [&](int t, int it) {
-          const int par = it & 1;
-          __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
-          const bool raw = t >= g.tq;
+            for (int k = 0; k < 4; ++k) {
+              e[k] = tc_ex2(fmaf(v[4 * e4 + k], c1, -oo[k]));
+              if (!((sees >> (4 * e4 + k)) & 1u)) e[k] = 0.0f;
+            }
+            const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
+            w[2 * e4] = *reinterpret_cast<const uint32_t*>(&h0);
+            w[2 * e4 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          }
+          *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        tc_fence_before();
+        tc_fence_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc_arrive(&bars.p_full[par]);
+          tc_arrive(&bars.s_empty[par]);
+          tc_arrive(&bars.z_empty[par]);
+        }
+      }
+    } else if (warp < 18) {
+      // ==== sum_d q_d z_gd of a tile's four groups: 16-row chunks zw, zw + 2, ..
+      const int zw = warp - 16, zt = zw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
+      int it = it0, st = st0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int par = it & 1;
+        const bool raw = t >= g.tq;
+        __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH) + par * 4 * Ge::ZLD;
+        if (!raw) {
+          const int s = st % Ge::NST;
+          const M* kz = reinterpret_cast<const M*>(sm + Ge::S_RING + s * Ge::STAGE + Ge::O_KZ);
+          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+#pragma unroll
+          for (int j = 0; j < 4 * D / 64; ++j) {
+            const int i = zt + 64 * j;
+            zh[i / D * Ge::ZLD + tc_pos<E>(i % D)] = __float2half_rn(to_f32(kz[i]));
+          }
+          tc_pair_sync();
+          if (lane == 0) tc_arrive(&bars.raw_empty[s]);
+          ++st;
+        }
+        if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
+        // lane n8 of a column reads group n8's row; columns 4 .. 7 are read by nobody
+        const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
+#pragma unroll 1
+        for (int ch = zw; ch < nch; ch += 2) {
+          float zc[4] = {0.f, 0.f, 0.f, 0.f};
           if (!raw) {
-            const int s = st % Ge::NST;
-            const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-            const long long n = g.n_q - (long long)t * kTcTile;
-            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-            const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
-            const M* vz = reinterpret_cast<const M*>(stg + Ge::O_VZ);
-#pragma unroll 2
-            for (int i = ht; i < 4 * D; i += 128)
-              zh[i / D * Ge::ZLD + tc_pos<E>(i % D)] = __float2half_rn(to_f32(kz[i]));
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              zv[j * Ge::ZLD + tc_pos<E>(ht)] =
-                  ht < n ? __float2half_rn(to_f32(vz[ht * NJ + j])) : __ushort_as_half(0);
-            tc_named<4>();
-            if (lane == 0) tc_arrive(&bars.raw_empty[s]);
-            ++st;
-          } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ht] = __ushort_as_half(0);
-            tc_named<4>();
-          }
-          if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
-          float zc[2][4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zc[k][e] = 0.f;
-          if (!raw && hw < nch) {
-#pragma unroll 2
+            // rows 16 ch + (lane % 16), channels 16 ks + 8 (lane / 16)
+            const int row = 16 * ch + (lane & 15);
+            const uint32_t qa =
+                tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
+#pragma unroll(KS >= 4 ? 4 : KS)
             for (int ks = 0; ks < KS; ++ks) {
-              // rows 4 .. 7 of the table are not there: columns that nothing reads
-              const __half* zr = zh + (n8 & 3) * Ge::ZLD + 16 * ks + kq;
-              const uint32_t b0 = *reinterpret_cast<const uint32_t*>(zr);
-              const uint32_t b1 = *reinterpret_cast<const uint32_t*>(zr + 8);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int ch = hw + 4 * k;
-                if (ch < nch) {
-                  // rows 16 ch + (lane % 16), channels 16 ks + 8 (lane / 16)
-                  uint32_t av[4];
-                  const int row = 16 * ch + (lane & 15);
-                  tc_ldm<false>(av, tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) +
-                                        (2 * ks + (lane >> 4)) * 128 + row % 8 * 16);
-                  tc_mma16816(zc[k], av, b0, b1);
-                }
-              }
+              uint32_t av[4];
+              tc_ldm<false>(av, qa + 256 * ks);
+              tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                          *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
             }
           }
-          // lane (row n8, n8 + 8; groups kq, kq + 1)
-          if (kq < 4) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int ch = hw + 4 * k;
-              if (ch < nch) {
-                float* z = zk_s + par * 4 * 128 + 16 * ch + n8;
-                z[kq * 128] = zc[k][0] * a.qscale;
-                z[(kq + 1) * 128] = zc[k][1] * a.qscale;
-                z[kq * 128 + 8] = zc[k][2] * a.qscale;
-                z[(kq + 1) * 128 + 8] = zc[k][3] * a.qscale;
-              }
-            }
+          if (kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
+            float* z = zk_s + (par * 4 + kq) * 128 + 16 * ch + n8;
+            z[0] = zc[0] * a.qscale;
+            z[128] = zc[1] * a.qscale;
+            z[8] = zc[2] * a.qscale;
+            z[136] = zc[3] * a.qscale;
           }
-          __syncwarp();
-          if (lane == 0) tc_arrive(&bars.z_full[par]);
-          tc_named<4>();  // the keys' table may be written again
-        };
-        int it = it0;
-        zeros(g.t0, it);
-        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          const int par = it & 1;
-          if (t + 1 < g.t0 + g.nt) zeros(t + 1, it + 1);
-          // ---- sums over the tile's tokens
-          tc_wait(&bars.p_full[par], it >> 1, dead);
-          const __half* zv = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
-          const uint32_t pbase = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int ch = hw + 4 * k;
-            if (ch < nch) {
-              if (s_resc[par][ch]) {
-                const float f0 = f_s[par * 128 + 16 * ch + n8], f1 = f_s[par * 128 + 16 * ch + n8 + 8];
-                acc[k][0] *= f0;
-                acc[k][1] *= f0;
-                acc[k][2] *= f1;
-                acc[k][3] *= f1;
-              }
-#pragma unroll 2
-              for (int ks = 0; ks < 8; ++ks) {
-                // 8 x 8 blocks (tokens x rows), transposed on the way: rows 16 ch + 0 / 8,
-                // tokens 16 ks + 0 / 8
-                const int blk = lane >> 3;
-                uint32_t av[4];
-                tc_ldm<true>(av, pbase + (2 * ch + (blk & 1)) * 2048 + (2 * ks + (blk >> 1)) * 128 +
-                                     (lane & 7) * 16);
-                tc_mma16816(acc[k], av, *reinterpret_cast<const uint32_t*>(zv + 16 * ks),
-                            *reinterpret_cast<const uint32_t*>(zv + 16 * ks + 8));
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) tc_arrive(&bars.h_done[par]);
         }
+        __syncwarp();
+        if (lane == 0) tc_arrive(&bars.z_full[par]);
+      }
+    } else if (warp < 22) {
+      // ==== sums over tokens, of the weights and of the values' zeros: chunks uw, uw + 4,
+      // or with two streams chunk uw of each
+      const int uw = warp - 18, ut = uw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
+      float acc[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+      int it = it0, st = st0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int par = it & 1;
+        __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
+        if (t < g.tq) {
+          const int s = st % Ge::NST;
+          const M* vz = reinterpret_cast<const M*>(sm + Ge::S_RING + s * Ge::STAGE + Ge::O_VZ);
+          const int n = (int)min(g.n_q - (long long)t * kTcTile, 128LL);
+          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const int i = ut + 128 * j;
+            zv[i % NJ * Ge::ZLD + tc_pos<E>(i / NJ)] =
+                i / NJ < n ? __float2half_rn(to_f32(vz[i])) : __ushort_as_half(0);
+          }
+          tc_sums_sync();
+          if (lane == 0) tc_arrive(&bars.raw_empty[s]);
+          ++st;
+        } else {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ut] = __ushort_as_half(0);
+          tc_sums_sync();
+        }
+        tc_wait(&bars.p_full[par], it >> 1, dead);
+        const __half* zr = zv + n8 * Ge::ZLD + kq;
+        // 8 x 8 blocks (tokens x rows) of weights, transposed on the way: rows 16 ch + 0 / 8,
+        // tokens 16 ks + 0 / 8
+        const int blk = lane >> 3;
+        const uint32_t pbase = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2) + (blk & 1) * 2048 +
+                               (blk >> 1) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int ch = hw + 4 * k;
-          if (ch < nch) {
-            float* z = lz_s + (16 * ch + n8) * 8 + kq;
-            z[0] = acc[k][0];
-            z[1] = acc[k][1];
-            z[64] = acc[k][2];
-            z[65] = acc[k][3];
+          const int ch = two ? uw : uw + 4 * k;
+          if (ch < nch && (!two || k == par)) {
+            if (s_resc[par][ch]) {
+              const float f0 = f_s[par * 128 + 16 * ch + n8], f1 = f_s[par * 128 + 16 * ch + n8 + 8];
+              acc[k][0] *= f0;
+              acc[k][1] *= f0;
+              acc[k][2] *= f1;
+              acc[k][3] *= f1;
+            }
+#pragma unroll 2
+            for (int ks = 0; ks < 8; ++ks) {
+              uint32_t av[4];
+              tc_ldm<true>(av, pbase + ch * 4096 + ks * 256);
+              tc_mma16816(acc[k], av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                          *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+            }
           }
         }
-      } else if (warp == 20) {
-        // ==== matrix instructions
-        const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
-        const uint64_t q_desc = tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
-        const uint64_t p_desc = tc_desc(tc_smem(sm + Ge::S_P), 128, 2048);
-        const bool one = tc_elect();
-        auto scores = [&](int t, int it) {
-          const int par = __shfl_sync(0xffffffffu, it & 1, 0);
-          tc_wait(&bars.k_full, it, dead);
-          if (s2) {
-            if (it >= 2) tc_wait(&bars.s_empty[par], (it >> 1) - 1, dead);
-          } else if (it >= 1) {
-            tc_wait(&bars.s_empty[par ^ 1], (it - 1) >> 1, dead);
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + kTS + (s2 ? 64 * par : 0);
-          const bool lo = t < g.tq;
-          if (one) {
-            tc_mma_row<KS>(d, tmem + kTKhi, q_desc, id_s, false);
-            if (lo) tc_mma_row<KS>(d, tmem + kTKlo, q_desc, id_s, true);
-            tc_commit(&bars.s_full[par]);
-          }
-          __syncwarp();
-        };
-        int it = it0;
-        scores(g.t0, it);
-        for (int t = g.t0; t < g.t0 + g.nt; ++t, ++it) {
-          const int par = __shfl_sync(0xffffffffu, it & 1, 0);
-          if (t + 1 < g.t0 + g.nt) scores(t + 1, it + 1);
-          tc_wait(&bars.v_full, it, dead);
-          tc_wait(&bars.p_full[par], it >> 1, dead);
-          tc_fence_after();
-          const uint64_t pd = p_desc + (par ? 128 * 128 * 2 / 16 : 0);
-          const bool lo = t < g.tq, add = t > g.t0;
-          if (one) {
-            tc_mma_row<8>(tmem + kTO, tmem + kTVhi, pd, id_o, add);
-            if (lo) tc_mma_row<8>(tmem + kTO, tmem + kTVlo, pd, id_o, true);
-            tc_commit(&bars.pv_done[par]);
-          }
-          __syncwarp();
-        }
-        it = it0 + g.nt - 1;
-        tc_wait(&bars.pv_done[it & 1], it >> 1, dead);
+        __syncwarp();
+        if (lane == 0) tc_arrive(&bars.h_done[par]);
       }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int ch = two ? uw : uw + 4 * k;
+        if (ch < nch) {
+          float* z = lz_s + ((two ? 64 * k : 0) + 16 * ch + n8) * 8 + kq;
+          z[0] = acc[k][0];
+          z[1] = acc[k][1];
+          z[64] = acc[k][2];
+          z[65] = acc[k][3];
+        }
+      }
+    } else if (warp == 22) {
+      // ==== score products
+      const uint32_t id = tc_idesc(nr, false);
+      const uint64_t q_desc = tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
+      const bool one = tc_elect();
+      int it = it0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int par = __shfl_sync(0xffffffffu, it & 1, 0);
+        // S may be written again: two tiles ago, or with one buffer the last one
+        if (it >= (two ? 2 : 1))
+          tc_wait(&bars.s_empty[two ? par : par ^ 1], two ? (it >> 1) - 1 : (it - 1) >> 1, dead);
+        tc_wait(&bars.k_full, it, dead);
+        tc_fence_after();
+        const uint32_t d = tmem + kTS + (two ? 64 * par : 0);
+        const bool lo = t < g.tq;
+        if (one) {
+          tc_mma_row<KS>(d, tmem + kTKhi, q_desc, id, false);
+          if (lo) tc_mma_row<KS>(d, tmem + kTKlo, q_desc, id, true);
+          tc_commit(&bars.s_full[par]);
+        }
+        __syncwarp();
+      }
+    } else {
+      // ==== value products
+      const uint32_t id = tc_idesc(nr, true);
+      const uint64_t p_desc = tc_desc(tc_smem(sm + Ge::S_P), 128, 2048);
+      const bool one = tc_elect();
+      int it = it0;
+      for (int t = g.t0; t < t1; ++t, ++it) {
+        const int par = __shfl_sync(0xffffffffu, it & 1, 0);
+        tc_wait(&bars.v_full, it, dead);
+        tc_wait(&bars.p_full[par], it >> 1, dead);
+        tc_fence_after();
+        const uint64_t pd = p_desc + (par ? 128 * 128 * 2 / 16 : 0);
+        const uint32_t o = tmem + kTO + (two ? 64 * par : 0);
+        const bool lo = t < g.tq, add = t - g.t0 >= (two ? 2 : 1);
+        if (one) {
+          tc_mma_row<8>(o, tmem + kTVhi, pd, id, add);
+          if (lo) tc_mma_row<8>(o, tmem + kTVlo, pd, id, true);
+          tc_commit(&bars.pv_done[par]);
+        }
+        __syncwarp();
+      }
+      --it;
+      tc_wait(&bars.pv_done[it & 1], it >> 1, dead);  // and all before it
     }
     tc_sync_segment();
 
-    // ---- end of a segment: lane = channel, 16 rows at a time
+    // ---- end of a segment: lane = channel, 4 rows at a time
     if (warp >= 8 && warp < 16) {
       const int sg = (warp - 8) >> 2, sw = warp & 3;
       const int ch_d = sw * 32 + lane;
-      const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16);
+      const uint32_t t_lane = tmem + kTO + ((uint32_t)(sw * 32) << 16);
       const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
+      // streams that took a tile: by the parity of the block's count
+      const bool u0 = !two || g.nt > 1 || (it0 & 1) == 0, u1 = two && (g.nt > 1 || (it0 & 1) == 1);
+      const int i1 = s_odd ? min((t1 - g.tq) * kTcTile, g.r + a.N) : 0;
       float* part = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
-      for (int ch = sg; ch < nch; ch += 2) {
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        if (g.ok) tc_ld16(t_lane + kTO + ch * 16, v);
-        if (ch_d >= D) continue;
-        // infinite or NaN raw values, of the tokens that a row attends to
-        const int i1 = s_odd ? min((g.t0 + g.nt - g.tq) * kTcTile, g.r + a.N) : 0;
+      __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
 #pragma unroll 1
-        for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
-          const __half w = i < g.r ? static_cast<const __half*>(a.c.v_res)[(g.unit * a.c.R + i) * D + ch_d]
-                                   : static_cast<const __half*>(a.v)[(g.unit * a.N + i - g.r) * D + ch_d];
-          if ((__half_as_ushort(w) & 0x7C00u) != 0x7C00u) continue;
-          const uint32_t sees = i < g.r ? 0xFFFFu : tc_seen(mask_s, i - g.r, g.row0 + ch * 16, a.N);
+      for (int e4 = 4 * sg; e4 < g.nrows && sw < NJ; e4 += 8) {
+        float v0[4] = {0.f, 0.f, 0.f, 0.f}, v1[4] = {0.f, 0.f, 0.f, 0.f};
+        if (g.ok && u0) tc_ld4(t_lane + e4, v0);
+        if (g.ok && u1) tc_ld4(t_lane + 64 + e4, v1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if ((sees >> e) & 1u) v[e] += __half2float(w);
-        }
-        __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0 + ch * 16) * (long long)D + ch_d;
-        const float* lz = lz_s + ch * 128;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int row = ch * 16 + e;
-          const float l = poison ? kNaN : lz[8 * e + 4];
-          const float o = fmaf(2.0f, v[e], lz[8 * e + sw]);
-          if (row >= g.nrows) continue;
+        for (int e = 0; e < 4; ++e) {
+          const int row = e4 + e;
+          if (row >= g.nrows) break;
+          // the streams' parts, against the larger reference
+          float m = m_s[row], o = fmaf(2.0f, v0[e], lz_s[8 * row + sw]), l = lz_s[8 * row + 4];
+          if (!u0) o = l = 0.f;
+          if (u1) {
+            const float m1 = m_s[64 + row], mx = fmaxf(m, m1);
+            const float w0 = tc_ex2(m - mx), w1 = tc_ex2(m1 - mx);
+            o = w0 * o + w1 * fmaf(2.0f, v1[e], lz_s[8 * (64 + row) + sw]);
+            l = w0 * l + w1 * lz_s[8 * (64 + row) + 4];
+            m = mx;
+          }
+          // infinite or NaN raw values, of the tokens that the row attends to
+#pragma unroll 1
+          for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
+            const __half w = i < g.r
+                                 ? static_cast<const __half*>(a.c.v_res)[(g.unit * a.c.R + i) * D + ch_d]
+                                 : static_cast<const __half*>(a.v)[(g.unit * a.N + i - g.r) * D + ch_d];
+            if ((__half_as_ushort(w) & 0x7C00u) == 0x7C00u &&
+                (i < g.r || (tc_seen(mask_s, i - g.r, g.row0 + row, a.N) & 1u)))
+              o += __half2float(w);
+          }
+          if (poison) {
+            o = m = 0.f;
+            l = kNaN;
+          }
           if (g.whole) {
-            out[e * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(poison ? 0.f : o, l));
+            out[row * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(o, l));
           } else {
-            part[2 * nr + row * D + ch_d] = poison ? 0.f : o;
+            part[2 * nr + row * D + ch_d] = o;
             if (ch_d == 0) {
-              part[2 * row] = poison ? 0.f : m_s[row];
+              part[2 * row] = m;
               part[2 * row + 1] = l;
             }
           }
@@ -1155,14 +1186,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     if (tid == 0) s_poison[(seg & 1) ^ 1] = 0;  // the next segment's
     if (g.ok) {
       it0 += g.nt;
-      const int q1 = min(g.t0 + g.nt, g.tq);
-      if (q1 > g.t0) st0 += q1 - g.t0;
+      st0 += max(min(t1, g.tq) - g.t0, 0);
     }
     tc_sync_segment();
   }
 
   __syncthreads();
-  if (warp == 20) {
+  if (warp == 22) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
