@@ -96,8 +96,8 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 }  // namespace
 
 // The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all
-// fit.  Tensor cores: up to 128 rows a block, more in blocks of equal size, since
-// each block unpacks the cache again; one block of threads per SM.
+// fit.  Tensor cores: up to 64 rows a block, more in blocks of equal size (each
+// unpacks the cache again); one block of threads per SM.
 static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
   const int rows = gq * N;
   TreePlan p;
@@ -108,7 +108,7 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.ctas = sms * (p.rb == 16 ? 4 : 2);
     p.min_w = 4;
   } else {
-    p.n_rb = (rows + 127) / 128;
+    p.n_rb = (rows + 63) / 64;
     p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 128;

@@ -4,7 +4,7 @@
 //
 // The work is split as kivi_tree.cuh says, in tiles of 128 tokens; a row is a
 // (query head of the group, node) pair, `nr` rows (a multiple of 16, at most
-// 128) at a time.  Both products are taken transposed, so that the cache's side
+// 64) at a time.  Both products are taken transposed, so that the cache's side
 // fills the 128 rows of the matrix instruction whatever the tree's size is:
 //   S^T [128 tokens x nr]  = K^ [128 x D]      . Q^T   (A = K^, B = Q)
 //   O^T [128 (D) x nr]    += V^^T [D x 128]    . P^T   (A = V^^T, B = P)
@@ -30,20 +30,24 @@
 // rounding.  Scores, maxima, sums and accumulators are binary32.
 //
 // Running maximum: a row's reference m is raised only when a score of a tile
-// exceeds it by more than 8 (in units of log2), since weights up to 2^8 lose
-// nothing; that is checked for all rows by one vote, and the rare tile that
-// needs it rescales O^T in tensor memory.
+// exceeds it by more than 14 (in units of log2): weights up to 2^14 lose nothing
+// in binary16 or in the binary32 sums.  The weights of a tile are formed with the
+// references as they are while the excess is watched; one vote tells whether
+// that held, and the rare tile where it did not raises the references, rescales
+// O^T in tensor memory and forms its weights again.
 //
 // Warps: 4 unpack keys and 4 values (one code), 2 groups of 4 softmax, 2 the
-// zeros' products with the queries, 4 the sums over tokens, one issues the score
+// scales and zeros of keys and the zeros' products with the queries, 4 the
+// scales and zeros of values and the sums over tokens, one issues the score
 // products, one the value products, one the copies (cp.async.bulk of each
-// tile's ranges into a ring).  With up to 64 rows the two softmax groups take
-// every other tile, each with its own references and accumulators (two
-// streams, joined at the end of a segment); with more rows they share a tile,
-// 16 rows each in turn.  A role's code is a small loop: together they have to
-// fit the instruction cache (unrolled, the kernel took three times as long).
-// All waits are bounded: one that runs out marks the block dead, whose further
-// waits return at once and whose results are NaN.
+// tile's ranges into a ring).  The two softmax groups take every other tile,
+// each with its own S^T, O^T and references (two streams, joined at the end of
+// a segment), so that one's latencies hide behind the other.  Operands are
+// handed over by halves, so that one half is unpacked while the products of the
+// other run.  A role's code is a small loop: together they have to fit the
+// instruction cache (with the roles unrolled, 369 KB of code, the kernel took
+// four times as long).  All waits are bounded: one that runs out marks the block
+// dead, whose further waits return at once and whose results are NaN.
 #pragma once
 
 #include <type_traits>
@@ -56,7 +60,7 @@ namespace {
 constexpr int kTcTile = 128;        // tokens
 constexpr int kTcWarps = 25;
 constexpr int kTcThreads = kTcWarps * 32;
-constexpr float kTcSlack = 8.0f;    // log2 units a score may exceed m by
+constexpr float kTcSlack = 14.0f;   // log2 units a score may exceed m by
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
 
 // ---- layouts ---------------------------------------------------------------
@@ -79,22 +83,24 @@ struct TcGeo {
   static constexpr int NST = 3;
   // shared memory
   static constexpr int S_RING = 0;
-  static constexpr int S_Q = S_RING + NST * STAGE;        // B operand, 128 rows
-  static constexpr int S_P = S_Q + 128 * D * 2;           // 2 x [128 rows x 128 tokens]
-  static constexpr int S_KSC = S_P + 2 * 128 * 128 * 2;   // 4 warps x D x (hi, lo) halves
-  static constexpr int S_VSC = S_KSC + 4 * D * 4;         // 4 warps x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 4 * 128 * 4;        // 2 x [4 groups][128 rows] float
-  static constexpr int S_OFF = S_ZK + 2 * 4 * 128 * 4;    // [4 warps][128 rows] float
-  static constexpr int S_WMAX = S_OFF + 4 * 128 * 4;      // [4 warps][128 rows]
-  static constexpr int S_M = S_WMAX + 4 * 128 * 4;        // [128 rows]
-  static constexpr int S_F = S_M + 128 * 4;               // 2 x [128 rows]
-  static constexpr int S_LZ = S_F + 2 * 128 * 4;          // [128 rows][8]
-  static constexpr int S_MASK = S_LZ + 128 * 8 * 4;       // [256][8] words
+  static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
+  static constexpr int S_P = S_Q + 64 * D * 2;           // 2 x [64 rows][128 tokens]
+  static constexpr int P_B = 64 * 128 * 2;
+  static constexpr int S_RAW = S_P + 2 * P_B;            // raw values [128 tokens][D]
+  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 2 x 4 groups x D x (hi, lo) halves
+  static constexpr int S_VSC = S_KSC + 2 * 4 * D * 4;    // 2 x 4 groups x 128 x (hi, lo)
+  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // 2 x [4 groups][64 rows] float
+  static constexpr int S_OFF = S_ZK + 2 * 4 * 64 * 4;    // [2 streams][4 warps][64 rows] float
+  static constexpr int S_WMAX = S_OFF + 2 * 4 * 64 * 4;  // the same
+  static constexpr int S_M = S_WMAX + 2 * 4 * 64 * 4;    // [2 streams][64 rows]
+  static constexpr int S_F = S_M + 2 * 64 * 4;           // the same
+  static constexpr int S_LZ = S_F + 2 * 64 * 4;          // [2 streams][64 rows][8]
+  static constexpr int S_MASK = S_LZ + 2 * 64 * 8 * 4;   // [256][8] words
   // zeros as binary16 in operand order, rows padded against bank conflicts:
   // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
   static constexpr int ZLD = 136;
   static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
-  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;     // 2 x (both tables)
+  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;    // 2 x (both tables)
   static constexpr int BYTES = S_ZV + 2 * 8 * ZLD * 2;
 };
 
@@ -183,6 +189,15 @@ __device__ __forceinline__ void tc_ld16(uint32_t t, float (&r)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
+__device__ __forceinline__ void tc_st16(uint32_t t, const float (&r)[16]) {
+  uint32_t u[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(r[8 * h + i]);
+    tc_st8(t + 8 * h, u);
+  }
+}
 // Four columns, for the loops that run seldom.
 __device__ __forceinline__ void tc_ld4(uint32_t t, float (&r)[4]) {
   uint32_t u[4];
@@ -192,11 +207,6 @@ __device__ __forceinline__ void tc_ld4(uint32_t t, float (&r)[4]) {
   tc_wait_ld();
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = __uint_as_float(u[i]);
-}
-__device__ __forceinline__ void tc_st4(uint32_t t, const float (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t),
-               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])),
-               "r"(__float_as_uint(r[2])), "r"(__float_as_uint(r[3])));
 }
 // Instruction descriptor of kind::f16: D binary32, A and B binary16, A K-major.
 __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_mn) {
@@ -235,6 +245,11 @@ __device__ __forceinline__ bool tc_elect() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
+}
+__device__ __forceinline__ float tc_warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float tc_ex2(float x) {
   float y;
@@ -275,8 +290,10 @@ __device__ __forceinline__ void tc_group(int sg) {
   else
     asm volatile("bar.sync 2, 128;" ::: "memory");
 }
-// Barriers of the two warps of the zeros' products and the four of the sums.
+// Barriers of the two warps of the zeros' products, the four that unpack values
+// and the four of the sums.
 __device__ __forceinline__ void tc_pair_sync() { asm volatile("bar.sync 4, 64;" ::: "memory"); }
+__device__ __forceinline__ void tc_values_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
 __device__ __forceinline__ void tc_sums_sync() { asm volatile("bar.sync 5, 128;" ::: "memory"); }
 // Barrier of the group that tells whether any of its threads has `x`.
 __device__ __forceinline__ bool tc_group_any(int sg, bool x) {
@@ -405,18 +422,16 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-// A lane's words (`stride` words apart) into its row of the two planes, n codes (n
-// a multiple of 32); sc: their scales' parts, hi[n] and lo[n].  The loop stays a
-// loop: the kernel's roles share the instruction cache.
+// Some units of a lane's words (`stride` words apart) into its row of the two planes;
+// hi, lo: the parts of their scales.  The loop stays a loop: the kernel's roles share
+// the instruction cache.
 template <int BITS>
 __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, int stride,
-                                          const __half* sc, int n) {
+                                          const uint4* hi, const uint4* lo, int units) {
   using U = TcUnit<BITS>;
   constexpr int H = U::kUnit / 16;
-  const uint4* hi = reinterpret_cast<const uint4*>(sc);
-  const uint4* lo = reinterpret_cast<const uint4*>(sc + n);
 #pragma unroll 1
-  for (int u = n / U::kUnit; u > 0; --u) {
+  for (int u = units; u > 0; --u) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
     for (int i = 0; i < U::kUnitW; ++i) w[i] = words[i * stride];
@@ -468,13 +483,32 @@ __device__ __forceinline__ void tc_raw_pairs(const uint4& x, const uint4& y, uin
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
 }
-// A lane's raw key row, halved, into its operand row: 16 places are two runs of 8
-// channels E / 2 apart (or two blocks of 8 channels).  src null: zeros.
-template <int D, int E>
-__device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* src) {
+// 128 raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
+// at dp up to n) into rows of D in shared memory, by the 128 threads of the values'
+// warps.
+template <int D>
+__device__ __forceinline__ void tc_stage_raw(uint4* dst, int th, const __half* wp, const __half* dp,
+                                             int first, int r, int n) {
+  const bool al = ((uintptr_t)dp & 15) == 0;
+#pragma unroll 4
+  for (int j = 0; j < D / 8; ++j) {
+    const int k = th + 128 * j, i = first + k / (D / 8), c = k % (D / 8) * 8;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (i < r)
+      x = *reinterpret_cast<const uint4*>(wp + i * D + c);
+    else if (i < n)
+      x = tc_raw8(dp + (i - r) * D + c, al);
+    dst[k] = x;
+  }
+  tc_values_sync();
+}
+// C0 .. C1 of a lane's raw key row, halved, into its operand row: 16 places are two
+// runs of 8 channels E / 2 apart (or two blocks of 8 channels).  src null: zeros.
+template <int E>
+__device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* src, int c0, int c1) {
   const bool al = ((uintptr_t)src & 15) == 0;
 #pragma unroll 2
-  for (int c = 0; c < D / 16; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
     uint4 x = make_uint4(0, 0, 0, 0), y = x;
     if (src != nullptr) {
@@ -486,29 +520,25 @@ __device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* src) {
     tc_st8(t_hi + 8 * c, r);
   }
 }
-// A lane's channel of 128 raw tokens from `first` on (the window's r tokens at wp,
-// then the drafted ones at dp up to n), halved, into its operand row.  Infinities
-// and NaN are left out (they join at the segment's end, for the rows that attend
-// to them); returns whether there were any.
+// Places 16 c0 .. 16 c1 - 1 of a lane's channel of 128 raw tokens (`v`, rows of D
+// in shared memory), halved, into its operand row.  Infinities and NaN are left out
+// (they join at the segment's end, for the rows that attend to them); returns
+// whether there were any.
 template <int D, int E>
-__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* wp, const __half* dp,
-                                              int first, int r, int n) {
+__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, int c0, int c1) {
   uint32_t odd = 0;
 #pragma unroll 1
-  for (int c = 0; c < 8; ++c) {
-    const int e0 = first + (E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c);
-    uint16_t v[16];
+  for (int c = c0; c < c1; ++c) {
+    const __half* s0 = v + (E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c) * D;
+    const __half* s1 = s0 + (E >= 16 ? E / 2 : 8) * D;
+    uint32_t a[8], b[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int i = e0 + k % 8 + (k / 8) * (E >= 16 ? E / 2 : 8);
-      const __half* src = i < r ? wp + i * D : dp + (i - r) * D;
-      v[k] = 0;
-      if (i < n) v[k] = __half_as_ushort(*src);
+    for (int k = 0; k < 8; ++k) {
+      a[k] = __half_as_ushort(s0[k * D]);
+      b[k] = __half_as_ushort(s1[k * D]);
     }
-    const uint4 x = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
-                               v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
-    const uint4 y = make_uint4(v[8] | (uint32_t)v[9] << 16, v[10] | (uint32_t)v[11] << 16,
-                               v[12] | (uint32_t)v[13] << 16, v[14] | (uint32_t)v[15] << 16);
+    const uint4 x = make_uint4(a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16);
+    const uint4 y = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
     uint32_t q[8];
     tc_raw_pairs<E>(x, y, q);
 #pragma unroll
@@ -539,7 +569,10 @@ constexpr uint32_t kTKhi = 0, kTKlo = 64, kTVhi = 128, kTVlo = 192, kTO = 256, k
 
 struct TcBars {
   uint64_t raw_full[3], raw_empty[3];
-  uint64_t k_full, v_full;
+  // scales' parts set out for the unpacking warps: [keys, values][tile parity]
+  uint64_t sc_full[2][2], sc_free[2][2];
+  // halves of the operands in tensor memory: [keys, values][half]
+  uint64_t a_full[2][2], a_free[2][2];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2], h_done[2];
   uint64_t z_full[2], z_empty[2];
@@ -569,13 +602,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
   __shared__ int s_poison[2];   // [segment parity]
-  __shared__ int s_resc[2][8];  // [tile parity][16 rows]: rows were rescaled
+  __shared__ int s_resc[2];     // [stream]: the tile's rows were rescaled
   volatile int* dead = &s_dead;
   // what a whole warp shares is broadcast, so that it lives in uniform registers
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
   const int nr = p.rb, nch = nr / 16;
-  const bool two = nr <= 64;  // two streams: tiles in turn, each its S and O
 
   // ---- set-up
   if (warp == 22) {
@@ -606,17 +638,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       tc_bar_init(&bars.raw_full[i], 1);
       tc_bar_init(&bars.raw_empty[i], 14);
     }
-    tc_bar_init(&bars.k_full, 4);
-    tc_bar_init(&bars.v_full, 4);
-    const int soft = two ? 4 : 8;  // softmax warps of a tile
     for (int i = 0; i < 2; ++i) {
+      tc_bar_init(&bars.sc_full[0][i], 2);
+      tc_bar_init(&bars.sc_full[1][i], 4);
+      for (int k = 0; k < 2; ++k) {
+        tc_bar_init(&bars.sc_free[k][i], 4);
+        tc_bar_init(&bars.a_full[k][i], 4);
+        tc_bar_init(&bars.a_free[k][i], 1);
+      }
       tc_bar_init(&bars.s_full[i], 1);
-      tc_bar_init(&bars.s_empty[i], soft);
-      tc_bar_init(&bars.p_full[i], soft);
+      tc_bar_init(&bars.s_empty[i], 4);
+      tc_bar_init(&bars.p_full[i], 4);
       tc_bar_init(&bars.pv_done[i], 1);
       tc_bar_init(&bars.h_done[i], 4);
       tc_bar_init(&bars.z_full[i], 2);
-      tc_bar_init(&bars.z_empty[i], soft);
+      tc_bar_init(&bars.z_empty[i], 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -628,10 +664,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   TcWalk walk = s_walk;
 
-  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // [stream][64] or [128]
-  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // [tile parity][128]
-  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [tile parity][group][128]
-  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // rows as m_s, 8 each
+  // streams: tiles of even and of odd count
+  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // [stream][64]
+  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // [stream][64]
+  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [stream][group][64]
+  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [stream][64][8]
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
   // A range ends within a group at most at its own end: segments after the first
@@ -748,86 +785,85 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     if (!g.ok) {
     } else if (warp < 8) {
       // ==== keys (lane = token of subtile w) and values (lane = channel of group w),
-      // by one code
-      const bool vals = warp >= 4;
-      const int w = warp & 3, n_codes = vals ? 128 : D;
+      // by one code, in halves (keys of 32 channels in one piece)
+      using U = TcUnit<BITS>;
+      const int vals = warp >> 2, w = warp & 3;
+      const int n_codes = vals ? 128 : D, halves = vals || D > 32 ? 2 : 1;
+      const int units = n_codes / halves / U::kUnit, cols = n_codes / halves / 2;
       const uint32_t t_hi = tmem + ((uint32_t)(w * 32) << 16) + (vals ? kTVhi : kTKhi);
-      __half* sc = reinterpret_cast<__half*>(vals ? sm + Ge::S_VSC + w * 512 : sm + Ge::S_KSC + w * D * 4);
-      const int o_sc = vals ? Ge::O_VS + w * (int)sizeof(M) : Ge::O_KS + w * Ge::KM;
+      const __half* sc0 = reinterpret_cast<const __half*>(sm + (vals ? Ge::S_VSC : Ge::S_KSC)) + w * 2 * n_codes;
       const int o_w = vals ? Ge::O_VC + (w * 32 + lane) * 4 : Ge::O_KC + w * Ge::KC + lane * WK * 4;
-      const int s_str = vals ? NJ : 1, w_str = vals ? D : 1;
-      uint64_t* done = vals ? bars.pv_done : bars.s_full;
-      uint64_t* full = vals ? &bars.v_full : &bars.k_full;
+      const int w_str = vals ? D : 1;
       const bool act = !vals || w < NJ;
       int it = it0, st = st0;
       for (int t = g.t0; t < t1; ++t, ++it) {
         const int s = st % Ge::NST;
         const bool raw = t >= g.tq;
         const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+        const int first = (t - g.tq) * kTcTile;  // of the raw tokens
+        const __half* src = nullptr;
         if (!raw) {
+          // (the scales' writers have waited for the copies)
           tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-          const M* src = reinterpret_cast<const M*>(stg + o_sc);
-          // tokens that exist (values of others must not be NaN: weight 0 times them)
-          const int n = vals ? (int)min(g.n_q - (long long)t * kTcTile, 128LL) : D;
-          __syncwarp();
-#pragma unroll 2
-          for (int c = lane; c < n_codes; c += 32) {
-            __half hi = __ushort_as_half(0), lo = hi;
-            if (act && c < n) tc_split(to_f32(src[c * s_str]), &hi, &lo);
-            sc[tc_pos<E>(c)] = hi;
-            sc[n_codes + tc_pos<E>(c)] = lo;
-          }
-          __syncwarp();
-        }
-        if (it > 0) tc_wait(&done[(it - 1) & 1], (it - 1) >> 1, dead);
-        tc_fence_after();
-        if (!act) {
-        } else if (!raw) {
-          tc_unpack<BITS>(t_hi, reinterpret_cast<const uint32_t*>(stg + o_w), w_str, sc, n_codes);
+          tc_wait(&bars.sc_full[vals][st & 1], st >> 1, dead);
         } else if (!vals) {
           // raw tokens: the window, then the drafted ones; halved like s
-          const int i = (t - g.tq) * kTcTile + w * 32 + lane;
-          const __half* src = nullptr;
+          const int i = first + w * 32 + lane;
           if (i < g.r)
             src = static_cast<const __half*>(a.c.k_res) + (g.unit * a.c.R + i) * D;
           else if (i < g.r + a.N)
             src = static_cast<const __half*>(a.k) + (g.unit * a.N + (i - g.r)) * D;
-          tc_raw_keys<D, E>(t_hi, src);
         } else {
-          const int ch = w * 32 + lane;
-          const bool odd = tc_raw_values<D, E>(
-              t_hi, static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D + ch,
-              static_cast<const __half*>(a.v) + g.unit * a.N * D + ch, (t - g.tq) * kTcTile, g.r,
-              g.r + a.N);
-          if (odd) s_odd = 1;
+          tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), w * 32 + lane,
+                          static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D,
+                          static_cast<const __half*>(a.v) + g.unit * a.N * D, first, g.r, g.r + a.N);
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (!raw) tc_arrive(&bars.raw_empty[s]);
-          tc_arrive(full);
+        const __half* sc = sc0 + (st & 1) * 8 * n_codes;
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          if (it > 0) tc_wait(&bars.a_free[vals][h], it - 1, dead);
+          tc_fence_after();
+          if (!act) {
+          } else if (!raw) {
+            tc_unpack<BITS>(t_hi + h * cols, reinterpret_cast<const uint32_t*>(stg + o_w) + h * units * U::kUnitW * w_str,
+                            w_str, reinterpret_cast<const uint4*>(sc) + h * (cols / 4),
+                            reinterpret_cast<const uint4*>(sc + n_codes) + h * (cols / 4), units);
+          } else if (!vals) {
+            tc_raw_keys<E>(t_hi, src, h * cols / 8, (h + 1) * cols / 8);
+          } else {
+            if (tc_raw_values<D, E>(t_hi, reinterpret_cast<const __half*>(sm + Ge::S_RAW) + w * 32 + lane,
+                                    h * cols / 8, (h + 1) * cols / 8))
+              s_odd = 1;
+          }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc_arrive(&bars.a_full[vals][h]);
         }
-        st += !raw;
+        if (!raw) {
+          if (lane == 0) {
+            tc_arrive(&bars.raw_empty[s]);
+            tc_arrive(&bars.sc_free[vals][st & 1]);
+          }
+          ++st;
+        } else if (vals) {
+          tc_values_sync();  // the raw values may be written again
+        }
       }
     } else if (warp < 16) {
-      // ==== softmax: lane = token.  Two streams: group sg takes the tiles of parity
-      // sg, all rows; else 16-row chunks sg, sg + 2, .. of each tile
+      // ==== softmax: lane = token; stream sg takes the tiles of its parity
       const int sg = (warp - 8) >> 2, sw = warp & 3;
-      const int ch0 = two ? 0 : sg, chs = two ? 1 : 2, ro = two ? 64 * sg : 0;
-      const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16);
-      float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + sw * 128 + ro;
-      float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + ro;  // + 128 warp
-      float* mr_s = m_s + ro;
+      const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16) + 64 * sg;
+      float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + (sg * 4 + sw) * 64;
+      float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + sg * 256;  // + 64 warp
+      float* mr_s = m_s + 64 * sg;
+      const float* zk = zk_s + (sg * 4 + sw) * 64;
       const float c1 = 2.0f * a.qscale;
       const int pk = tc_pos<E>(sw * 32 + lane);  // the token's place in the second product
-      int it = it0;
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int par = it & 1;
-        if (two && par != sg) continue;
+      unsigned char* pb = sm + Ge::S_P + sg * Ge::P_B + pk / 8 * 128 + pk % 8 * 16;
+      for (int t = g.t0 + ((it0 + sg) & 1); t < t1; t += 2) {
+        const int it = it0 + t - g.t0;
         const bool raw = t >= g.tq;
-        const uint32_t t_s = t_lane + kTS + (two ? 64 * par : 0);
-        const float* zk = zk_s + (par * 4 + sw) * 128;
         // the token of this lane: in the cache (all rows see it), drafted, or none
         const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
         const bool in = raw ? i < g.r : i < g.n_q;
@@ -835,128 +871,98 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         auto seen = [&](int ch) -> uint32_t {  // 16 bits, one for each row of chunk ch
           return in ? 0xFFFFu : (node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + ch * 16, a.N));
         };
-        // what the products two tiles ago read (weights, factors) may be written again
+        // what the products of the stream's last tile read may be written again
         if (it >= 2) {
-          tc_wait(&bars.pv_done[par], (it >> 1) - 1, dead);
-          tc_wait(&bars.h_done[par], (it >> 1) - 1, dead);
+          tc_wait(&bars.pv_done[sg], (it >> 1) - 1, dead);
+          tc_wait(&bars.h_done[sg], (it >> 1) - 1, dead);
         }
-        tc_wait(&bars.z_full[par], it >> 1, dead);
-        auto offsets = [&]() {
-          for (int e = lane; e < nr; e += 32)
-            if (two || ((e >> 4) & 1) == sg) off_s[e] = mr_s[e] - zk[e];
-          __syncwarp();
-        };
-        offsets();
-        tc_wait(&bars.s_full[par], it >> 1, dead);
+        tc_wait(&bars.z_full[sg], it >> 1, dead);
+        tc_wait(&bars.s_full[sg], it >> 1, dead);
         tc_fence_after();
-        // ---- does any score exceed its row's reference by too much?
-        float over = -__builtin_huge_valf();
-        for (int ch = ch0; ch < nch; ch += chs) {
-          float v[16];
-          tc_ld16(t_s + ch * 16, v);
-          const uint32_t sees = seen(ch);
-#pragma unroll
-          for (int e4 = 0; e4 < 4; ++e4) {
-            const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
-            const float oo[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float d = fmaf(v[4 * e4 + e], c1, -oo[e]);
-              over = fmaxf(over, (sees >> (4 * e4 + e)) & 1u ? d : over);
-            }
-          }
-        }
-        const bool need = tc_group_any(sg, over > kTcSlack);
-        if (need) {
-          // ---- new references: each warp's maxima, joined
+        bool resc = false;
 #pragma unroll 1
-          for (int ch = ch0; ch < nch; ch += chs) {
+        for (int tries = 0; tries < 2; ++tries) {
+          for (int e = lane; e < nr; e += 32) off_s[e] = mr_s[e] - zk[e];
+          __syncwarp();
+          // ---- weights against the references, and by how much a score exceeds its own
+          float over = -__builtin_huge_valf();
+#pragma unroll 1
+          for (int ch = 0; ch < nch; ++ch) {
+            float v[16];
+            tc_ld16(t_lane + kTS + ch * 16, v);
             const uint32_t sees = seen(ch);
-#pragma unroll 1
-            for (int e4 = 0; e4 < 16; e4 += 4) {
-              float v[4];
-              tc_ld4(t_s + ch * 16 + e4, v);
+            uint32_t w[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int row = ch * 16 + e4 + e;
-                const float d =
-                    warp_max((sees >> (e4 + e)) & 1u ? fmaf(v[e], c1, zk[row]) : kTcNone);
-                if (lane == 0) wmax_s[sw * 128 + row] = d;
+            for (int e4 = 0; e4 < 4; ++e4) {
+              const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
+              const float oo[4] = {o.x, o.y, o.z, o.w};
+              float e[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float d = fmaf(v[4 * e4 + k], c1, -oo[k]);
+                if (!((sees >> (4 * e4 + k)) & 1u)) d = -__builtin_huge_valf();
+                over = fmaxf(over, d);
+                e[k] = tc_ex2(d);
               }
+              const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
+              w[2 * e4] = *reinterpret_cast<const uint32_t*>(&h0);
+              w[2 * e4 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
             }
+            *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          if (!tc_group_any(sg, over > kTcSlack) || tries == 1) break;
+          // ---- new references: each warp's maxima, joined
+          resc = true;
+#pragma unroll 1
+          for (int ch = 0; ch < nch; ++ch) {
+            float v[16];
+            tc_ld16(t_lane + kTS + ch * 16, v);
+            const uint32_t sees = seen(ch);
+            float mine = kTcNone;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float d = tc_warp_max((sees >> e) & 1u ? fmaf(v[e], c1, zk[ch * 16 + e]) : kTcNone);
+              if (lane == e) mine = d;
+            }
+            if (lane < 16) wmax_s[sw * 64 + ch * 16 + lane] = mine;
           }
           tc_group(sg);
           const int e = sw * 32 + lane;  // a row of each thread
-          if (e < nr && (two || ((e >> 4) & 1) == sg)) {
+          if (e < nr) {
             const float old = mr_s[e];
-            const float mn = fmaxf(fmaxf(fmaxf(wmax_s[e], wmax_s[128 + e]),
-                                         fmaxf(wmax_s[256 + e], wmax_s[384 + e])),
+            const float mn = fmaxf(fmaxf(fmaxf(wmax_s[e], wmax_s[64 + e]),
+                                         fmaxf(wmax_s[128 + e], wmax_s[192 + e])),
                                    old);
-            f_s[par * 128 + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
+            f_s[64 * sg + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
             mr_s[e] = mn;
           }
           tc_group(sg);
-          offsets();
-          if (t - g.t0 >= (two ? 2 : 1)) {
-            // ---- accumulators so far, once the product before this one is done (the
-            // stream's last one was waited for above)
-            if (!two) tc_wait(&bars.pv_done[par ^ 1], (it - 1) >> 1, dead);
-            tc_fence_after();
+          if (t - g.t0 >= 2) {  // accumulators so far (their product was waited for above)
 #pragma unroll 1
-            for (int ch = ch0; ch < nch; ch += chs)
-#pragma unroll 1
-              for (int e4 = ch * 16; e4 < ch * 16 + 16; e4 += 4) {
-                const uint32_t t_o = t_lane + kTO + (two ? 64 * par : 0) + e4;
-                const float4 f = *reinterpret_cast<const float4*>(f_s + par * 128 + e4);
-                float v[4];
-                tc_ld4(t_o, v);
-                v[0] *= f.x;
-                v[1] *= f.y;
-                v[2] *= f.z;
-                v[3] *= f.w;
-                tc_st4(t_o, v);
-              }
+            for (int ch = 0; ch < nch; ++ch) {
+              float v[16];
+              tc_ld16(t_lane + kTO + ch * 16, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] *= f_s[64 * sg + ch * 16 + k];
+              tc_st16(t_lane + kTO + ch * 16, v);
+            }
             tc_wait_st();
           }
-          __syncwarp();
         }
-        if (lane == 0 && sw == 0)
-          for (int ch = ch0; ch < nch; ch += chs) s_resc[par][ch] = need;
-        // ---- weights
-        unsigned char* pb = sm + Ge::S_P + par * 128 * 128 * 2 + pk / 8 * 128 + pk % 8 * 16;
-        for (int ch = ch0; ch < nch; ch += chs) {
-          float v[16];
-          tc_ld16(t_s + ch * 16, v);
-          const uint32_t sees = seen(ch);
-          uint32_t w[8];
-#pragma unroll
-          for (int e4 = 0; e4 < 4; ++e4) {
-            const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
-            const float oo[4] = {o.x, o.y, o.z, o.w};
-            float e[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e[k] = tc_ex2(fmaf(v[4 * e4 + k], c1, -oo[k]));
-              if (!((sees >> (4 * e4 + k)) & 1u)) e[k] = 0.0f;
-            }
-            const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
-            w[2 * e4] = *reinterpret_cast<const uint32_t*>(&h0);
-            w[2 * e4 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-          }
-          *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+        if (lane == 0 && sw == 0) s_resc[sg] = resc;
         tc_fence_before();
         tc_fence_smem();
         __syncwarp();
         if (lane == 0) {
-          tc_arrive(&bars.p_full[par]);
-          tc_arrive(&bars.s_empty[par]);
-          tc_arrive(&bars.z_empty[par]);
+          tc_arrive(&bars.p_full[sg]);
+          tc_arrive(&bars.s_empty[sg]);
+          tc_arrive(&bars.z_empty[sg]);
         }
       }
     } else if (warp < 18) {
-      // ==== sum_d q_d z_gd of a tile's four groups: 16-row chunks zw, zw + 2, ..
+      // ==== keys' scales in two parts, and sum_d q_d z_gd of the tile's four groups:
+      // 16-row chunks zw, zw + 2
       const int zw = warp - 16, zt = zw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
       int it = it0, st = st0;
       for (int t = g.t0; t < t1; ++t, ++it) {
@@ -965,15 +971,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH) + par * 4 * Ge::ZLD;
         if (!raw) {
           const int s = st % Ge::NST;
-          const M* kz = reinterpret_cast<const M*>(sm + Ge::S_RING + s * Ge::STAGE + Ge::O_KZ);
+          const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+          const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
+          const M* ks = reinterpret_cast<const M*>(stg + Ge::O_KS);
+          __half* sc = reinterpret_cast<__half*>(sm + Ge::S_KSC) + (st & 1) * 8 * D;
           tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-#pragma unroll
+          if (st >= 2) tc_wait(&bars.sc_free[0][st & 1], (st >> 1) - 1, dead);
+#pragma unroll 2
           for (int j = 0; j < 4 * D / 64; ++j) {
-            const int i = zt + 64 * j;
-            zh[i / D * Ge::ZLD + tc_pos<E>(i % D)] = __float2half_rn(to_f32(kz[i]));
+            const int i = zt + 64 * j, gr = i / D, c = tc_pos<E>(i % D);
+            zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(kz[i]));
+            tc_split(to_f32(ks[i]), &sc[gr * 2 * D + c], &sc[gr * 2 * D + D + c]);
           }
           tc_pair_sync();
-          if (lane == 0) tc_arrive(&bars.raw_empty[s]);
+          if (lane == 0) {
+            tc_arrive(&bars.raw_empty[s]);
+            tc_arrive(&bars.sc_full[0][st & 1]);
+          }
           ++st;
         }
         if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
@@ -987,7 +1001,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             const int row = 16 * ch + (lane & 15);
             const uint32_t qa =
                 tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
-#pragma unroll(KS >= 4 ? 4 : KS)
+#pragma unroll 2
             for (int ks = 0; ks < KS; ++ks) {
               uint32_t av[4];
               tc_ldm<false>(av, qa + 256 * ks);
@@ -996,73 +1010,90 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             }
           }
           if (kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
-            float* z = zk_s + (par * 4 + kq) * 128 + 16 * ch + n8;
+            float* z = zk_s + (par * 4 + kq) * 64 + 16 * ch + n8;
             z[0] = zc[0] * a.qscale;
-            z[128] = zc[1] * a.qscale;
+            z[64] = zc[1] * a.qscale;
             z[8] = zc[2] * a.qscale;
-            z[136] = zc[3] * a.qscale;
+            z[72] = zc[3] * a.qscale;
           }
         }
         __syncwarp();
         if (lane == 0) tc_arrive(&bars.z_full[par]);
       }
     } else if (warp < 22) {
-      // ==== sums over tokens, of the weights and of the values' zeros: chunks uw, uw + 4,
-      // or with two streams chunk uw of each
+      // ==== values' scales in two parts, and the sums over tokens of the weights and of the
+      // values' zeros: chunk uw of each stream.  A tile is prepared before the sums of
+      // the one before it.
       const int uw = warp - 18, ut = uw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
       float acc[2][4];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-      int it = it0, st = st0;
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int par = it & 1;
-        __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
-        if (t < g.tq) {
-          const int s = st % Ge::NST;
-          const M* vz = reinterpret_cast<const M*>(sm + Ge::S_RING + s * Ge::STAGE + Ge::O_VZ);
-          const int n = (int)min(g.n_q - (long long)t * kTcTile, 128LL);
-          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+      int st = st0;
+#pragma unroll 1
+      for (int t = g.t0; t <= t1; ++t) {
+        if (t < t1) {
+          const int par = (it0 + t - g.t0) & 1;
+          __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
+          if (t < g.tq) {
+            const int s = st % Ge::NST;
+            const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+            const M* vz = reinterpret_cast<const M*>(stg + Ge::O_VZ) + ut * NJ;
+            const M* vs = reinterpret_cast<const M*>(stg + Ge::O_VS) + ut * NJ;
+            __half* sc = reinterpret_cast<__half*>(sm + Ge::S_VSC) + (st & 1) * 8 * 128 + tc_pos<E>(ut);
+            // tokens that do not exist: 0 (their weight 0 times NaN would not be)
+            const bool have = ut < g.n_q - (long long)t * kTcTile;
+            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
+            if (st >= 2) tc_wait(&bars.sc_free[1][st & 1], (st >> 1) - 1, dead);
+#pragma unroll 2
+            for (int j = 0; j < NJ; ++j) {
+              zv[j * Ge::ZLD + tc_pos<E>(ut)] = __float2half_rn(have ? to_f32(vz[j]) : 0.f);
+              tc_split(have ? to_f32(vs[j]) : 0.f, &sc[j * 256], &sc[j * 256 + 128]);
+            }
+            tc_sums_sync();
+            if (lane == 0) {
+              tc_arrive(&bars.raw_empty[s]);
+              tc_arrive(&bars.sc_full[1][st & 1]);
+            }
+            ++st;
+          } else {
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const int i = ut + 128 * j;
-            zv[i % NJ * Ge::ZLD + tc_pos<E>(i / NJ)] =
-                i / NJ < n ? __float2half_rn(to_f32(vz[i])) : __ushort_as_half(0);
+            for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ut] = __ushort_as_half(0);
+            tc_sums_sync();
           }
-          tc_sums_sync();
-          if (lane == 0) tc_arrive(&bars.raw_empty[s]);
-          ++st;
-        } else {
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ut] = __ushort_as_half(0);
-          tc_sums_sync();
         }
-        tc_wait(&bars.p_full[par], it >> 1, dead);
-        const __half* zr = zv + n8 * Ge::ZLD + kq;
-        // 8 x 8 blocks (tokens x rows) of weights, transposed on the way: rows 16 ch + 0 / 8,
+        if (t == g.t0) continue;
+        const int it = it0 + t - 1 - g.t0, par = it & 1;
+        const __half* zr = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
+        // 8 x 8 blocks (tokens x rows) of weights, transposed on the way: rows 16 uw + 0 / 8,
         // tokens 16 ks + 0 / 8
         const int blk = lane >> 3;
-        const uint32_t pbase = tc_smem(sm + Ge::S_P + par * 128 * 128 * 2) + (blk & 1) * 2048 +
+        const uint32_t pbase = tc_smem(sm + Ge::S_P + par * Ge::P_B) + uw * 4096 + (blk & 1) * 2048 +
                                (blk >> 1) * 128 + (lane & 7) * 16;
+        tc_wait(&bars.p_full[par], it >> 1, dead);
+        if (uw < nch) {
+          float x[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int ch = two ? uw : uw + 4 * k;
-          if (ch < nch && (!two || k == par)) {
-            if (s_resc[par][ch]) {
-              const float f0 = f_s[par * 128 + 16 * ch + n8], f1 = f_s[par * 128 + 16 * ch + n8 + 8];
-              acc[k][0] *= f0;
-              acc[k][1] *= f0;
-              acc[k][2] *= f1;
-              acc[k][3] *= f1;
-            }
-#pragma unroll 2
-            for (int ks = 0; ks < 8; ++ks) {
-              uint32_t av[4];
-              tc_ldm<true>(av, pbase + ch * 4096 + ks * 256);
-              tc_mma16816(acc[k], av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
-                          *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
-            }
+          for (int e = 0; e < 4; ++e) x[e] = par ? acc[1][e] : acc[0][e];
+          if (s_resc[par]) {
+            const float f0 = f_s[par * 64 + 16 * uw + n8], f1 = f_s[par * 64 + 16 * uw + n8 + 8];
+            x[0] *= f0;
+            x[1] *= f0;
+            x[2] *= f1;
+            x[3] *= f1;
+          }
+#pragma unroll 4
+          for (int ks = 0; ks < 8; ++ks) {
+            uint32_t av[4];
+            tc_ldm<true>(av, pbase + ks * 256);
+            tc_mma16816(x, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                        *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[0][e] = par ? acc[0][e] : x[e];
+            acc[1][e] = par ? x[e] : acc[1][e];
           }
         }
         __syncwarp();
@@ -1070,60 +1101,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int ch = two ? uw : uw + 4 * k;
-        if (ch < nch) {
-          float* z = lz_s + ((two ? 64 * k : 0) + 16 * ch + n8) * 8 + kq;
+        if (uw < nch) {
+          float* z = lz_s + (64 * k + 16 * uw + n8) * 8 + kq;
           z[0] = acc[k][0];
           z[1] = acc[k][1];
           z[64] = acc[k][2];
           z[65] = acc[k][3];
         }
       }
-    } else if (warp == 22) {
-      // ==== score products
-      const uint32_t id = tc_idesc(nr, false);
-      const uint64_t q_desc = tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
-      const bool one = tc_elect();
-      int it = it0;
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int par = __shfl_sync(0xffffffffu, it & 1, 0);
-        // S may be written again: two tiles ago, or with one buffer the last one
-        if (it >= (two ? 2 : 1))
-          tc_wait(&bars.s_empty[two ? par : par ^ 1], two ? (it >> 1) - 1 : (it - 1) >> 1, dead);
-        tc_wait(&bars.k_full, it, dead);
-        tc_fence_after();
-        const uint32_t d = tmem + kTS + (two ? 64 * par : 0);
-        const bool lo = t < g.tq;
-        if (one) {
-          tc_mma_row<KS>(d, tmem + kTKhi, q_desc, id, false);
-          if (lo) tc_mma_row<KS>(d, tmem + kTKlo, q_desc, id, true);
-          tc_commit(&bars.s_full[par]);
-        }
-        __syncwarp();
-      }
     } else {
-      // ==== value products
-      const uint32_t id = tc_idesc(nr, true);
-      const uint64_t p_desc = tc_desc(tc_smem(sm + Ge::S_P), 128, 2048);
+      // ==== score products (warp 22) and value products (23), by halves of the operand
+      const int vals = warp - 22;
       const bool one = tc_elect();
+      const uint32_t id = tc_idesc(nr, vals);
+      const uint64_t desc = vals ? tc_desc(tc_smem(sm + Ge::S_P), 128, 2048)
+                                 : tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
+      const int halves = vals || D > 32 ? 2 : 1, ksh = (vals ? 8 : KS) / halves;
+      const uint32_t t_a = tmem + (vals ? kTVhi : kTKhi), t_d = tmem + (vals ? kTO : kTS);
       int it = it0;
+#pragma unroll 1
       for (int t = g.t0; t < t1; ++t, ++it) {
         const int par = __shfl_sync(0xffffffffu, it & 1, 0);
-        tc_wait(&bars.v_full, it, dead);
-        tc_wait(&bars.p_full[par], it >> 1, dead);
-        tc_fence_after();
-        const uint64_t pd = p_desc + (par ? 128 * 128 * 2 / 16 : 0);
-        const uint32_t o = tmem + kTO + (two ? 64 * par : 0);
-        const bool lo = t < g.tq, add = t - g.t0 >= (two ? 2 : 1);
-        if (one) {
-          tc_mma_row<8>(o, tmem + kTVhi, pd, id, add);
-          if (lo) tc_mma_row<8>(o, tmem + kTVlo, pd, id, true);
-          tc_commit(&bars.pv_done[par]);
+        const bool lo = t < g.tq;
+        bool add = vals && t - g.t0 >= 2;
+        if (vals)
+          tc_wait(&bars.p_full[par], it >> 1, dead);
+        else if (it >= 2)
+          tc_wait(&bars.s_empty[par], (it >> 1) - 1, dead);
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          tc_wait(&bars.a_full[vals][h], it, dead);
+          tc_fence_after();
+          if (one) {
+            const uint64_t b = desc + (vals ? par * (Ge::P_B / 16) : 0) + h * ksh * 16;
+            const uint32_t aa = t_a + h * ksh * 8;
+#pragma unroll 1
+            for (int pl = 0; pl < (lo ? 2 : 1); ++pl)
+#pragma unroll 2
+              for (int ks = 0; ks < ksh; ++ks) {
+                tc_mma(t_d + 64 * par, aa + 64 * pl + 8 * ks, b + 16 * ks, id, add);
+                add = true;
+              }
+            tc_commit(&bars.a_free[vals][h]);
+            if (h == halves - 1) tc_commit(vals ? &bars.pv_done[par] : &bars.s_full[par]);
+          }
+          add = true;
+          __syncwarp();
         }
-        __syncwarp();
       }
       --it;
-      tc_wait(&bars.pv_done[it & 1], it >> 1, dead);  // and all before it
+      if (vals) tc_wait(&bars.pv_done[it & 1], it >> 1, dead);  // and all before it
     }
     tc_sync_segment();
 
@@ -1134,7 +1161,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       const uint32_t t_lane = tmem + kTO + ((uint32_t)(sw * 32) << 16);
       const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
       // streams that took a tile: by the parity of the block's count
-      const bool u0 = !two || g.nt > 1 || (it0 & 1) == 0, u1 = two && (g.nt > 1 || (it0 & 1) == 1);
+      const bool u0 = g.nt > 1 || (it0 & 1) == 0, u1 = g.nt > 1 || (it0 & 1) == 1;
       const int i1 = s_odd ? min((t1 - g.tq) * kTcTile, g.r + a.N) : 0;
       float* part = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
       __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
