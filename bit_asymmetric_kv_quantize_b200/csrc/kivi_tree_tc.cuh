@@ -36,7 +36,7 @@
 // that held, and the rare tile where it did not raises the references, rescales
 // O^T in tensor memory and forms its weights again.
 //
-// Warps: 4 unpack keys and 4 values (one code), 2 groups of 4 softmax, 2 the
+// Warps: 4 unpack keys and 4 values (one code), 2 groups of 4 softmax, 4 the
 // scales and zeros of keys and the zeros' products with the queries, 4 the
 // scales and zeros of values and the sums over tokens, one issues the score
 // products, one the value products, one the copies (cp.async.bulk of each
@@ -58,7 +58,7 @@ namespace kivi {
 namespace {
 
 constexpr int kTcTile = 128;        // tokens
-constexpr int kTcWarps = 25;
+constexpr int kTcWarps = 27;
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr float kTcSlack = 14.0f;   // log2 units a score may exceed m by
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
@@ -130,21 +130,29 @@ __device__ __forceinline__ void tc_expect(uint64_t* b, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
-// Waits for phase `n` (counted from 0) of a barrier; bounded: each try suspends
-// for up to a microsecond, so some seconds at most.
+// Waits for phase `n` (counted from 0) of a barrier; bounded: a try suspends for a
+// moment, 16 of them make a round, and after 2^20 rounds (some seconds) the block is
+// given up.
 __device__ __forceinline__ void tc_wait(uint64_t* b, int n, volatile int* dead) {
   const uint32_t addr = tc_smem(b), par = (uint32_t)(n & 1);
 #pragma unroll 1
-  for (int tries = 0; tries < (1 << 21); ++tries) {
-    uint32_t ok;
+  for (int rounds = 0; rounds < (1 << 20); ++rounds) {
+    uint32_t left;  // tries left, 0: none of them saw the phase end
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .u32 k;\n\t"
+        "mov.u32 k, 16;\n\t"
+        "TRY:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
+        "@p bra DONE;\n\t"
+        "sub.u32 k, k, 1;\n\t"
+        "setp.ne.u32 p, k, 0;\n\t"
+        "@p bra TRY;\n\t"
+        "DONE:\n\t"
+        "mov.u32 %0, k;\n\t}"
+        : "=r"(left)
         : "r"(addr), "r"(par)
         : "memory");
-    if (ok || *dead) return;
+    if (left != 0 || *dead) return;
   }
   *dead = 1;
 }
@@ -290,9 +298,9 @@ __device__ __forceinline__ void tc_group(int sg) {
   else
     asm volatile("bar.sync 2, 128;" ::: "memory");
 }
-// Barriers of the two warps of the zeros' products, the four that unpack values
-// and the four of the sums.
-__device__ __forceinline__ void tc_pair_sync() { asm volatile("bar.sync 4, 64;" ::: "memory"); }
+// Barriers of the four warps of the zeros' products, of those that unpack values
+// and of those of the sums.
+__device__ __forceinline__ void tc_zeros_sync() { asm volatile("bar.sync 4, 128;" ::: "memory"); }
 __device__ __forceinline__ void tc_values_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
 __device__ __forceinline__ void tc_sums_sync() { asm volatile("bar.sync 5, 128;" ::: "memory"); }
 // Barrier of the group that tells whether any of its threads has `x`.
@@ -430,8 +438,8 @@ __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, 
                                           const uint4* hi, const uint4* lo, int units) {
   using U = TcUnit<BITS>;
   constexpr int H = U::kUnit / 16;
-#pragma unroll 1
-  for (int u = units; u > 0; --u) {
+#pragma unroll(H == 2 ? 1 : 2)
+  for (int u = 0; u < units; ++u) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
     for (int i = 0; i < U::kUnitW; ++i) w[i] = words[i * stride];
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   const int nr = p.rb, nch = nr / 16;
 
   // ---- set-up
-  if (warp == 22) {
+  if (warp == 24) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      tc_smem(&s_tmem))
                  : "memory");
@@ -636,12 +644,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     for (int i = 0; i < 2; ++i) s_poison[i] = 0;
     for (int i = 0; i < 3; ++i) {
       tc_bar_init(&bars.raw_full[i], 1);
-      tc_bar_init(&bars.raw_empty[i], 14);
+      tc_bar_init(&bars.raw_empty[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
-      tc_bar_init(&bars.sc_full[0][i], 2);
-      tc_bar_init(&bars.sc_full[1][i], 4);
       for (int k = 0; k < 2; ++k) {
+        tc_bar_init(&bars.sc_full[k][i], 4);
         tc_bar_init(&bars.sc_free[k][i], 4);
         tc_bar_init(&bars.a_full[k][i], 4);
         tc_bar_init(&bars.a_free[k][i], 1);
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       tc_bar_init(&bars.p_full[i], 4);
       tc_bar_init(&bars.pv_done[i], 1);
       tc_bar_init(&bars.h_done[i], 4);
-      tc_bar_init(&bars.z_full[i], 2);
+      tc_bar_init(&bars.z_full[i], 4);
       tc_bar_init(&bars.z_empty[i], 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     return g;
   };
 
-  if (warp == 24) {
+  if (warp == 26) {
     // ==== copies: runs ahead over all segments; the ring alone holds it back.
     // Lane i < 4 copies subtile i.
     int st = 0;
@@ -743,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   // ==== segments
   // counters of this block: tiles, and tiles that went through the ring
   int it0 = 0, st0 = 0;
-  for (int seg = 0; warp < 24 && walk.left > 0; ++seg) {
+  for (int seg = 0; warp < 26 && walk.left > 0; ++seg) {
     const TcSeg g = next_seg(walk);
     const int t1 = g.t0 + g.nt;
     // ---- start of a segment: queries, mask, references, pages
@@ -891,22 +898,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             float v[16];
             tc_ld16(t_lane + kTS + ch * 16, v);
             const uint32_t sees = seen(ch);
-            uint32_t w[8];
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
               const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
-              const float oo[4] = {o.x, o.y, o.z, o.w};
-              float e[4];
+              v[4 * e4] = fmaf(v[4 * e4], c1, -o.x);
+              v[4 * e4 + 1] = fmaf(v[4 * e4 + 1], c1, -o.y);
+              v[4 * e4 + 2] = fmaf(v[4 * e4 + 2], c1, -o.z);
+              v[4 * e4 + 3] = fmaf(v[4 * e4 + 3], c1, -o.w);
+            }
+            if (__any_sync(0xffffffffu, sees != 0xFFFFu)) {  // raw tokens, or the end
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float d = fmaf(v[4 * e4 + k], c1, -oo[k]);
-                if (!((sees >> (4 * e4 + k)) & 1u)) d = -__builtin_huge_valf();
-                over = fmaxf(over, d);
-                e[k] = tc_ex2(d);
-              }
-              const __half2 h0 = __floats2half2_rn(e[0], e[1]), h1 = __floats2half2_rn(e[2], e[3]);
-              w[2 * e4] = *reinterpret_cast<const uint32_t*>(&h0);
-              w[2 * e4 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+              for (int e = 0; e < 16; ++e)
+                if (!((sees >> e) & 1u)) v[e] = -__builtin_huge_valf();
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              over = fmaxf(over, fmaxf(v[e], v[e + 1]));
+              const __half2 h = __floats2half2_rn(tc_ex2(v[e]), tc_ex2(v[e + 1]));
+              w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
             }
             *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -960,9 +970,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           tc_arrive(&bars.z_empty[sg]);
         }
       }
-    } else if (warp < 18) {
-      // ==== keys' scales in two parts, and sum_d q_d z_gd of the tile's four groups:
-      // 16-row chunks zw, zw + 2
+    } else if (warp < 20) {
+      // ==== keys' scales in two parts, and sum_d q_d z_gd of the tile's four groups for
+      // 16-row chunk zw
       const int zw = warp - 16, zt = zw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
       int it = it0, st = st0;
       for (int t = g.t0; t < t1; ++t, ++it) {
@@ -978,12 +988,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
           if (st >= 2) tc_wait(&bars.sc_free[0][st & 1], (st >> 1) - 1, dead);
 #pragma unroll 2
-          for (int j = 0; j < 4 * D / 64; ++j) {
-            const int i = zt + 64 * j, gr = i / D, c = tc_pos<E>(i % D);
+          for (int j = 0; j < 4 * D / 128; ++j) {
+            const int i = zt + 128 * j, gr = i / D, c = tc_pos<E>(i % D);
             zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(kz[i]));
             tc_split(to_f32(ks[i]), &sc[gr * 2 * D + c], &sc[gr * 2 * D + D + c]);
           }
-          tc_pair_sync();
+          tc_zeros_sync();
           if (lane == 0) {
             tc_arrive(&bars.raw_empty[s]);
             tc_arrive(&bars.sc_full[0][st & 1]);
@@ -993,15 +1003,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
         // lane n8 of a column reads group n8's row; columns 4 .. 7 are read by nobody
         const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
-#pragma unroll 1
-        for (int ch = zw; ch < nch; ch += 2) {
+        if (zw < nch) {
+          const int ch = zw;
           float zc[4] = {0.f, 0.f, 0.f, 0.f};
           if (!raw) {
             // rows 16 ch + (lane % 16), channels 16 ks + 8 (lane / 16)
             const int row = 16 * ch + (lane & 15);
             const uint32_t qa =
                 tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
-#pragma unroll 2
+#pragma unroll 4
             for (int ks = 0; ks < KS; ++ks) {
               uint32_t av[4];
               tc_ldm<false>(av, qa + 256 * ks);
@@ -1020,11 +1030,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         __syncwarp();
         if (lane == 0) tc_arrive(&bars.z_full[par]);
       }
-    } else if (warp < 22) {
+    } else if (warp < 24) {
       // ==== values' scales in two parts, and the sums over tokens of the weights and of the
       // values' zeros: chunk uw of each stream.  A tile is prepared before the sums of
       // the one before it.
-      const int uw = warp - 18, ut = uw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
+      const int uw = warp - 20, ut = uw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
       float acc[2][4];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -1110,8 +1120,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         }
       }
     } else {
-      // ==== score products (warp 22) and value products (23), by halves of the operand
-      const int vals = warp - 22;
+      // ==== score products (warp 24) and value products (25), by halves of the operand
+      const int vals = warp - 24;
       const bool one = tc_elect();
       const uint32_t id = tc_idesc(nr, vals);
       const uint64_t desc = vals ? tc_desc(tc_smem(sm + Ge::S_P), 128, 2048)
@@ -1219,7 +1229,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   }
 
   __syncthreads();
-  if (warp == 22) {
+  if (warp == 24) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
