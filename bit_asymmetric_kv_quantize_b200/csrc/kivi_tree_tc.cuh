@@ -119,30 +119,29 @@ __host__ __device__ constexpr int tc_elem(int k) {
 __device__ __forceinline__ uint32_t tc_smem(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ void tc_bar_init(uint64_t* b, int n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(tc_smem(b)), "r"(n) : "memory");
+// Barriers go by their 32-bit shared address.
+__device__ __forceinline__ void tc_bar_init(uint32_t b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
 }
-__device__ __forceinline__ void tc_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(b)) : "memory");
+__device__ __forceinline__ void tc_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
 }
-__device__ __forceinline__ void tc_expect(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(b)),
-               "r"(bytes)
+__device__ __forceinline__ void tc_expect(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
                : "memory");
 }
-// Waits for phase `n` (counted from 0) of a barrier; bounded: a try suspends for a
-// moment, 16 of them make a round, and after 2^20 rounds (some seconds) the block is
-// given up.
-__device__ __forceinline__ void tc_wait(uint64_t* b, int n, volatile int* dead) {
-  const uint32_t addr = tc_smem(b), par = (uint32_t)(n & 1);
+// Waits for phase `n` (counted from 0) of a barrier; bounded: rounds of 4096 tries,
+// between which a dead block gives up, and some seconds of them in all.  (Tries
+// without a time limit: with one they sleep, and wake late.)
+__device__ __forceinline__ void tc_wait(uint32_t b, int n, volatile int* dead) {
 #pragma unroll 1
-  for (int rounds = 0; rounds < (1 << 20); ++rounds) {
+  for (int rounds = 0; rounds < (1 << 15); ++rounds) {
     uint32_t left;  // tries left, 0: none of them saw the phase end
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .u32 k;\n\t"
-        "mov.u32 k, 16;\n\t"
+        "mov.u32 k, 4096;\n\t"
         "TRY:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra DONE;\n\t"
         "sub.u32 k, k, 1;\n\t"
         "setp.ne.u32 p, k, 0;\n\t"
@@ -150,17 +149,17 @@ __device__ __forceinline__ void tc_wait(uint64_t* b, int n, volatile int* dead) 
         "DONE:\n\t"
         "mov.u32 %0, k;\n\t}"
         : "=r"(left)
-        : "r"(addr), "r"(par)
+        : "r"(b), "r"(n & 1)
         : "memory");
     if (left != 0 || *dead) return;
   }
   *dead = 1;
 }
-__device__ __forceinline__ void tc_copy(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
+__device__ __forceinline__ void tc_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t b) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          tc_smem(dst)),
-      "l"(src), "r"(bytes), "r"(tc_smem(b))
+          dst),
+      "l"(src), "r"(bytes), "r"(b)
       : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() {
@@ -234,9 +233,8 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-__device__ __forceinline__ void tc_commit(uint64_t* b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   tc_smem(b))
+__device__ __forceinline__ void tc_commit(uint32_t b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b)
                : "memory");
 }
 // A row of K-slices of one product: 8 columns of A and 256 bytes of B each.
@@ -575,15 +573,16 @@ __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, in
 // Tensor-memory columns.
 constexpr uint32_t kTKhi = 0, kTKlo = 64, kTVhi = 128, kTVlo = 192, kTO = 256, kTS = 384;
 
-struct TcBars {
-  uint64_t raw_full[3], raw_empty[3];
+// Barriers, 8 bytes each, by their number.
+struct TcBar {
+  static constexpr int raw_full = 0, raw_empty = 3;  // [stage]
   // scales' parts set out for the unpacking warps: [keys, values][tile parity]
-  uint64_t sc_full[2][2], sc_free[2][2];
+  static constexpr int sc_full = 6, sc_free = 10;
   // halves of the operands in tensor memory: [keys, values][half]
-  uint64_t a_full[2][2], a_free[2][2];
-  uint64_t s_full[2], s_empty[2];
-  uint64_t p_full[2], pv_done[2], h_done[2];
-  uint64_t z_full[2], z_empty[2];
+  static constexpr int a_full = 14, a_free = 18;
+  static constexpr int s_full = 22, s_empty = 24;  // [stream], and those that follow
+  static constexpr int p_full = 26, pv_done = 28, h_done = 30, z_full = 32, z_empty = 34;
+  static constexpr int N = 36;
 };
 
 // One segment: tiles [t0, t0 + nt) of a group.
@@ -605,13 +604,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   constexpr int E = Ge::E, WK = Ge::WK, NJ = Ge::NJ;
   constexpr int KS = D / 16;  // k-slices of the scores
   extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ TcBars bars;
+  __shared__ uint64_t s_bars[TcBar::N];
   __shared__ TcWalk s_walk;
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
   __shared__ int s_poison[2];   // [segment parity]
   __shared__ int s_resc[2];     // [stream]: the tile's rows were rescaled
   volatile int* dead = &s_dead;
+  const uint32_t bar0 = tc_smem(s_bars), sm0 = tc_smem(sm);
+  auto bar = [&](int k) -> uint32_t { return bar0 + 8u * (uint32_t)k; };
   // what a whole warp shares is broadcast, so that it lives in uniform registers
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
@@ -643,23 +644,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     s_dead = 0;
     for (int i = 0; i < 2; ++i) s_poison[i] = 0;
     for (int i = 0; i < 3; ++i) {
-      tc_bar_init(&bars.raw_full[i], 1);
-      tc_bar_init(&bars.raw_empty[i], 16);
+      tc_bar_init(bar(TcBar::raw_full + i), 1);
+      tc_bar_init(bar(TcBar::raw_empty + i), 16);
     }
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 2; ++k) {
-        tc_bar_init(&bars.sc_full[k][i], 4);
-        tc_bar_init(&bars.sc_free[k][i], 4);
-        tc_bar_init(&bars.a_full[k][i], 4);
-        tc_bar_init(&bars.a_free[k][i], 1);
+        tc_bar_init(bar(TcBar::sc_full + 2 * k + i), 4);
+        tc_bar_init(bar(TcBar::sc_free + 2 * k + i), 4);
+        tc_bar_init(bar(TcBar::a_full + 2 * k + i), 4);
+        tc_bar_init(bar(TcBar::a_free + 2 * k + i), 1);
       }
-      tc_bar_init(&bars.s_full[i], 1);
-      tc_bar_init(&bars.s_empty[i], 4);
-      tc_bar_init(&bars.p_full[i], 4);
-      tc_bar_init(&bars.pv_done[i], 1);
-      tc_bar_init(&bars.h_done[i], 4);
-      tc_bar_init(&bars.z_full[i], 4);
-      tc_bar_init(&bars.z_empty[i], 4);
+      tc_bar_init(bar(TcBar::s_full + i), 1);
+      tc_bar_init(bar(TcBar::s_empty + i), 4);
+      tc_bar_init(bar(TcBar::p_full + i), 4);
+      tc_bar_init(bar(TcBar::pv_done + i), 1);
+      tc_bar_init(bar(TcBar::h_done + i), 4);
+      tc_bar_init(bar(TcBar::z_full + i), 4);
+      tc_bar_init(bar(TcBar::z_empty + i), 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -715,17 +716,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       const TcSeg g = next_seg(walk);
       for (int t = g.t0; t < min(g.t0 + g.nt, g.tq); ++t, ++st) {
         const int s = st % Ge::NST;
-        if (st >= Ge::NST) tc_wait(&bars.raw_empty[s], st / Ge::NST - 1, dead);
+        if (st >= Ge::NST) tc_wait(bar(TcBar::raw_empty + s), st / Ge::NST - 1, dead);
         const long long tile = t * 4LL + lane;
         long long su = 0, stl = 0;
         const bool have = lane < 4 && tile < g.n_q / kTile && store_tile(a.c, g.unit, tile, &su, &stl);
         const int n = __popc(__ballot_sync(0xffffffffu, have));
-        uint64_t* fb = &bars.raw_full[s];
+        const uint32_t fb = bar(TcBar::raw_full + s);
         if (lane == 0) tc_expect(fb, n * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM));
         __syncwarp();
         if (have && !*dead) {
           using Lt = Layout<D, BITS>;
-          unsigned char* dst = sm + Ge::S_RING + s * Ge::STAGE;
+          const uint32_t dst = sm0 + Ge::S_RING + s * Ge::STAGE;
           const long long km = su * Lt::k_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::KM;
           const long long vm = su * Lt::v_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::VM;
           tc_copy(dst + Ge::O_KC + lane * Ge::KC,
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     // block has stages without copies, whose waits run out)
     int never = 0;
     for (int i = max(st - Ge::NST, 0); i < st; ++i)
-      tc_wait(&bars.raw_full[i % Ge::NST], i / Ge::NST, &never);
+      tc_wait(bar(TcBar::raw_full + (i % Ge::NST)), i / Ge::NST, &never);
     __syncwarp();
   }
 
@@ -811,8 +812,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         const __half* src = nullptr;
         if (!raw) {
           // (the scales' writers have waited for the copies)
-          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-          tc_wait(&bars.sc_full[vals][st & 1], st >> 1, dead);
+          tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
+          tc_wait(bar(TcBar::sc_full + 2 * vals + (st & 1)), st >> 1, dead);
         } else if (!vals) {
           // raw tokens: the window, then the drafted ones; halved like s
           const int i = first + w * 32 + lane;
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         const __half* sc = sc0 + (st & 1) * 8 * n_codes;
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
-          if (it > 0) tc_wait(&bars.a_free[vals][h], it - 1, dead);
+          if (it > 0) tc_wait(bar(TcBar::a_free + 2 * vals + h), it - 1, dead);
           tc_fence_after();
           if (!act) {
           } else if (!raw) {
@@ -845,12 +846,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc_arrive(&bars.a_full[vals][h]);
+          if (lane == 0) tc_arrive(bar(TcBar::a_full + 2 * vals + h));
         }
         if (!raw) {
           if (lane == 0) {
-            tc_arrive(&bars.raw_empty[s]);
-            tc_arrive(&bars.sc_free[vals][st & 1]);
+            tc_arrive(bar(TcBar::raw_empty + s));
+            tc_arrive(bar(TcBar::sc_free + 2 * vals + (st & 1)));
           }
           ++st;
         } else if (vals) {
@@ -880,11 +881,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         };
         // what the products of the stream's last tile read may be written again
         if (it >= 2) {
-          tc_wait(&bars.pv_done[sg], (it >> 1) - 1, dead);
-          tc_wait(&bars.h_done[sg], (it >> 1) - 1, dead);
+          tc_wait(bar(TcBar::pv_done + sg), (it >> 1) - 1, dead);
+          tc_wait(bar(TcBar::h_done + sg), (it >> 1) - 1, dead);
         }
-        tc_wait(&bars.z_full[sg], it >> 1, dead);
-        tc_wait(&bars.s_full[sg], it >> 1, dead);
+        tc_wait(bar(TcBar::z_full + sg), it >> 1, dead);
+        tc_wait(bar(TcBar::s_full + sg), it >> 1, dead);
         tc_fence_after();
         bool resc = false;
 #pragma unroll 1
@@ -965,9 +966,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         tc_fence_smem();
         __syncwarp();
         if (lane == 0) {
-          tc_arrive(&bars.p_full[sg]);
-          tc_arrive(&bars.s_empty[sg]);
-          tc_arrive(&bars.z_empty[sg]);
+          tc_arrive(bar(TcBar::p_full + sg));
+          tc_arrive(bar(TcBar::s_empty + sg));
+          tc_arrive(bar(TcBar::z_empty + sg));
         }
       }
     } else if (warp < 20) {
@@ -985,8 +986,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
           const M* ks = reinterpret_cast<const M*>(stg + Ge::O_KS);
           __half* sc = reinterpret_cast<__half*>(sm + Ge::S_KSC) + (st & 1) * 8 * D;
-          tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-          if (st >= 2) tc_wait(&bars.sc_free[0][st & 1], (st >> 1) - 1, dead);
+          tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
+          if (st >= 2) tc_wait(bar(TcBar::sc_free + (st & 1)), (st >> 1) - 1, dead);
 #pragma unroll 2
           for (int j = 0; j < 4 * D / 128; ++j) {
             const int i = zt + 128 * j, gr = i / D, c = tc_pos<E>(i % D);
@@ -995,12 +996,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           }
           tc_zeros_sync();
           if (lane == 0) {
-            tc_arrive(&bars.raw_empty[s]);
-            tc_arrive(&bars.sc_full[0][st & 1]);
+            tc_arrive(bar(TcBar::raw_empty + s));
+            tc_arrive(bar(TcBar::sc_full + (st & 1)));
           }
           ++st;
         }
-        if (it >= 2) tc_wait(&bars.z_empty[par], (it >> 1) - 1, dead);
+        if (it >= 2) tc_wait(bar(TcBar::z_empty + par), (it >> 1) - 1, dead);
         // lane n8 of a column reads group n8's row; columns 4 .. 7 are read by nobody
         const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
         if (zw < nch) {
@@ -1010,7 +1011,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             // rows 16 ch + (lane % 16), channels 16 ks + 8 (lane / 16)
             const int row = 16 * ch + (lane & 15);
             const uint32_t qa =
-                tc_smem(sm + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
+                (sm0 + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
 #pragma unroll 4
             for (int ks = 0; ks < KS; ++ks) {
               uint32_t av[4];
@@ -1028,7 +1029,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           }
         }
         __syncwarp();
-        if (lane == 0) tc_arrive(&bars.z_full[par]);
+        if (lane == 0) tc_arrive(bar(TcBar::z_full + par));
       }
     } else if (warp < 24) {
       // ==== values' scales in two parts, and the sums over tokens of the weights and of the
@@ -1054,8 +1055,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             __half* sc = reinterpret_cast<__half*>(sm + Ge::S_VSC) + (st & 1) * 8 * 128 + tc_pos<E>(ut);
             // tokens that do not exist: 0 (their weight 0 times NaN would not be)
             const bool have = ut < g.n_q - (long long)t * kTcTile;
-            tc_wait(&bars.raw_full[s], st / Ge::NST, dead);
-            if (st >= 2) tc_wait(&bars.sc_free[1][st & 1], (st >> 1) - 1, dead);
+            tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
+            if (st >= 2) tc_wait(bar(TcBar::sc_free + 2 + (st & 1)), (st >> 1) - 1, dead);
 #pragma unroll 2
             for (int j = 0; j < NJ; ++j) {
               zv[j * Ge::ZLD + tc_pos<E>(ut)] = __float2half_rn(have ? to_f32(vz[j]) : 0.f);
@@ -1063,8 +1064,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             }
             tc_sums_sync();
             if (lane == 0) {
-              tc_arrive(&bars.raw_empty[s]);
-              tc_arrive(&bars.sc_full[1][st & 1]);
+              tc_arrive(bar(TcBar::raw_empty + s));
+              tc_arrive(bar(TcBar::sc_full + 2 + (st & 1)));
             }
             ++st;
           } else {
@@ -1079,9 +1080,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         // 8 x 8 blocks (tokens x rows) of weights, transposed on the way: rows 16 uw + 0 / 8,
         // tokens 16 ks + 0 / 8
         const int blk = lane >> 3;
-        const uint32_t pbase = tc_smem(sm + Ge::S_P + par * Ge::P_B) + uw * 4096 + (blk & 1) * 2048 +
+        const uint32_t pbase = (sm0 + Ge::S_P + par * Ge::P_B) + uw * 4096 + (blk & 1) * 2048 +
                                (blk >> 1) * 128 + (lane & 7) * 16;
-        tc_wait(&bars.p_full[par], it >> 1, dead);
+        tc_wait(bar(TcBar::p_full + par), it >> 1, dead);
         if (uw < nch) {
           float x[4];
 #pragma unroll
@@ -1107,7 +1108,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           }
         }
         __syncwarp();
-        if (lane == 0) tc_arrive(&bars.h_done[par]);
+        if (lane == 0) tc_arrive(bar(TcBar::h_done + par));
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -1124,8 +1125,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       const int vals = warp - 24;
       const bool one = tc_elect();
       const uint32_t id = tc_idesc(nr, vals);
-      const uint64_t desc = vals ? tc_desc(tc_smem(sm + Ge::S_P), 128, 2048)
-                                 : tc_desc(tc_smem(sm + Ge::S_Q), 128, D * 16);
+      const uint64_t desc = vals ? tc_desc((sm0 + Ge::S_P), 128, 2048)
+                                 : tc_desc((sm0 + Ge::S_Q), 128, D * 16);
       const int halves = vals || D > 32 ? 2 : 1, ksh = (vals ? 8 : KS) / halves;
       const uint32_t t_a = tmem + (vals ? kTVhi : kTKhi), t_d = tmem + (vals ? kTO : kTS);
       int it = it0;
@@ -1135,12 +1136,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         const bool lo = t < g.tq;
         bool add = vals && t - g.t0 >= 2;
         if (vals)
-          tc_wait(&bars.p_full[par], it >> 1, dead);
+          tc_wait(bar(TcBar::p_full + par), it >> 1, dead);
         else if (it >= 2)
-          tc_wait(&bars.s_empty[par], (it >> 1) - 1, dead);
+          tc_wait(bar(TcBar::s_empty + par), (it >> 1) - 1, dead);
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
-          tc_wait(&bars.a_full[vals][h], it, dead);
+          tc_wait(bar(TcBar::a_full + 2 * vals + h), it, dead);
           tc_fence_after();
           if (one) {
             const uint64_t b = desc + (vals ? par * (Ge::P_B / 16) : 0) + h * ksh * 16;
@@ -1152,15 +1153,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 tc_mma(t_d + 64 * par, aa + 64 * pl + 8 * ks, b + 16 * ks, id, add);
                 add = true;
               }
-            tc_commit(&bars.a_free[vals][h]);
-            if (h == halves - 1) tc_commit(vals ? &bars.pv_done[par] : &bars.s_full[par]);
+            tc_commit(bar(TcBar::a_free + 2 * vals + h));
+            if (h == halves - 1) tc_commit(vals ? bar(TcBar::pv_done + par) : bar(TcBar::s_full + par));
           }
           add = true;
           __syncwarp();
         }
       }
       --it;
-      if (vals) tc_wait(&bars.pv_done[it & 1], it >> 1, dead);  // and all before it
+      if (vals) tc_wait(bar(TcBar::pv_done + (it & 1)), it >> 1, dead);  // and all before it
     }
     tc_sync_segment();
 
