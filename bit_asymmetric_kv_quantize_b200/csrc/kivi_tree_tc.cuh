@@ -36,18 +36,21 @@
 // that held, and the rare tile where it did not raises the references, rescales
 // O^T in tensor memory and forms its weights again.
 //
-// Warps: 4 unpack keys and 4 values (one code), 2 groups of 4 softmax, 4 the
-// scales and zeros of keys and the zeros' products with the queries, 4 the
-// scales and zeros of values and the sums over tokens, one issues the score
-// products, one the value products, one the copies (cp.async.bulk of each
-// tile's ranges into a ring).  The two softmax groups take every other tile,
-// each with its own S^T, O^T and references (two streams, joined at the end of
-// a segment), so that one's latencies hide behind the other.  Operands are
-// handed over by halves, so that one half is unpacked while the products of the
-// other run.  A role's code is a small loop: together they have to fit the
-// instruction cache (with the roles unrolled, 369 KB of code, the kernel took
-// four times as long).  All waits are bounded: one that runs out marks the block
-// dead, whose further waits return at once and whose results are NaN.
+// Sixteen warps walk through a tile's work together, two barriers of the block a
+// tile (no polling); warp w has lanes 32 (w % 4) .. + 31 of tensor memory and a
+// quarter w / 4 of the columns:
+//   a  set out scales and zeros: keys' of the next tile, values' of this one
+//   b  unpack the next tile's keys; its zeros' products
+//   c  this tile's weights (its scores were begun a tile ago)
+//   d  unpack this tile's values
+//   f  (a further warp issues the next scores and this tile's value products)
+//      sums over this tile's tokens
+// One more warp issues the copies (cp.async.bulk of each tile's ranges into a ring).
+// With a role to each warp instead, handing over by mbarriers, the same work took
+// twice as long: the waiting warps' polling and their different code filled the
+// issue slots and the instruction cache.  Waits on copies and matrix instructions
+// are bounded: one that runs out marks the block dead, whose further waits return
+// soon and whose results are NaN.
 #pragma once
 
 #include <type_traits>
@@ -58,7 +61,8 @@ namespace kivi {
 namespace {
 
 constexpr int kTcTile = 128;        // tokens
-constexpr int kTcWarps = 27;
+constexpr int kTcWorkers = 512;
+constexpr int kTcWarps = 18;  // workers, matrix instructions, copies
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr float kTcSlack = 14.0f;   // log2 units a score may exceed m by
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
@@ -80,27 +84,27 @@ struct TcGeo {
   static constexpr int O_VS = O_VC + 4 * VC;
   static constexpr int O_VZ = O_VS + 4 * VM;
   static constexpr int STAGE = O_VZ + 4 * VM;
-  static constexpr int NST = 3;
+  static constexpr int NST = 4;
   // shared memory
   static constexpr int S_RING = 0;
   static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
   static constexpr int S_P = S_Q + 64 * D * 2;           // 2 x [64 rows][128 tokens]
   static constexpr int P_B = 64 * 128 * 2;
   static constexpr int S_RAW = S_P + 2 * P_B;            // raw values [128 tokens][D]
-  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 2 x 4 groups x D x (hi, lo) halves
-  static constexpr int S_VSC = S_KSC + 2 * 4 * D * 4;    // 2 x 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // 2 x [4 groups][64 rows] float
-  static constexpr int S_OFF = S_ZK + 2 * 4 * 64 * 4;    // [2 streams][4 warps][64 rows] float
-  static constexpr int S_WMAX = S_OFF + 2 * 4 * 64 * 4;  // the same
-  static constexpr int S_M = S_WMAX + 2 * 4 * 64 * 4;    // [2 streams][64 rows]
-  static constexpr int S_F = S_M + 2 * 64 * 4;           // the same
-  static constexpr int S_LZ = S_F + 2 * 64 * 4;          // [2 streams][64 rows][8]
-  static constexpr int S_MASK = S_LZ + 2 * 64 * 8 * 4;   // [256][8] words
+  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 4 groups x D x (hi, lo) halves
+  static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 4 groups x 128 x (hi, lo)
+  static constexpr int S_ZK = S_VSC + 4 * 128 * 4;       // 2 x [4 parts][4 groups][64 rows] float
+  static constexpr int S_OFF = S_ZK + 2 * 16 * 64 * 4;   // [16 warps][16 rows]
+  static constexpr int S_WMAX = S_OFF + 16 * 16 * 4;     // [4 groups][64 rows]
+  static constexpr int S_M = S_WMAX + 4 * 64 * 4;        // [64 rows]
+  static constexpr int S_F = S_M + 64 * 4;               // [64 rows]
+  static constexpr int S_LZ = S_F + 64 * 4;              // [4 parts][64 rows][8]
+  static constexpr int S_MASK = S_LZ + 4 * 64 * 8 * 4;   // [256][8] words
   // zeros as binary16 in operand order, rows padded against bank conflicts:
   // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
   static constexpr int ZLD = 136;
   static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
-  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;    // 2 x (both tables)
+  static constexpr int S_ZV = S_ZH + 4 * ZLD * 2;        // 2 x
   static constexpr int BYTES = S_ZV + 2 * 8 * ZLD * 2;
 };
 
@@ -283,41 +287,22 @@ __device__ __forceinline__ void tc_ldm(uint32_t (&a)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// All warps but the copying one, which runs ahead over the segments.
-__device__ __forceinline__ void tc_sync_segment() {
+// Barriers: of the workers (1), and of the block with a vote (2: a thread's `x`).
+__device__ __forceinline__ void tc_sync_workers() {
   tc_fence_before();
-  asm volatile("bar.sync 3, %0;" ::"n"(kTcThreads - 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kTcWorkers) : "memory");
   tc_fence_after();
 }
-// Barrier of softmax group `sg` (barriers 1 and 2).
-__device__ __forceinline__ void tc_group(int sg) {
-  if (sg == 0)
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-  else
-    asm volatile("bar.sync 2, 128;" ::: "memory");
-}
-// Barriers of the four warps of the zeros' products, of those that unpack values
-// and of those of the sums.
-__device__ __forceinline__ void tc_zeros_sync() { asm volatile("bar.sync 4, 128;" ::: "memory"); }
-__device__ __forceinline__ void tc_values_sync() { asm volatile("bar.sync 6, 128;" ::: "memory"); }
-__device__ __forceinline__ void tc_sums_sync() { asm volatile("bar.sync 5, 128;" ::: "memory"); }
-// Barrier of the group that tells whether any of its threads has `x`.
-__device__ __forceinline__ bool tc_group_any(int sg, bool x) {
+__device__ __forceinline__ bool tc_sync_any(bool x) {
   uint32_t r;
-  if (sg == 0)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred.aligned q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x)
-        : "memory");
+  tc_fence_before();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kTcThreads)
+      : "memory");
+  tc_fence_after();
   return r != 0;
 }
 
@@ -337,32 +322,48 @@ __device__ __forceinline__ uint32_t tc_hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-template <int E_BIT>
-__device__ __forceinline__ uint32_t tc_code(uint32_t masked) {
-  if constexpr (E_BIT == 0) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(masked | 0x64006400u), "r"(0xE400E400u));
-    return d;
-  } else {
-    constexpr uint32_t inv = (uint32_t)(15 - E_BIT) << 10;            // 2^-e
-    constexpr uint32_t off = 0x8000u | ((uint32_t)(25 - E_BIT) << 10);  // -2^(10 - e)
-    return tc_hfma2(masked | 0x64006400u, inv | (inv << 16), off | (off << 16));
+// The constants stand in registers that the compiler does not see through: it would
+// form them again for each pair (an instruction each, a third of the unpacking).
+struct TcConst {
+  uint32_t magic;           // 1024 in both halves
+  uint32_t inv[10], off[10];  // 2^-e and -2^(10 - e)
+};
+__device__ __forceinline__ TcConst tc_const() {
+  TcConst k;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k.magic));
+#pragma unroll
+  for (int e = 1; e < 10; ++e) {
+    k.inv[e] = ((15u - e) << 10) * 0x00010001u;
+    k.off[e] = (0x8000u | (25u - e) << 10) * 0x00010001u;
+    asm volatile("" : "+r"(k.inv[e]), "+r"(k.off[e]));
   }
+  return k;
+}
+// (x & m) | magic, then 1024 + c 2^e to c.
+template <int E_BIT>
+__device__ __forceinline__ uint32_t tc_code(uint32_t x, uint32_t m, const TcConst& k) {
+  uint32_t d, y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(m), "r"(k.magic));
+  if constexpr (E_BIT == 0)
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(y), "r"(0xE400E400u));
+  else
+    d = tc_hfma2(y, k.inv[E_BIT], k.off[E_BIT]);
+  return d;
 }
 // Pair I of a block whose words are w[0 .. WB).
 template <int BITS, int I>
-__device__ __forceinline__ uint32_t tc_pair(const uint32_t* w) {
+__device__ __forceinline__ uint32_t tc_pair(const uint32_t* w, const TcConst& k) {
   if constexpr (BITS == 3) {
     constexpr int e = I & 7, sh = I < 8 ? 0 : 8;
     constexpr uint32_t m = 0x00010001u << e;
     const uint32_t p = ((w[0] >> sh) & m) | (((w[1] >> sh) << 1) & (m << 1)) |
                        (((w[2] >> sh) << 2) & (m << 2));
-    return tc_code<e>(p);
+    return tc_code<e>(p, 0xFFFFFFFFu, k);
   } else {
     constexpr int per = 10 / BITS;  // pairs whose codes end below bit 10 of the half
     constexpr int sh = I / per * per * BITS, e = I % per * BITS;
     constexpr uint32_t m = ((1u << BITS) - 1u) * 0x00010001u << e;
-    return tc_code<e>((sh ? w[0] >> sh : w[0]) & m);
+    return tc_code<e>(sh ? w[0] >> sh : w[0], m, k);
   }
 }
 // What a loop over a lane's words takes at a time: kUnit codes in kUnitW words.
@@ -374,25 +375,25 @@ struct TcUnit {
 };
 // 16 of a unit's codes, registers 8 HALF .. of its part of the operand row.
 template <int BITS, int HALF>
-__device__ __forceinline__ void tc_codes16(const uint32_t* w, uint32_t (&c)[8]) {
+__device__ __forceinline__ void tc_codes16(const uint32_t* w, uint32_t (&c)[8], const TcConst& k) {
   if constexpr (BITS == 4) {
-    c[0] = tc_pair<4, 0>(w);
-    c[1] = tc_pair<4, 1>(w);
-    c[2] = tc_pair<4, 2>(w);
-    c[3] = tc_pair<4, 3>(w);
-    c[4] = tc_pair<4, 0>(w + 1);
-    c[5] = tc_pair<4, 1>(w + 1);
-    c[6] = tc_pair<4, 2>(w + 1);
-    c[7] = tc_pair<4, 3>(w + 1);
+    c[0] = tc_pair<4, 0>(w, k);
+    c[1] = tc_pair<4, 1>(w, k);
+    c[2] = tc_pair<4, 2>(w, k);
+    c[3] = tc_pair<4, 3>(w, k);
+    c[4] = tc_pair<4, 0>(w + 1, k);
+    c[5] = tc_pair<4, 1>(w + 1, k);
+    c[6] = tc_pair<4, 2>(w + 1, k);
+    c[7] = tc_pair<4, 3>(w + 1, k);
   } else {
-    c[0] = tc_pair<BITS, 8 * HALF + 0>(w);
-    c[1] = tc_pair<BITS, 8 * HALF + 1>(w);
-    c[2] = tc_pair<BITS, 8 * HALF + 2>(w);
-    c[3] = tc_pair<BITS, 8 * HALF + 3>(w);
-    c[4] = tc_pair<BITS, 8 * HALF + 4>(w);
-    c[5] = tc_pair<BITS, 8 * HALF + 5>(w);
-    c[6] = tc_pair<BITS, 8 * HALF + 6>(w);
-    c[7] = tc_pair<BITS, 8 * HALF + 7>(w);
+    c[0] = tc_pair<BITS, 8 * HALF + 0>(w, k);
+    c[1] = tc_pair<BITS, 8 * HALF + 1>(w, k);
+    c[2] = tc_pair<BITS, 8 * HALF + 2>(w, k);
+    c[3] = tc_pair<BITS, 8 * HALF + 3>(w, k);
+    c[4] = tc_pair<BITS, 8 * HALF + 4>(w, k);
+    c[5] = tc_pair<BITS, 8 * HALF + 5>(w, k);
+    c[6] = tc_pair<BITS, 8 * HALF + 6>(w, k);
+    c[7] = tc_pair<BITS, 8 * HALF + 7>(w, k);
   }
 }
 // Half of s in two binary16 parts: its leading 7 bits, and the rest.
@@ -428,29 +429,25 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-// Some units of a lane's words (`stride` words apart) into its row of the two planes;
-// hi, lo: the parts of their scales.  The loop stays a loop: the kernel's roles share
-// the instruction cache.
+// Units `part`, part + 4, .. (of n) of a lane's words (`stride` words apart) into its
+// row of the two planes; hi, lo: the parts of the row's scales.
 template <int BITS>
 __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, int stride,
-                                          const uint4* hi, const uint4* lo, int units) {
+                                          const uint4* hi, const uint4* lo, int part, int n,
+                                          const TcConst& k) {
   using U = TcUnit<BITS>;
   constexpr int H = U::kUnit / 16;
 #pragma unroll(H == 2 ? 1 : 2)
-  for (int u = 0; u < units; ++u) {
+  for (int u = part; u < n; u += 4) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
-    for (int i = 0; i < U::kUnitW; ++i) w[i] = words[i * stride];
-    words += U::kUnitW * stride;
-    tc_codes16<BITS, 0>(w, c);
-    tc_put16(t_hi, t_hi + 64, c, hi, lo);
+    for (int i = 0; i < U::kUnitW; ++i) w[i] = words[(u * U::kUnitW + i) * stride];
+    tc_codes16<BITS, 0>(w, c, k);
+    tc_put16(t_hi + 8 * H * u, t_hi + 8 * H * u + 64, c, hi + 2 * H * u, lo + 2 * H * u);
     if constexpr (H == 2) {
-      tc_codes16<BITS, 1>(w, c);
-      tc_put16(t_hi + 8, t_hi + 72, c, hi + 2, lo + 2);
+      tc_codes16<BITS, 1>(w, c, k);
+      tc_put16(t_hi + 16 * u + 8, t_hi + 16 * u + 72, c, hi + 4 * u + 2, lo + 4 * u + 2);
     }
-    hi += 2 * H;
-    lo += 2 * H;
-    t_hi += 8 * H;
   }
 }
 // Eight adjacent raw elements; aligned: by one 16-byte load.
@@ -490,51 +487,57 @@ __device__ __forceinline__ void tc_raw_pairs(const uint4& x, const uint4& y, uin
   for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
 }
 // 128 raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
-// at dp up to n) into rows of D in shared memory, by the 128 threads of the values'
-// warps.
+// at dp up to n) into rows of D in shared memory, by all workers.  Loads without
+// branches, so that they are under way together; a token that does not exist reads
+// the window's first row.
 template <int D>
-__device__ __forceinline__ void tc_stage_raw(uint4* dst, int th, const __half* wp, const __half* dp,
+__device__ __forceinline__ void tc_stage_raw(uint4* dst, const __half* wp, const __half* dp,
                                              int first, int r, int n) {
+  constexpr int J = 128 * (D / 8) / kTcWorkers;
   const bool al = ((uintptr_t)dp & 15) == 0;
-#pragma unroll 4
-  for (int j = 0; j < D / 8; ++j) {
-    const int k = th + 128 * j, i = first + k / (D / 8), c = k % (D / 8) * 8;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (i < r)
-      x = *reinterpret_cast<const uint4*>(wp + i * D + c);
-    else if (i < n)
-      x = tc_raw8(dp + (i - r) * D + c, al);
-    dst[k] = x;
+  uint4 x[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int k = threadIdx.x + kTcWorkers * j, i = first + k / (D / 8), c = k % (D / 8) * 8;
+    x[j] = *reinterpret_cast<const uint4*>(al && i >= r && i < n ? dp + (i - r) * D + c
+                                                                 : wp + (i < r ? i * D + c : c));
+    if (i >= n) x[j] = make_uint4(0, 0, 0, 0);
+    if (!al && i >= r && i < n) x[j] = tc_raw8(dp + (i - r) * D + c, false);
   }
-  tc_values_sync();
+#pragma unroll
+  for (int j = 0; j < J; ++j) dst[threadIdx.x + kTcWorkers * j] = x[j];
 }
-// C0 .. C1 of a lane's raw key row, halved, into its operand row: 16 places are two
-// runs of 8 channels E / 2 apart (or two blocks of 8 channels).  src null: zeros.
-template <int E>
-__device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* src, int c0, int c1) {
-  const bool al = ((uintptr_t)src & 15) == 0;
-#pragma unroll 2
-  for (int c = c0; c < c1; ++c) {
-    const int e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (src != nullptr) {
-      x = tc_raw8(src + e0, al);
-      y = tc_raw8(src + e0 + (E >= 16 ? E / 2 : 8), al);
-    }
+// A lane's raw key row, halved, into its operand row, 16-place pieces c0 .. c0 + N - 1:
+// two runs of 8 channels E / 2 apart each (or two blocks of 8 channels).  Loads as
+// above; row: a readable row, have: whether its numbers count.
+template <int E, int N>
+__device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* row, bool have, int c0) {
+  const bool al = ((uintptr_t)row & 15) == 0;
+  uint4 x[N], y[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int c = c0 + j, e0 = E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c;
+    x[j] = tc_raw8(row + e0, al);
+    y[j] = tc_raw8(row + e0 + (E >= 16 ? E / 2 : 8), al);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
     uint32_t r[8];
-    tc_raw_pairs<E>(x, y, r);
-    tc_st8(t_hi + 8 * c, r);
+    tc_raw_pairs<E>(x[j], y[j], r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = have ? r[k] : 0u;
+    tc_st8(t_hi + 8 * (c0 + j), r);
   }
 }
-// Places 16 c0 .. 16 c1 - 1 of a lane's channel of 128 raw tokens (`v`, rows of D
-// in shared memory), halved, into its operand row.  Infinities and NaN are left out
-// (they join at the segment's end, for the rows that attend to them); returns
+// A lane's channel of 128 raw tokens (`v`, rows of D in shared memory), halved, into
+// its operand row: 16-place pieces `part`, part + 4.  Infinities and NaN are left
+// out (they join at the segment's end, for the rows that attend to them); returns
 // whether there were any.
 template <int D, int E>
-__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, int c0, int c1) {
+__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, int part) {
   uint32_t odd = 0;
 #pragma unroll 1
-  for (int c = c0; c < c1; ++c) {
+  for (int c = part; c < 8; c += 4) {
     const __half* s0 = v + (E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c) * D;
     const __half* s1 = s0 + (E >= 16 ? E / 2 : 8) * D;
     uint32_t a[8], b[8];
@@ -570,25 +573,19 @@ __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, in
   return bits;
 }
 
-// Tensor-memory columns.
-constexpr uint32_t kTKhi = 0, kTKlo = 64, kTVhi = 128, kTVlo = 192, kTO = 256, kTS = 384;
+// Tensor-memory columns: two planes of keys and of values, O^T, two S^T.
+constexpr uint32_t kTK = 0, kTV = 128, kTO = 256, kTS = 320;
 
-// Barriers, 8 bytes each, by their number.
+// Barriers for what is asynchronous, 8 bytes each, by their number.
 struct TcBar {
-  static constexpr int raw_full = 0, raw_empty = 3;  // [stage]
-  // scales' parts set out for the unpacking warps: [keys, values][tile parity]
-  static constexpr int sc_full = 6, sc_free = 10;
-  // halves of the operands in tensor memory: [keys, values][half]
-  static constexpr int a_full = 14, a_free = 18;
-  static constexpr int s_full = 22, s_empty = 24;  // [stream], and those that follow
-  static constexpr int p_full = 26, pv_done = 28, h_done = 30, z_full = 32, z_empty = 34;
-  static constexpr int N = 36;
+  static constexpr int raw = 0, scores = 4, values = 5, N = 6;  // raw: [stage]
 };
 
-// One segment: tiles [t0, t0 + nt) of a group.
+// One segment of a group.
 struct TcSeg {
   long long b, unit, n_q;
-  int t0, nt, tq;      // first tile, tiles, tiles of quantized tokens
+  int t0, t1, tq;      // tiles [t0, t1); of the group, tq of quantized tokens
+  int t1s;             // the segment's end of those
   int r, row0, nrows;  // nrows: rows of this block that exist
   bool whole, ok;
 };
@@ -609,7 +606,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
   __shared__ int s_poison[2];   // [segment parity]
-  __shared__ int s_resc[2];     // [stream]: the tile's rows were rescaled
   volatile int* dead = &s_dead;
   const uint32_t bar0 = tc_smem(s_bars), sm0 = tc_smem(sm);
   auto bar = [&](int k) -> uint32_t { return bar0 + 8u * (uint32_t)k; };
@@ -619,7 +615,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   const int nr = p.rb, nch = nr / 16;
 
   // ---- set-up
-  if (warp == 24) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      tc_smem(&s_tmem))
                  : "memory");
@@ -643,25 +639,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   if (tid == 32) {
     s_dead = 0;
     for (int i = 0; i < 2; ++i) s_poison[i] = 0;
-    for (int i = 0; i < 3; ++i) {
-      tc_bar_init(bar(TcBar::raw_full + i), 1);
-      tc_bar_init(bar(TcBar::raw_empty + i), 16);
-    }
-    for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 2; ++k) {
-        tc_bar_init(bar(TcBar::sc_full + 2 * k + i), 4);
-        tc_bar_init(bar(TcBar::sc_free + 2 * k + i), 4);
-        tc_bar_init(bar(TcBar::a_full + 2 * k + i), 4);
-        tc_bar_init(bar(TcBar::a_free + 2 * k + i), 1);
-      }
-      tc_bar_init(bar(TcBar::s_full + i), 1);
-      tc_bar_init(bar(TcBar::s_empty + i), 4);
-      tc_bar_init(bar(TcBar::p_full + i), 4);
-      tc_bar_init(bar(TcBar::pv_done + i), 1);
-      tc_bar_init(bar(TcBar::h_done + i), 4);
-      tc_bar_init(bar(TcBar::z_full + i), 4);
-      tc_bar_init(bar(TcBar::z_empty + i), 4);
-    }
+    for (int i = 0; i < TcBar::N; ++i) tc_bar_init(bar(i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = tid; i < 2 * 8 * Ge::ZLD; i += kTcThreads)
@@ -672,11 +650,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   TcWalk walk = s_walk;
 
-  // streams: tiles of even and of odd count
-  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // [stream][64]
-  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // [stream][64]
-  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [stream][group][64]
-  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [stream][64][8]
+  float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // references
+  float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // factors of a rise
+  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [tile parity][part][group][64]
+  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [part][64][8]
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
   // A range ends within a group at most at its own end: segments after the first
@@ -685,7 +662,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     const TreeSeq q = tree_seq(a, p, w.b);
     TcSeg g;
     g.t0 = w.t;
-    g.nt = (int)min(q.ut - w.t, w.left);
+    g.t1 = w.t + (int)min(q.ut - w.t, w.left);
     g.b = w.b;
     g.unit = w.b * a.Hkv + w.h;
     g.row0 = w.rb * nr;
@@ -694,8 +671,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     g.r = q.r;
     g.ok = q.ok;
     g.tq = q.ok ? (int)((q.n_q + kTcTile - 1) / kTcTile) : 0;
-    g.whole = w.t == 0 && g.nt == q.ut;
-    w.left -= g.nt;
+    g.t1s = min(g.t1, g.tq);
+    g.whole = w.t == 0 && g.t1 == q.ut;
+    w.left -= g.t1 - g.t0;
     w.t = 0;
     if (++w.rb == p.n_rb) {
       w.rb = 0;
@@ -707,26 +685,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     return g;
   };
 
-  if (warp == 26) {
-    // ==== copies: runs ahead over all segments; the ring alone holds it back.
-    // Lane i < 4 copies subtile i.
-    int st = 0;
+  if (warp == 17) {
+    // ==== copies: lane i < 4 copies subtile i of a tile; a tile's stage is free once
+    // the block has passed the second barrier of the tile NST before it
+    TcWalk ahead = walk;
+    TcSeg n{};
+    int nt = 0, issued = 0, done = 0;  // the next tile of n, tiles copied and used up
     const long long Ts = store_tokens(a.c);
-    while (walk.left > 0) {
-      const TcSeg g = next_seg(walk);
-      for (int t = g.t0; t < min(g.t0 + g.nt, g.tq); ++t, ++st) {
-        const int s = st % Ge::NST;
-        if (st >= Ge::NST) tc_wait(bar(TcBar::raw_empty + s), st / Ge::NST - 1, dead);
-        const long long tile = t * 4LL + lane;
+    auto fill = [&]() {
+      while (issued < done + Ge::NST) {
+        while (nt >= n.t1s) {  // the next segment with quantized tiles
+          if (ahead.left <= 0) return;
+          n = next_seg(ahead);
+          nt = n.t0;
+        }
+        const int s = issued % Ge::NST;
+        const long long tile = nt * 4LL + lane;
         long long su = 0, stl = 0;
-        const bool have = lane < 4 && tile < g.n_q / kTile && store_tile(a.c, g.unit, tile, &su, &stl);
-        const int n = __popc(__ballot_sync(0xffffffffu, have));
-        const uint32_t fb = bar(TcBar::raw_full + s);
-        if (lane == 0) tc_expect(fb, n * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM));
+        const bool have =
+            lane < 4 && tile < n.n_q / kTile && store_tile(a.c, n.unit, tile, &su, &stl);
+        const int k = __popc(__ballot_sync(0xffffffffu, have));
+        const uint32_t fb = bar(TcBar::raw + s), dst = sm0 + Ge::S_RING + s * Ge::STAGE;
+        if (lane == 0) tc_expect(fb, k * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM));
         __syncwarp();
-        if (have && !*dead) {
+        if (have) {
           using Lt = Layout<D, BITS>;
-          const uint32_t dst = sm0 + Ge::S_RING + s * Ge::STAGE;
           const long long km = su * Lt::k_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::KM;
           const long long vm = su * Lt::v_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::VM;
           tc_copy(dst + Ge::O_KC + lane * Ge::KC,
@@ -738,170 +721,229 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           tc_copy(dst + Ge::O_VS + lane * Ge::VM, (const char*)a.c.v_scale + vm, Ge::VM, fb);
           tc_copy(dst + Ge::O_VZ + lane * Ge::VM, (const char*)a.c.v_zero + vm, Ge::VM, fb);
         }
+        ++nt;
+        ++issued;
+      }
+    };
+    fill();
+    while (walk.left > 0) {
+      const TcSeg g = next_seg(walk);
+      for (int t = g.t0 - 1; t < g.t1; ++t) {  // the block's second barriers
+        if (!g.ok) break;
+        if (tc_sync_any(false)) tc_sync_any(false);
+        if (t >= g.t0 && t < g.t1s) {
+          ++done;
+          fill();
+        }
       }
     }
-    // no copy may still be under way when the block ends (bounded again; a dead
-    // block has stages without copies, whose waits run out)
-    int never = 0;
-    for (int i = max(st - Ge::NST, 0); i < st; ++i)
-      tc_wait(bar(TcBar::raw_full + (i % Ge::NST)), i / Ge::NST, &never);
-    __syncwarp();
-  }
-
-  // ==== segments
-  // counters of this block: tiles, and tiles that went through the ring
-  int it0 = 0, st0 = 0;
-  for (int seg = 0; warp < 26 && walk.left > 0; ++seg) {
-    const TcSeg g = next_seg(walk);
-    const int t1 = g.t0 + g.nt;
-    // ---- start of a segment: queries, mask, references, pages
-    if (tid == 0) s_odd = 0;
-    if (!g.ok) s_poison[seg & 1] = 1;
-    if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
-      const long long i1 = min(t1 * 4LL, g.n_q / kTile);
-#pragma unroll 1
-      for (long long i = g.t0 * 4LL + tid; i < i1; i += kTcThreads - 32) {
-        long long su, stl;
-        if (!store_tile(a.c, g.unit, i, &su, &stl)) s_poison[seg & 1] = 1;
+    for (int i = max(issued - Ge::NST, 0); i < issued; ++i)  // none is under way at the end
+      tc_wait(bar(TcBar::raw + i % Ge::NST), i / Ge::NST, dead);
+  } else if (warp == 16) {
+    // ==== matrix instructions, after each second barrier: the scores of the next tile,
+    // the value products of this one
+    const bool one = tc_elect();
+    const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
+    const uint64_t q_desc = tc_desc(sm0 + Ge::S_Q, 128, D * 16);
+    int it = 0;
+    while (walk.left > 0) {
+      const TcSeg g = next_seg(walk);
+      if (!g.ok) continue;
+      for (int t = g.t0 - 1; t < g.t1; ++t) {
+        if (tc_sync_any(false)) tc_sync_any(false);
+        const int par = __shfl_sync(0xffffffffu, it & 1, 0);  // of tile t + 1
+        if (one) {
+          if (t + 1 < g.t1) {
+            const uint32_t d = tmem + kTS + 64 * par;
+            tc_mma_row<KS>(d, tmem + kTK, q_desc, id_s, false);
+            if (t + 1 < g.t1s) tc_mma_row<KS>(d, tmem + kTK + 64, q_desc, id_s, true);
+            tc_commit(bar(TcBar::scores));
+          }
+          if (t >= g.t0) {
+            const uint64_t b = tc_desc(sm0 + Ge::S_P + (par ^ 1) * Ge::P_B, 128, 2048);
+            tc_mma_row<8>(tmem + kTO, tmem + kTV, b, id_o, t > g.t0);
+            if (t < g.t1s) tc_mma_row<8>(tmem + kTO, tmem + kTV + 64, b, id_o, true);
+            tc_commit(bar(TcBar::values));
+          }
+        }
+        __syncwarp();
+        if (t + 1 < g.t1) ++it;
       }
     }
-    {
-      const __half* qp = static_cast<const __half*>(a.q) + (g.unit * rows + g.row0) * D;
-      const bool al = ((uintptr_t)qp & 15) == 0;
-      // operand order along channels; rows that do not exist are 0
+  } else {
+    // ==== workers
+    const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, quarter of columns
+    const uint32_t t_q = tmem + ((uint32_t)(q * 32) << 16);
+    const int n8 = lane >> 2, kq = (lane & 3) * 2;  // fragments of mma.sync
+    const int pk = tc_pos<E>(q * 32 + lane);        // this lane's token in the second product
+    const float c1 = 2.0f * a.qscale;
+    const TcConst konst = tc_const();
+    __half* ksc = reinterpret_cast<__half*>(sm + Ge::S_KSC);
+    __half* vsc = reinterpret_cast<__half*>(sm + Ge::S_VSC);
+    __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
+    float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + warp * 16;
+    float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX);
+    int it0 = 0, st0 = 0;  // tiles of the segments before, and those of the ring
+    for (int seg = 0; walk.left > 0; ++seg) {
+      const TcSeg g = next_seg(walk);
+      const __half* wk = static_cast<const __half*>(a.c.k_res) + g.unit * a.c.R * D;
+      const __half* wv = static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D;
+      const __half* dk = static_cast<const __half*>(a.k) + g.unit * a.N * D;
+      const __half* dv = static_cast<const __half*>(a.v) + g.unit * a.N * D;
+      const int n_raw = g.r + a.N;
+      // ---- start of a segment: queries, mask, references, pages
+      if (tid == 0) s_odd = 0;
+      if (!g.ok) s_poison[seg & 1] = 1;
+      if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
+        const long long i1 = min(g.t1 * 4LL, g.n_q / kTile);
 #pragma unroll 1
-      for (int i = tid; i < nr * (D / 8); i += kTcThreads - 32) {
-        const int row = i / (D / 8), c0 = i % (D / 8) * 8;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < g.nrows) x = tc_raw8(qp + row * D + c0, al);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        unsigned char* q = sm + Ge::S_Q + row / 8 * (D * 16) + row % 8 * 16;
+        for (long long i = g.t0 * 4LL + tid; i < i1; i += kTcWorkers) {
+          long long su, stl;
+          if (!store_tile(a.c, g.unit, i, &su, &stl)) s_poison[seg & 1] = 1;
+        }
+      }
+      {
+        const __half* qp = static_cast<const __half*>(a.q) + (g.unit * rows + g.row0) * D;
+        const bool al = ((uintptr_t)qp & 15) == 0;
+        // operand order along channels; rows that do not exist are 0
+#pragma unroll 2
+        for (int i = tid; i < nr * (D / 8); i += kTcWorkers) {
+          const int row = i / (D / 8), c0 = i % (D / 8) * 8;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row < g.nrows) x = tc_raw8(qp + row * D + c0, al);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          unsigned char* d = sm + Ge::S_Q + row / 8 * (D * 16) + row % 8 * 16;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = tc_pos<E>(c0 + e);
-          *reinterpret_cast<uint16_t*>(q + k / 8 * 128 + k % 8 * 2) = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+          for (int e = 0; e < 8; ++e) {
+            const int k = tc_pos<E>(c0 + e);
+            *reinterpret_cast<uint16_t*>(d + k / 8 * 128 + k % 8 * 2) = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+          }
         }
-      }
 #pragma unroll 1
-      for (int i = tid; i < a.N * mw; i += kTcThreads - 32)
-        mask_s[i / mw * 8 + i % mw] = a.mask[g.b * a.N * mw + i];
-      if (tid < 128) m_s[tid] = kTcNone;
-    }
-    tc_fence_smem();
-    tc_sync_segment();
+        for (int i = tid; i < a.N * mw; i += kTcWorkers)
+          mask_s[i / mw * 8 + i % mw] = a.mask[g.b * a.N * mw + i];
+        if (tid < 64) m_s[tid] = kTcNone;
+      }
+      tc_fence_smem();
 
-    if (!g.ok) {
-    } else if (warp < 8) {
-      // ==== keys (lane = token of subtile w) and values (lane = channel of group w),
-      // by one code, in halves (keys of 32 channels in one piece)
-      using U = TcUnit<BITS>;
-      const int vals = warp >> 2, w = warp & 3;
-      const int n_codes = vals ? 128 : D, halves = vals || D > 32 ? 2 : 1;
-      const int units = n_codes / halves / U::kUnit, cols = n_codes / halves / 2;
-      const uint32_t t_hi = tmem + ((uint32_t)(w * 32) << 16) + (vals ? kTVhi : kTKhi);
-      const __half* sc0 = reinterpret_cast<const __half*>(sm + (vals ? Ge::S_VSC : Ge::S_KSC)) + w * 2 * n_codes;
-      const int o_w = vals ? Ge::O_VC + (w * 32 + lane) * 4 : Ge::O_KC + w * Ge::KC + lane * WK * 4;
-      const int w_str = vals ? D : 1;
-      const bool act = !vals || w < NJ;
-      int it = it0, st = st0;
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int s = st % Ge::NST;
-        const bool raw = t >= g.tq;
+      // scales and zeros of tile t's keys, or of its values
+      auto set_keys = [&](int t) {
+        if (t >= g.t1s) return;
+        const int st = st0 + t - g.t0, s = st % Ge::NST;
         const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-        const int first = (t - g.tq) * kTcTile;  // of the raw tokens
-        const __half* src = nullptr;
-        if (!raw) {
-          // (the scales' writers have waited for the copies)
-          tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
-          tc_wait(bar(TcBar::sc_full + 2 * vals + (st & 1)), st >> 1, dead);
-        } else if (!vals) {
-          // raw tokens: the window, then the drafted ones; halved like s
-          const int i = first + w * 32 + lane;
-          if (i < g.r)
-            src = static_cast<const __half*>(a.c.k_res) + (g.unit * a.c.R + i) * D;
-          else if (i < g.r + a.N)
-            src = static_cast<const __half*>(a.k) + (g.unit * a.N + (i - g.r)) * D;
+        tc_wait(bar(TcBar::raw + s), st / Ge::NST, dead);
+        if (tid < 4 * D) {
+          const int gr = tid / D, c = tc_pos<E>(tid % D);
+          zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[tid]));
+          tc_split(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[tid]), &ksc[gr * 2 * D + c],
+                   &ksc[gr * 2 * D + D + c]);
+        }
+      };
+      auto set_values = [&](int t, int par) {
+        __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
+        if (tid >= 128 * NJ) return;
+        const int tok = tid / NJ, j = tid % NJ, c = tc_pos<E>(tok);
+        float z = 0.f;
+        if (t < g.t1s) {
+          const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+          // tokens that do not exist: 0 (their weight 0 times NaN would not be)
+          const bool have = tok < g.n_q - (long long)t * kTcTile;
+          z = have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[tid]) : 0.f;
+          tc_split(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[tid]) : 0.f,
+                   &vsc[j * 256 + c], &vsc[j * 256 + 128 + c]);
+        }
+        zv[j * Ge::ZLD + c] = __float2half_rn(z);
+      };
+      // keys of tile t into tensor memory, and their zeros' products
+      auto put_keys = [&](int t, int par) {
+        float zc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (t < g.t1s) {
+          const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+          const __half* sc = ksc + q * 2 * D;
+          tc_unpack<BITS>(t_q + kTK, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
+                          reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
+                          D / TcUnit<BITS>::kUnit, konst);
+          if (q < nch) {
+            // sum_d q_d z_gd for rows 16 q .., over a quarter of the channels (this warp's
+            // q counts rows here); lane n8 of a column reads group n8's row, columns 4 .. 7
+            // are read by nobody
+            const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
+            const int row = 16 * q + (lane & 15);
+            const uint32_t qa = sm0 + Ge::S_Q + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
+#pragma unroll
+            for (int j = 0; j < (KS + 3) / 4; ++j) {
+              const int ks = part + 4 * j;
+              if (ks < KS) {
+                uint32_t av[4];
+                tc_ldm<false>(av, qa + 256 * ks);
+                tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                            *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+              }
+            }
+          }
         } else {
-          tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), w * 32 + lane,
-                          static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D,
-                          static_cast<const __half*>(a.v) + g.unit * a.N * D, first, g.r, g.r + a.N);
+          // raw tokens: the window, then the drafted ones; halved like s
+          const int i = (t - g.tq) * kTcTile + q * 32 + lane;
+          const __half* src = i < g.r ? wk + i * D : (i < n_raw ? dk + (i - g.r) * D : wk);
+          if (16 * part < D) {
+            tc_raw_keys<E, 1>(t_q + kTK, src, i < n_raw, part);
+            if (D == 128) tc_raw_keys<E, 1>(t_q + kTK, src, i < n_raw, part + 4);
+          }
         }
-        const __half* sc = sc0 + (st & 1) * 8 * n_codes;
+        if (q < nch && kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
+          float* z = zk_s + ((par * 4 + part) * 4 + kq) * 64 + 16 * q + n8;
+          z[0] = zc[0] * a.qscale;
+          z[64] = zc[1] * a.qscale;
+          z[8] = zc[2] * a.qscale;
+          z[72] = zc[3] * a.qscale;
+        }
+      };
+
+      if (g.ok) {
+        tc_sync_workers();
+        set_keys(g.t0);
+        tc_sync_workers();
+        put_keys(g.t0, it0 & 1);
+        tc_wait_st();
+        tc_sync_any(false);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          if (it > 0) tc_wait(bar(TcBar::a_free + 2 * vals + h), it - 1, dead);
+        for (int t = g.t0; t < g.t1; ++t) {
+          const int it = it0 + t - g.t0, par = it & 1;
+          const bool raw = t >= g.t1s, more = t + 1 < g.t1;
+          // ---- a
+          if (more) set_keys(t + 1);
+          set_values(t, par);
+          if (raw)
+            tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv, (t - g.tq) * kTcTile, g.r, n_raw);
+          tc_sync_workers();
+          // ---- b
+          tc_wait(bar(TcBar::scores), it, dead);
           tc_fence_after();
-          if (!act) {
-          } else if (!raw) {
-            tc_unpack<BITS>(t_hi + h * cols, reinterpret_cast<const uint32_t*>(stg + o_w) + h * units * U::kUnitW * w_str,
-                            w_str, reinterpret_cast<const uint4*>(sc) + h * (cols / 4),
-                            reinterpret_cast<const uint4*>(sc + n_codes) + h * (cols / 4), units);
-          } else if (!vals) {
-            tc_raw_keys<E>(t_hi, src, h * cols / 8, (h + 1) * cols / 8);
-          } else {
-            if (tc_raw_values<D, E>(t_hi, reinterpret_cast<const __half*>(sm + Ge::S_RAW) + w * 32 + lane,
-                                    h * cols / 8, (h + 1) * cols / 8))
-              s_odd = 1;
-          }
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc_arrive(bar(TcBar::a_full + 2 * vals + h));
-        }
-        if (!raw) {
-          if (lane == 0) {
-            tc_arrive(bar(TcBar::raw_empty + s));
-            tc_arrive(bar(TcBar::sc_free + 2 * vals + (st & 1)));
-          }
-          ++st;
-        } else if (vals) {
-          tc_values_sync();  // the raw values may be written again
-        }
-      }
-    } else if (warp < 16) {
-      // ==== softmax: lane = token; stream sg takes the tiles of its parity
-      const int sg = (warp - 8) >> 2, sw = warp & 3;
-      const uint32_t t_lane = tmem + ((uint32_t)(sw * 32) << 16) + 64 * sg;
-      float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + (sg * 4 + sw) * 64;
-      float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX) + sg * 256;  // + 64 warp
-      float* mr_s = m_s + 64 * sg;
-      const float* zk = zk_s + (sg * 4 + sw) * 64;
-      const float c1 = 2.0f * a.qscale;
-      const int pk = tc_pos<E>(sw * 32 + lane);  // the token's place in the second product
-      unsigned char* pb = sm + Ge::S_P + sg * Ge::P_B + pk / 8 * 128 + pk % 8 * 16;
-      for (int t = g.t0 + ((it0 + sg) & 1); t < t1; t += 2) {
-        const int it = it0 + t - g.t0;
-        const bool raw = t >= g.tq;
-        // the token of this lane: in the cache (all rows see it), drafted, or none
-        const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + sw * 32 + lane;
-        const bool in = raw ? i < g.r : i < g.n_q;
-        const int node = raw && i >= g.r && i < g.r + a.N ? (int)(i - g.r) : -1;
-        auto seen = [&](int ch) -> uint32_t {  // 16 bits, one for each row of chunk ch
-          return in ? 0xFFFFu : (node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + ch * 16, a.N));
-        };
-        // what the products of the stream's last tile read may be written again
-        if (it >= 2) {
-          tc_wait(bar(TcBar::pv_done + sg), (it >> 1) - 1, dead);
-          tc_wait(bar(TcBar::h_done + sg), (it >> 1) - 1, dead);
-        }
-        tc_wait(bar(TcBar::z_full + sg), it >> 1, dead);
-        tc_wait(bar(TcBar::s_full + sg), it >> 1, dead);
-        tc_fence_after();
-        bool resc = false;
-#pragma unroll 1
-        for (int tries = 0; tries < 2; ++tries) {
-          for (int e = lane; e < nr; e += 32) off_s[e] = mr_s[e] - zk[e];
-          __syncwarp();
-          // ---- weights against the references, and by how much a score exceeds its own
-          float over = -__builtin_huge_valf();
-#pragma unroll 1
-          for (int ch = 0; ch < nch; ++ch) {
-            float v[16];
-            tc_ld16(t_lane + kTS + ch * 16, v);
-            const uint32_t sees = seen(ch);
+          if (more) put_keys(t + 1, par ^ 1);
+          // ---- c: weights of rows 16 part .., against the references; `over`: by how much
+          // a score exceeds its own.  The lane's token: in the cache (all rows see it),
+          // drafted, or none
+          const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + q * 32 + lane;
+          const bool in = raw ? i < g.r : i < g.n_q;
+          const int node = raw && i >= g.r && i < n_raw ? (int)(i - g.r) : -1;
+          const uint32_t t_s = t_q + kTS + 64 * par + 16 * part;
+          unsigned char* pb = sm + Ge::S_P + par * Ge::P_B + pk / 8 * 128 + pk % 8 * 16 + part * 4096;
+          uint32_t sees = 0xFFFFu;  // one bit for each row
+          if (!in) sees = node < 0 || part >= nch ? 0u : tc_seen(mask_s, node, g.row0 + 16 * part, a.N);
+          // the zeros' products of the lane's group
+          auto zk = [&](int row) {
+            const float* z = zk_s + (par * 16 + q) * 64 + row;
+            return (z[0] + z[4 * 64]) + (z[8 * 64] + z[12 * 64]);
+          };
+          auto weights = [&]() -> float {
+            if (lane < 16) off_s[lane] = m_s[16 * part + lane] - zk(16 * part + lane);
+            __syncwarp();
+            float v[16], over = -__builtin_huge_valf();
+            tc_ld16(t_s, v);
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
-              const float4 o = *reinterpret_cast<const float4*>(off_s + ch * 16 + 4 * e4);
+              const float4 o = *reinterpret_cast<const float4*>(off_s + 4 * e4);
               v[4 * e4] = fmaf(v[4 * e4], c1, -o.x);
               v[4 * e4 + 1] = fmaf(v[4 * e4 + 1], c1, -o.y);
               v[4 * e4 + 2] = fmaf(v[4 * e4 + 2], c1, -o.z);
@@ -919,318 +961,159 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
               const __half2 h = __floats2half2_rn(tc_ex2(v[e]), tc_ex2(v[e + 1]));
               w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(pb + (2 * ch) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(pb + (2 * ch + 1) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(pb) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(pb + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+            return over;
+          };
+          float over = -__builtin_huge_valf();
+          if (part < nch) over = weights();
+          // ---- d
+          if (t > g.t0) {
+            tc_wait(bar(TcBar::values), it - 1, dead);
+            tc_fence_after();
           }
-          if (!tc_group_any(sg, over > kTcSlack) || tries == 1) break;
-          // ---- new references: each warp's maxima, joined
-          resc = true;
-#pragma unroll 1
-          for (int ch = 0; ch < nch; ++ch) {
-            float v[16];
-            tc_ld16(t_lane + kTS + ch * 16, v);
-            const uint32_t sees = seen(ch);
-            float mine = kTcNone;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float d = tc_warp_max((sees >> e) & 1u ? fmaf(v[e], c1, zk[ch * 16 + e]) : kTcNone);
-              if (lane == e) mine = d;
+          if (q < NJ) {
+            if (!raw) {
+              const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+              const __half* sc = vsc + q * 256;
+              tc_unpack<BITS>(t_q + kTV, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
+                              reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
+                              128 / TcUnit<BITS>::kUnit, konst);
+            } else if (tc_raw_values<D, E>(t_q + kTV, reinterpret_cast<const __half*>(sm + Ge::S_RAW) + q * 32 + lane,
+                                           part)) {
+              s_odd = 1;
             }
-            if (lane < 16) wmax_s[sw * 64 + ch * 16 + lane] = mine;
           }
-          tc_group(sg);
-          const int e = sw * 32 + lane;  // a row of each thread
-          if (e < nr) {
-            const float old = mr_s[e];
-            const float mn = fmaxf(fmaxf(fmaxf(wmax_s[e], wmax_s[64 + e]),
-                                         fmaxf(wmax_s[128 + e], wmax_s[192 + e])),
-                                   old);
-            f_s[64 * sg + e] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
-            mr_s[e] = mn;
-          }
-          tc_group(sg);
-          if (t - g.t0 >= 2) {  // accumulators so far (their product was waited for above)
-#pragma unroll 1
-            for (int ch = 0; ch < nch; ++ch) {
+          tc_wait_st();
+          tc_fence_smem();
+          const bool rise = tc_sync_any(over > kTcSlack);
+          if (rise) {
+            // ---- new references: the maxima of the tile, joined over its groups
+            if (part < nch) {
               float v[16];
-              tc_ld16(t_lane + kTO + ch * 16, v);
+              tc_ld16(t_s, v);
+              const float z = lane < 16 ? zk(16 * part + lane) : 0.f;
+              float mine = kTcNone;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] *= f_s[64 * sg + ch * 16 + k];
-              tc_st16(t_lane + kTO + ch * 16, v);
+              for (int e = 0; e < 16; ++e) {
+                const float d = fmaf(v[e], c1, __shfl_sync(0xffffffffu, z, e));
+                const float m = tc_warp_max((sees >> e) & 1u ? d : kTcNone);
+                if (lane == e) mine = m;
+              }
+              if (lane < 16) wmax_s[q * 64 + 16 * part + lane] = mine;
             }
-            tc_wait_st();
+            tc_sync_workers();
+            if (tid < nr) {
+              const float old = m_s[tid];
+              const float mn = fmaxf(fmaxf(fmaxf(wmax_s[tid], wmax_s[64 + tid]),
+                                           fmaxf(wmax_s[128 + tid], wmax_s[192 + tid])),
+                                     old);
+              f_s[tid] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
+              m_s[tid] = mn;
+            }
+            tc_sync_workers();
+            if (part < nch) {
+              weights();
+              if (t > g.t0) {  // the accumulators so far (their products are done)
+                float v[16];
+                tc_ld16(t_q + kTO + 16 * part, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] *= f_s[16 * part + k];
+                tc_st16(t_q + kTO + 16 * part, v);
+                tc_wait_st();
+              }
+            }
+            if (q < nch) {
+              const float f0 = f_s[16 * q + n8], f1 = f_s[16 * q + n8 + 8];
+              acc[0] *= f0;
+              acc[1] *= f0;
+              acc[2] *= f1;
+              acc[3] *= f1;
+            }
+            tc_fence_smem();
+            tc_sync_any(false);
           }
-        }
-        if (lane == 0 && sw == 0) s_resc[sg] = resc;
-        tc_fence_before();
-        tc_fence_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc_arrive(bar(TcBar::p_full + sg));
-          tc_arrive(bar(TcBar::s_empty + sg));
-          tc_arrive(bar(TcBar::z_empty + sg));
-        }
-      }
-    } else if (warp < 20) {
-      // ==== keys' scales in two parts, and sum_d q_d z_gd of the tile's four groups for
-      // 16-row chunk zw
-      const int zw = warp - 16, zt = zw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
-      int it = it0, st = st0;
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int par = it & 1;
-        const bool raw = t >= g.tq;
-        __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH) + par * 4 * Ge::ZLD;
-        if (!raw) {
-          const int s = st % Ge::NST;
-          const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-          const M* kz = reinterpret_cast<const M*>(stg + Ge::O_KZ);
-          const M* ks = reinterpret_cast<const M*>(stg + Ge::O_KS);
-          __half* sc = reinterpret_cast<__half*>(sm + Ge::S_KSC) + (st & 1) * 8 * D;
-          tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
-          if (st >= 2) tc_wait(bar(TcBar::sc_free + (st & 1)), (st >> 1) - 1, dead);
-#pragma unroll 2
-          for (int j = 0; j < 4 * D / 128; ++j) {
-            const int i = zt + 128 * j, gr = i / D, c = tc_pos<E>(i % D);
-            zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(kz[i]));
-            tc_split(to_f32(ks[i]), &sc[gr * 2 * D + c], &sc[gr * 2 * D + D + c]);
-          }
-          tc_zeros_sync();
-          if (lane == 0) {
-            tc_arrive(bar(TcBar::raw_empty + s));
-            tc_arrive(bar(TcBar::sc_full + (st & 1)));
-          }
-          ++st;
-        }
-        if (it >= 2) tc_wait(bar(TcBar::z_empty + par), (it >> 1) - 1, dead);
-        // lane n8 of a column reads group n8's row; columns 4 .. 7 are read by nobody
-        const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
-        if (zw < nch) {
-          const int ch = zw;
-          float zc[4] = {0.f, 0.f, 0.f, 0.f};
-          if (!raw) {
-            // rows 16 ch + (lane % 16), channels 16 ks + 8 (lane / 16)
-            const int row = 16 * ch + (lane & 15);
-            const uint32_t qa =
-                (sm0 + Ge::S_Q) + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
-#pragma unroll 4
-            for (int ks = 0; ks < KS; ++ks) {
+          // ---- f: sums over the tile's tokens, of the weights and of the values' zeros:
+          // rows 16 q .., a quarter of the tokens
+          if (q < nch) {
+            const __half* zr = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
+            // 8 x 8 blocks (tokens x rows) of weights, transposed on the way
+            const int blk = lane >> 3;
+            const uint32_t pa = sm0 + Ge::S_P + par * Ge::P_B + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 +
+                                (lane & 7) * 16;
+#pragma unroll
+            for (int ks = 2 * part; ks < 2 * part + 2; ++ks) {
               uint32_t av[4];
-              tc_ldm<false>(av, qa + 256 * ks);
-              tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+              tc_ldm<true>(av, pa + ks * 256);
+              tc_mma16816(acc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
                           *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
             }
           }
-          if (kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
-            float* z = zk_s + (par * 4 + kq) * 64 + 16 * ch + n8;
-            z[0] = zc[0] * a.qscale;
-            z[64] = zc[1] * a.qscale;
-            z[8] = zc[2] * a.qscale;
-            z[72] = zc[3] * a.qscale;
-          }
         }
-        __syncwarp();
-        if (lane == 0) tc_arrive(bar(TcBar::z_full + par));
+        if (q < nch) {
+          float* z = lz_s + (part * 64 + 16 * q + n8) * 8 + kq;
+          z[0] = acc[0];
+          z[1] = acc[1];
+          z[64] = acc[2];
+          z[65] = acc[3];
+        }
+        tc_wait(bar(TcBar::values), it0 + g.t1 - 1 - g.t0, dead);
       }
-    } else if (warp < 24) {
-      // ==== values' scales in two parts, and the sums over tokens of the weights and of the
-      // values' zeros: chunk uw of each stream.  A tile is prepared before the sums of
-      // the one before it.
-      const int uw = warp - 20, ut = uw * 32 + lane, n8 = lane >> 2, kq = (lane & 3) * 2;
-      float acc[2][4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-      int st = st0;
+      tc_sync_workers();
+
+      // ---- end of a segment: lane = channel, rows 4 part .. of each 16
+      {
+        const int ch_d = q * 32 + lane;
+        const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
+        const int i1 = s_odd ? min((g.t1 - g.tq) * kTcTile, n_raw) : 0;
+        float* pt = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
+        __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
 #pragma unroll 1
-      for (int t = g.t0; t <= t1; ++t) {
-        if (t < t1) {
-          const int par = (it0 + t - g.t0) & 1;
-          __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
-          if (t < g.tq) {
-            const int s = st % Ge::NST;
-            const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-            const M* vz = reinterpret_cast<const M*>(stg + Ge::O_VZ) + ut * NJ;
-            const M* vs = reinterpret_cast<const M*>(stg + Ge::O_VS) + ut * NJ;
-            __half* sc = reinterpret_cast<__half*>(sm + Ge::S_VSC) + (st & 1) * 8 * 128 + tc_pos<E>(ut);
-            // tokens that do not exist: 0 (their weight 0 times NaN would not be)
-            const bool have = ut < g.n_q - (long long)t * kTcTile;
-            tc_wait(bar(TcBar::raw_full + s), st / Ge::NST, dead);
-            if (st >= 2) tc_wait(bar(TcBar::sc_free + 2 + (st & 1)), (st >> 1) - 1, dead);
-#pragma unroll 2
-            for (int j = 0; j < NJ; ++j) {
-              zv[j * Ge::ZLD + tc_pos<E>(ut)] = __float2half_rn(have ? to_f32(vz[j]) : 0.f);
-              tc_split(have ? to_f32(vs[j]) : 0.f, &sc[j * 256], &sc[j * 256 + 128]);
-            }
-            tc_sums_sync();
-            if (lane == 0) {
-              tc_arrive(bar(TcBar::raw_empty + s));
-              tc_arrive(bar(TcBar::sc_full + 2 + (st & 1)));
-            }
-            ++st;
-          } else {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) zv[j * Ge::ZLD + ut] = __ushort_as_half(0);
-            tc_sums_sync();
-          }
-        }
-        if (t == g.t0) continue;
-        const int it = it0 + t - 1 - g.t0, par = it & 1;
-        const __half* zr = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
-        // 8 x 8 blocks (tokens x rows) of weights, transposed on the way: rows 16 uw + 0 / 8,
-        // tokens 16 ks + 0 / 8
-        const int blk = lane >> 3;
-        const uint32_t pbase = (sm0 + Ge::S_P + par * Ge::P_B) + uw * 4096 + (blk & 1) * 2048 +
-                               (blk >> 1) * 128 + (lane & 7) * 16;
-        tc_wait(bar(TcBar::p_full + par), it >> 1, dead);
-        if (uw < nch) {
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = par ? acc[1][e] : acc[0][e];
-          if (s_resc[par]) {
-            const float f0 = f_s[par * 64 + 16 * uw + n8], f1 = f_s[par * 64 + 16 * uw + n8 + 8];
-            x[0] *= f0;
-            x[1] *= f0;
-            x[2] *= f1;
-            x[3] *= f1;
-          }
-#pragma unroll 4
-          for (int ks = 0; ks < 8; ++ks) {
-            uint32_t av[4];
-            tc_ldm<true>(av, pbase + ks * 256);
-            tc_mma16816(x, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
-                        *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
-          }
+        for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 16) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          if (g.ok) tc_ld4(t_q + kTO + e4, v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc[0][e] = par ? acc[0][e] : x[e];
-            acc[1][e] = par ? x[e] : acc[1][e];
-          }
-        }
-        __syncwarp();
-        if (lane == 0) tc_arrive(bar(TcBar::h_done + par));
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (uw < nch) {
-          float* z = lz_s + (64 * k + 16 * uw + n8) * 8 + kq;
-          z[0] = acc[k][0];
-          z[1] = acc[k][1];
-          z[64] = acc[k][2];
-          z[65] = acc[k][3];
-        }
-      }
-    } else {
-      // ==== score products (warp 24) and value products (25), by halves of the operand
-      const int vals = warp - 24;
-      const bool one = tc_elect();
-      const uint32_t id = tc_idesc(nr, vals);
-      const uint64_t desc = vals ? tc_desc((sm0 + Ge::S_P), 128, 2048)
-                                 : tc_desc((sm0 + Ge::S_Q), 128, D * 16);
-      const int halves = vals || D > 32 ? 2 : 1, ksh = (vals ? 8 : KS) / halves;
-      const uint32_t t_a = tmem + (vals ? kTVhi : kTKhi), t_d = tmem + (vals ? kTO : kTS);
-      int it = it0;
+            const int row = e4 + e;
+            if (row >= g.nrows) break;
+            const float* z = lz_s + row * 8;
+            float l = (z[4] + z[512 + 4]) + (z[1024 + 4] + z[1536 + 4]), m = m_s[row];
+            float o = fmaf(2.0f, v[e], (z[q] + z[512 + q]) + (z[1024 + q] + z[1536 + q]));
+            // infinite or NaN raw values, of the tokens that the row attends to
 #pragma unroll 1
-      for (int t = g.t0; t < t1; ++t, ++it) {
-        const int par = __shfl_sync(0xffffffffu, it & 1, 0);
-        const bool lo = t < g.tq;
-        bool add = vals && t - g.t0 >= 2;
-        if (vals)
-          tc_wait(bar(TcBar::p_full + par), it >> 1, dead);
-        else if (it >= 2)
-          tc_wait(bar(TcBar::s_empty + par), (it >> 1) - 1, dead);
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          tc_wait(bar(TcBar::a_full + 2 * vals + h), it, dead);
-          tc_fence_after();
-          if (one) {
-            const uint64_t b = desc + (vals ? par * (Ge::P_B / 16) : 0) + h * ksh * 16;
-            const uint32_t aa = t_a + h * ksh * 8;
-#pragma unroll 1
-            for (int pl = 0; pl < (lo ? 2 : 1); ++pl)
-#pragma unroll 2
-              for (int ks = 0; ks < ksh; ++ks) {
-                tc_mma(t_d + 64 * par, aa + 64 * pl + 8 * ks, b + 16 * ks, id, add);
-                add = true;
+            for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
+              const __half w = i < g.r ? wv[i * D + ch_d] : dv[(i - g.r) * D + ch_d];
+              if ((__half_as_ushort(w) & 0x7C00u) == 0x7C00u &&
+                  (i < g.r || (tc_seen(mask_s, i - g.r, g.row0 + row, a.N) & 1u)))
+                o += __half2float(w);
+            }
+            if (poison) {
+              o = m = 0.f;
+              l = kNaN;
+            }
+            if (g.whole) {
+              out[row * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(o, l));
+            } else {
+              pt[2 * nr + row * D + ch_d] = o;
+              if (ch_d == 0) {
+                pt[2 * row] = m;
+                pt[2 * row + 1] = l;
               }
-            tc_commit(bar(TcBar::a_free + 2 * vals + h));
-            if (h == halves - 1) tc_commit(vals ? bar(TcBar::pv_done + par) : bar(TcBar::s_full + par));
-          }
-          add = true;
-          __syncwarp();
-        }
-      }
-      --it;
-      if (vals) tc_wait(bar(TcBar::pv_done + (it & 1)), it >> 1, dead);  // and all before it
-    }
-    tc_sync_segment();
-
-    // ---- end of a segment: lane = channel, 4 rows at a time
-    if (warp >= 8 && warp < 16) {
-      const int sg = (warp - 8) >> 2, sw = warp & 3;
-      const int ch_d = sw * 32 + lane;
-      const uint32_t t_lane = tmem + kTO + ((uint32_t)(sw * 32) << 16);
-      const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
-      // streams that took a tile: by the parity of the block's count
-      const bool u0 = g.nt > 1 || (it0 & 1) == 0, u1 = g.nt > 1 || (it0 & 1) == 1;
-      const int i1 = s_odd ? min((t1 - g.tq) * kTcTile, g.r + a.N) : 0;
-      float* part = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
-      __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
-#pragma unroll 1
-      for (int e4 = 4 * sg; e4 < g.nrows && sw < NJ; e4 += 8) {
-        float v0[4] = {0.f, 0.f, 0.f, 0.f}, v1[4] = {0.f, 0.f, 0.f, 0.f};
-        if (g.ok && u0) tc_ld4(t_lane + e4, v0);
-        if (g.ok && u1) tc_ld4(t_lane + 64 + e4, v1);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = e4 + e;
-          if (row >= g.nrows) break;
-          // the streams' parts, against the larger reference
-          float m = m_s[row], o = fmaf(2.0f, v0[e], lz_s[8 * row + sw]), l = lz_s[8 * row + 4];
-          if (!u0) o = l = 0.f;
-          if (u1) {
-            const float m1 = m_s[64 + row], mx = fmaxf(m, m1);
-            const float w0 = tc_ex2(m - mx), w1 = tc_ex2(m1 - mx);
-            o = w0 * o + w1 * fmaf(2.0f, v1[e], lz_s[8 * (64 + row) + sw]);
-            l = w0 * l + w1 * lz_s[8 * (64 + row) + 4];
-            m = mx;
-          }
-          // infinite or NaN raw values, of the tokens that the row attends to
-#pragma unroll 1
-          for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
-            const __half w = i < g.r
-                                 ? static_cast<const __half*>(a.c.v_res)[(g.unit * a.c.R + i) * D + ch_d]
-                                 : static_cast<const __half*>(a.v)[(g.unit * a.N + i - g.r) * D + ch_d];
-            if ((__half_as_ushort(w) & 0x7C00u) == 0x7C00u &&
-                (i < g.r || (tc_seen(mask_s, i - g.r, g.row0 + row, a.N) & 1u)))
-              o += __half2float(w);
-          }
-          if (poison) {
-            o = m = 0.f;
-            l = kNaN;
-          }
-          if (g.whole) {
-            out[row * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(o, l));
-          } else {
-            part[2 * nr + row * D + ch_d] = o;
-            if (ch_d == 0) {
-              part[2 * row] = m;
-              part[2 * row + 1] = l;
             }
           }
         }
       }
+      if (tid == 0) s_poison[(seg & 1) ^ 1] = 0;  // the next segment's
+      if (g.ok) {
+        it0 += g.t1 - g.t0;
+        st0 += max(g.t1s - g.t0, 0);
+      }
+      tc_sync_workers();
     }
-    if (tid == 0) s_poison[(seg & 1) ^ 1] = 0;  // the next segment's
-    if (g.ok) {
-      it0 += g.nt;
-      st0 += max(min(t1, g.tq) - g.t0, 0);
-    }
-    tc_sync_segment();
   }
 
   __syncthreads();
-  if (warp == 24) {
+  if (warp == 16) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
