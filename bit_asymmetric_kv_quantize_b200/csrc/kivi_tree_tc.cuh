@@ -36,15 +36,15 @@
 // that held, and the rare tile where it did not raises the references, rescales
 // O^T in tensor memory and forms its weights again.
 //
-// Sixteen warps walk through a tile's work together, two barriers of the block a
-// tile (no polling); warp w has lanes 32 (w % 4) .. + 31 of tensor memory and a
-// quarter w / 4 of the columns:
-//   a  set out scales and zeros: keys' of the next tile, values' of this one
-//   b  unpack the next tile's keys; its zeros' products
-//   c  this tile's weights (its scores were begun a tile ago)
-//   d  unpack this tile's values
-//   f  (a further warp issues the next scores and this tile's value products)
-//      sums over this tile's tokens
+// Sixteen warps walk through the tiles together, one barrier of the block a tile (no
+// polled hand-overs); warp w has lanes 32 (w % 4) .. + 31 of tensor memory and a
+// quarter w / 4 of the columns.  Between two barriers, for tile t:
+//   sums over tile t - 1's tokens; scales and zeros set out, of tile t + 2's keys and
+//   of tile t + 1's values;
+//   tile t + 1's keys unpacked, and their zeros' products;
+//   tile t's weights (its scores were begun at the barrier before), its values
+//   unpacked.
+// A further warp then issues the scores of tile t + 1 and the value products of t.
 // One more warp issues the copies (cp.async.bulk of each tile's ranges into a ring).
 // With a role to each warp instead, handing over by mbarriers, the same work took
 // twice as long: the waiting warps' polling and their different code filled the
@@ -84,16 +84,16 @@ struct TcGeo {
   static constexpr int O_VS = O_VC + 4 * VC;
   static constexpr int O_VZ = O_VS + 4 * VM;
   static constexpr int STAGE = O_VZ + 4 * VM;
-  static constexpr int NST = 4;
+  static constexpr int NST = STAGE <= 20480 ? 5 : 4;
   // shared memory
   static constexpr int S_RING = 0;
   static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
   static constexpr int S_P = S_Q + 64 * D * 2;           // 2 x [64 rows][128 tokens]
   static constexpr int P_B = 64 * 128 * 2;
   static constexpr int S_RAW = S_P + 2 * P_B;            // raw values [128 tokens][D]
-  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 4 groups x D x (hi, lo) halves
-  static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 4 * 128 * 4;       // 2 x [4 parts][4 groups][64 rows] float
+  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 2 x 4 groups x D x (hi, lo) halves
+  static constexpr int S_VSC = S_KSC + 2 * 4 * D * 4;    // 2 x 4 groups x 128 x (hi, lo)
+  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // 2 x [4 parts][4 groups][64 rows] float
   static constexpr int S_OFF = S_ZK + 2 * 16 * 64 * 4;   // [16 warps][16 rows]
   static constexpr int S_WMAX = S_OFF + 16 * 16 * 4;     // [4 groups][64 rows]
   static constexpr int S_M = S_WMAX + 4 * 64 * 4;        // [64 rows]
@@ -104,8 +104,8 @@ struct TcGeo {
   // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
   static constexpr int ZLD = 136;
   static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
-  static constexpr int S_ZV = S_ZH + 4 * ZLD * 2;        // 2 x
-  static constexpr int BYTES = S_ZV + 2 * 8 * ZLD * 2;
+  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;    // 2 x keys', 4 x values'
+  static constexpr int BYTES = S_ZV + 4 * 8 * ZLD * 2;
 };
 
 // Position of code i of a block of E in the order of the operands: the pair
@@ -131,7 +131,7 @@ __device__ __forceinline__ void tc_arrive(uint32_t b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
 }
 __device__ __forceinline__ void tc_expect(uint32_t b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(bytes)
                : "memory");
 }
 // Waits for phase `n` (counted from 0) of a barrier; bounded: rounds of 4096 tries,
@@ -561,6 +561,10 @@ __device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, in
   return odd != 0;
 }
 
+// A warp's common truth value, in a uniform register.
+__device__ __forceinline__ bool tc_uniform(bool x) {
+  return __shfl_sync(0xffffffffu, (int)x, 0) != 0;
+}
 // Whether rows row0 .. row0 + 15 see drafted token `node`, one bit each.
 __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, int row0, int N) {
   uint32_t bits = 0;
@@ -578,7 +582,7 @@ constexpr uint32_t kTK = 0, kTV = 128, kTO = 256, kTS = 320;
 
 // Barriers for what is asynchronous, 8 bytes each, by their number.
 struct TcBar {
-  static constexpr int raw = 0, scores = 4, values = 5, N = 6;  // raw: [stage]
+  static constexpr int raw = 0, scores = 5, values = 6, N = 7;  // raw: [stage]
 };
 
 // One segment of a group.
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     for (int i = 0; i < TcBar::N; ++i) tc_bar_init(bar(i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < 2 * 8 * Ge::ZLD; i += kTcThreads)
+  for (int i = tid; i < 4 * 8 * Ge::ZLD; i += kTcThreads)
     reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 8 == 4 ? 1.0f : 0.0f);
   tc_fence_before();
   __syncthreads();
@@ -659,6 +663,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   // A range ends within a group at most at its own end: segments after the first
   // begin with a group.
   auto next_seg = [&](TcWalk& w) -> TcSeg {
+    // what steers the warp is broadcast: without that the compiler takes it for
+    // divergent and guards each tensor-memory access (some 50 instructions each)
     const TreeSeq q = tree_seq(a, p, w.b);
     TcSeg g;
     g.t0 = w.t;
@@ -674,6 +680,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     g.t1s = min(g.t1, g.tq);
     g.whole = w.t == 0 && g.t1 == q.ut;
     w.left -= g.t1 - g.t0;
+    g.t0 = __shfl_sync(0xffffffffu, g.t0, 0);
+    g.t1 = __shfl_sync(0xffffffffu, g.t1, 0);
+    g.tq = __shfl_sync(0xffffffffu, g.tq, 0);
+    g.t1s = __shfl_sync(0xffffffffu, g.t1s, 0);
+    g.r = __shfl_sync(0xffffffffu, g.r, 0);
+    g.nrows = __shfl_sync(0xffffffffu, g.nrows, 0);
+    g.ok = __shfl_sync(0xffffffffu, (int)g.ok, 0) != 0;
+    g.whole = __shfl_sync(0xffffffffu, (int)g.whole, 0) != 0;
     w.t = 0;
     if (++w.rb == p.n_rb) {
       w.rb = 0;
@@ -686,12 +700,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   };
 
   if (warp == 17) {
-    // ==== copies: lane i < 4 copies subtile i of a tile; a tile's stage is free once
-    // the block has passed the second barrier of the tile NST before it
+    // ==== copies: lane k < 6 copies a tile's part of array k, in one piece, or one for
+    // each page that it touches; a tile's stage is free once the block has passed the
+    // barrier of the tile NST before it
     TcWalk ahead = walk;
     TcSeg n{};
     int nt = 0, issued = 0, done = 0;  // the next tile of n, tiles copied and used up
     const long long Ts = store_tokens(a.c);
+    // array k: codes, scales, zeros of keys, then of values
+    const int k = lane % 3;
+    const bool val = lane >= 3;
+    const char* src = static_cast<const char*>(
+        val ? (k == 0 ? (const void*)a.c.v_codes : k == 1 ? a.c.v_scale : a.c.v_zero)
+            : (k == 0 ? (const void*)a.c.k_codes : k == 1 ? a.c.k_scale : a.c.k_zero));
+    const int size = val ? (k == 0 ? Ge::VC : Ge::VM) : (k == 0 ? Ge::KC : Ge::KM);
+    const long long unit_bytes = Ts / kTile * size;
+    const uint32_t o_dst = val ? (k == 0 ? Ge::O_VC : k == 1 ? Ge::O_VS : Ge::O_VZ)
+                               : (k == 0 ? Ge::O_KC : k == 1 ? Ge::O_KS : Ge::O_KZ);
     auto fill = [&]() {
       while (issued < done + Ge::NST) {
         while (nt >= n.t1s) {  // the next segment with quantized tiles
@@ -700,35 +725,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           nt = n.t0;
         }
         const int s = issued % Ge::NST;
-        const long long tile = nt * 4LL + lane;
-        long long su = 0, stl = 0;
-        const bool have =
-            lane < 4 && tile < n.n_q / kTile && store_tile(a.c, n.unit, tile, &su, &stl);
-        const int k = __popc(__ballot_sync(0xffffffffu, have));
         const uint32_t fb = bar(TcBar::raw + s), dst = sm0 + Ge::S_RING + s * Ge::STAGE;
-        if (lane == 0) tc_expect(fb, k * (Ge::KC + 2 * Ge::KM + Ge::VC + 2 * Ge::VM));
-        __syncwarp();
-        if (have) {
-          using Lt = Layout<D, BITS>;
-          const long long km = su * Lt::k_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::KM;
-          const long long vm = su * Lt::v_meta_unit(Ts) * (int)sizeof(M) + stl * Ge::VM;
-          tc_copy(dst + Ge::O_KC + lane * Ge::KC,
-                  (const char*)(a.c.k_codes + su * Lt::k_codes_unit(Ts)) + stl * Ge::KC, Ge::KC, fb);
-          tc_copy(dst + Ge::O_KS + lane * Ge::KM, (const char*)a.c.k_scale + km, Ge::KM, fb);
-          tc_copy(dst + Ge::O_KZ + lane * Ge::KM, (const char*)a.c.k_zero + km, Ge::KM, fb);
-          tc_copy(dst + Ge::O_VC + lane * Ge::VC,
-                  (const char*)(a.c.v_codes + su * Lt::v_codes_unit(Ts)) + stl * Ge::VC, Ge::VC, fb);
-          tc_copy(dst + Ge::O_VS + lane * Ge::VM, (const char*)a.c.v_scale + vm, Ge::VM, fb);
-          tc_copy(dst + Ge::O_VZ + lane * Ge::VM, (const char*)a.c.v_zero + vm, Ge::VM, fb);
+        const int subs = (int)min(n.n_q / kTile - nt * 4LL, 4LL), page = a.c.R / kTile;
+        for (int i = 0, run; i < subs; i += run) {
+          const long long tile = nt * 4LL + i;
+          run = a.c.bt == nullptr ? subs : min(subs - i, page - (int)(tile % page));
+          long long su, stl;
+          if (!store_tile(a.c, n.unit, tile, &su, &stl)) continue;
+          if (lane == 0) tc_expect(fb, run * (2 * Ge::KM + Ge::KC + Ge::VC + 2 * Ge::VM));
+          __syncwarp();
+          if (lane < 6)
+            tc_copy(dst + o_dst + i * size, src + su * unit_bytes + stl * size, run * size, fb);
         }
+        if (lane == 0) tc_arrive(fb);
         ++nt;
         ++issued;
       }
     };
     fill();
-    while (walk.left > 0) {
+    while (tc_uniform(walk.left > 0)) {
       const TcSeg g = next_seg(walk);
-      for (int t = g.t0 - 1; t < g.t1; ++t) {  // the block's second barriers
+      for (int t = g.t0 - 1; t < g.t1; ++t) {  // the block's barriers
         if (!g.ok) break;
         if (tc_sync_any(false)) tc_sync_any(false);
         if (t >= g.t0 && t < g.t1s) {
@@ -740,13 +757,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     for (int i = max(issued - Ge::NST, 0); i < issued; ++i)  // none is under way at the end
       tc_wait(bar(TcBar::raw + i % Ge::NST), i / Ge::NST, dead);
   } else if (warp == 16) {
-    // ==== matrix instructions, after each second barrier: the scores of the next tile,
+    // ==== matrix instructions, after each barrier: the scores of the next tile,
     // the value products of this one
     const bool one = tc_elect();
     const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
     const uint64_t q_desc = tc_desc(sm0 + Ge::S_Q, 128, D * 16);
     int it = 0;
-    while (walk.left > 0) {
+    while (tc_uniform(walk.left > 0)) {
       const TcSeg g = next_seg(walk);
       if (!g.ok) continue;
       for (int t = g.t0 - 1; t < g.t1; ++t) {
@@ -778,13 +795,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     const int pk = tc_pos<E>(q * 32 + lane);        // this lane's token in the second product
     const float c1 = 2.0f * a.qscale;
     const TcConst konst = tc_const();
-    __half* ksc = reinterpret_cast<__half*>(sm + Ge::S_KSC);
-    __half* vsc = reinterpret_cast<__half*>(sm + Ge::S_VSC);
-    __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
+    __half* ksc0 = reinterpret_cast<__half*>(sm + Ge::S_KSC);
+    __half* vsc0 = reinterpret_cast<__half*>(sm + Ge::S_VSC);
+    __half* zh0 = reinterpret_cast<__half*>(sm + Ge::S_ZH);
+    __half* zv0 = reinterpret_cast<__half*>(sm + Ge::S_ZV);
     float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + warp * 16;
     float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX);
     int it0 = 0, st0 = 0;  // tiles of the segments before, and those of the ring
-    for (int seg = 0; walk.left > 0; ++seg) {
+    for (int seg = 0; tc_uniform(walk.left > 0); ++seg) {
       const TcSeg g = next_seg(walk);
       const __half* wk = static_cast<const __half*>(a.c.k_res) + g.unit * a.c.R * D;
       const __half* wv = static_cast<const __half*>(a.c.v_res) + g.unit * a.c.R * D;
@@ -831,6 +849,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         if (t >= g.t1s) return;
         const int st = st0 + t - g.t0, s = st % Ge::NST;
         const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
+        __half* zh = zh0 + (t & 1) * 4 * Ge::ZLD;
+        __half* ksc = ksc0 + (t & 1) * 8 * D;
         tc_wait(bar(TcBar::raw + s), st / Ge::NST, dead);
         if (tid < 4 * D) {
           const int gr = tid / D, c = tc_pos<E>(tid % D);
@@ -839,8 +859,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                    &ksc[gr * 2 * D + D + c]);
         }
       };
-      auto set_values = [&](int t, int par) {
-        __half* zv = reinterpret_cast<__half*>(sm + Ge::S_ZV) + par * 8 * Ge::ZLD;
+      auto set_values = [&](int t) {
+        __half* zv = zv0 + (t & 3) * 8 * Ge::ZLD;
+        __half* vsc = vsc0 + (t & 1) * 1024;
         if (tid >= 128 * NJ) return;
         const int tok = tid / NJ, j = tid % NJ, c = tc_pos<E>(tok);
         float z = 0.f;
@@ -859,7 +880,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         float zc[4] = {0.f, 0.f, 0.f, 0.f};
         if (t < g.t1s) {
           const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-          const __half* sc = ksc + q * 2 * D;
+          const __half* sc = ksc0 + (t & 1) * 8 * D + q * 2 * D;
           tc_unpack<BITS>(t_q + kTK, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
                           reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
                           D / TcUnit<BITS>::kUnit, konst);
@@ -867,7 +888,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             // sum_d q_d z_gd for rows 16 q .., over a quarter of the channels (this warp's
             // q counts rows here); lane n8 of a column reads group n8's row, columns 4 .. 7
             // are read by nobody
-            const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
+            const __half* zr = zh0 + (t & 1) * 4 * Ge::ZLD + (n8 & 3) * Ge::ZLD + kq;
             const int row = 16 * q + (lane & 15);
             const uint32_t qa = sm0 + Ge::S_Q + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
 #pragma unroll
@@ -899,29 +920,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         }
       };
 
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      // sums over tile t's tokens, of the weights and of the values' zeros: rows 16 q ..,
+      // a quarter of the tokens
+      auto sums = [&](int t, int par) {
+        if (q >= nch) return;
+        const __half* zr = zv0 + ((t & 3) * 8 + n8) * Ge::ZLD + kq;
+        // 8 x 8 blocks (tokens x rows) of weights, transposed on the way
+        const int blk = lane >> 3;
+        const uint32_t pa = sm0 + Ge::S_P + par * Ge::P_B + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 +
+                            (lane & 7) * 16;
+#pragma unroll
+        for (int ks = 2 * part; ks < 2 * part + 2; ++ks) {
+          uint32_t av[4];
+          tc_ldm<true>(av, pa + ks * 256);
+          tc_mma16816(acc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                      *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+        }
+      };
+
       if (g.ok) {
         tc_sync_workers();
         set_keys(g.t0);
         tc_sync_workers();
-        put_keys(g.t0, it0 & 1);
-        tc_wait_st();
-        tc_sync_any(false);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int t = g.t0; t < g.t1; ++t) {
+        for (int t = g.t0 - 1; t < g.t1; ++t) {
           const int it = it0 + t - g.t0, par = it & 1;
           const bool raw = t >= g.t1s, more = t + 1 < g.t1;
-          // ---- a
-          if (more) set_keys(t + 1);
-          set_values(t, par);
+          if (t > g.t0) sums(t - 1, par ^ 1);
+          if (t + 2 < g.t1) set_keys(t + 2);
+          if (more) set_values(t + 1);
+          if (t < g.t0) {  // the first keys
+            put_keys(g.t0, par ^ 1);
+            tc_wait_st();
+            tc_sync_any(false);
+            continue;
+          }
           if (raw)
             tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv, (t - g.tq) * kTcTile, g.r, n_raw);
-          tc_sync_workers();
-          // ---- b
           tc_wait(bar(TcBar::scores), it, dead);
           tc_fence_after();
           if (more) put_keys(t + 1, par ^ 1);
-          // ---- c: weights of rows 16 part .., against the references; `over`: by how much
+          // ---- weights of rows 16 part .., against the references; `over`: by how much
           // a score exceeds its own.  The lane's token: in the cache (all rows see it),
           // drafted, or none
           const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + q * 32 + lane;
@@ -967,7 +1007,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           };
           float over = -__builtin_huge_valf();
           if (part < nch) over = weights();
-          // ---- d
+          // ---- values
+          if (raw) tc_sync_workers();
           if (t > g.t0) {
             tc_wait(bar(TcBar::values), it - 1, dead);
             tc_fence_after();
@@ -975,7 +1016,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           if (q < NJ) {
             if (!raw) {
               const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-              const __half* sc = vsc + q * 256;
+              const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
               tc_unpack<BITS>(t_q + kTV, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
                               reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
                               128 / TcUnit<BITS>::kUnit, konst);
@@ -986,7 +1027,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
           }
           tc_wait_st();
           tc_fence_smem();
-          const bool rise = tc_sync_any(over > kTcSlack);
+          const bool rise = tc_uniform(tc_sync_any(over > kTcSlack));
           if (rise) {
             // ---- new references: the maxima of the tile, joined over its groups
             if (part < nch) {
@@ -1033,23 +1074,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             tc_fence_smem();
             tc_sync_any(false);
           }
-          // ---- f: sums over the tile's tokens, of the weights and of the values' zeros:
-          // rows 16 q .., a quarter of the tokens
-          if (q < nch) {
-            const __half* zr = reinterpret_cast<const __half*>(sm + Ge::S_ZV) + (par * 8 + n8) * Ge::ZLD + kq;
-            // 8 x 8 blocks (tokens x rows) of weights, transposed on the way
-            const int blk = lane >> 3;
-            const uint32_t pa = sm0 + Ge::S_P + par * Ge::P_B + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 +
-                                (lane & 7) * 16;
-#pragma unroll
-            for (int ks = 2 * part; ks < 2 * part + 2; ++ks) {
-              uint32_t av[4];
-              tc_ldm<true>(av, pa + ks * 256);
-              tc_mma16816(acc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
-                          *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
-            }
-          }
         }
+        sums(g.t1 - 1, (it0 + g.t1 - 1 - g.t0) & 1);
         if (q < nch) {
           float* z = lz_s + (part * 64 + 16 * q + n8) * 8 + kq;
           z[0] = acc[0];
