@@ -97,7 +97,7 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 
 // The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all
 // fit.  Tensor cores: up to 64 rows a block, more in blocks of equal size (each
-// unpacks the cache again); one block of threads per SM.
+// unpacks the cache again); two blocks of threads per SM.
 static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
   const int rows = gq * N;
   TreePlan p;
@@ -112,7 +112,7 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 128;
-    p.ctas = sms;
+    p.ctas = 2 * sms;
     p.min_w = 1;
   }
   return p;

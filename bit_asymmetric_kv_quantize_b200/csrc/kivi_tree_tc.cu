@@ -7,10 +7,10 @@ namespace {
 
 template <int D, int BITS>
 cudaError_t tc_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  constexpr int bytes = TcGeo<D, BITS, (int)sizeof(float)>::BYTES;
-  static_assert(bytes <= 226 * 1024, "shared memory of a block");
+  const int bytes = a.N * ((a.N + 31) / 32) * 4 + TcGeo<D, BITS, (int)sizeof(float)>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, BITS, float>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             TcGeo<D, BITS, (int)sizeof(float)>::MOST);
   if (e != cudaSuccess) return e;
   tree_tc_kernel<D, BITS, float><<<p.ctas, kTcThreads, bytes, s>>>(a, p);
   return cudaGetLastError();

@@ -36,21 +36,22 @@
 // that held, and the rare tile where it did not raises the references, rescales
 // O^T in tensor memory and forms its weights again.
 //
-// Sixteen warps walk through the tiles together, one barrier of the block a tile (no
-// polled hand-overs); warp w has lanes 32 (w % 4) .. + 31 of tensor memory and a
-// quarter w / 4 of the columns.  Between two barriers, for tile t:
-//   sums over tile t - 1's tokens; scales and zeros set out, of tile t + 2's keys and
-//   of tile t + 1's values;
-//   tile t + 1's keys unpacked, and their zeros' products;
-//   tile t's weights (its scores were begun at the barrier before), its values
-//   unpacked.
-// A further warp then issues the scores of tile t + 1 and the value products of t.
+// Two blocks of threads share an SM, so that one computes while the other waits for
+// its matrix instructions or for tensor memory's store port (unpacking writes 128 KB
+// a tile, about 1000 cycles of it).  A block's eight warps walk through a tile
+// together; warp w has lanes 32 (w % 4) .. + 31 of tensor memory and half of the
+// columns.  For each tile:
+//   scales and zeros set out; keys unpacked, and their zeros' products
+//   (a further warp issues the score products)
+//   weights; values unpacked, into the keys' place
+//   (it issues the value products)
+//   sums over the tile's tokens
 // One more warp issues the copies (cp.async.bulk of each tile's ranges into a ring).
-// With a role to each warp instead, handing over by mbarriers, the same work took
-// twice as long: the waiting warps' polling and their different code filled the
-// issue slots and the instruction cache.  Waits on copies and matrix instructions
-// are bounded: one that runs out marks the block dead, whose further waits return
-// soon and whose results are NaN.
+// With a role to each warp and mbarriers between them, the same work took twice as
+// long: the waiting warps' polling and their different code filled the issue slots and
+// the instruction cache.  Waits on copies and matrix instructions are bounded: one
+// that runs out marks the block dead, whose further waits return soon and whose
+// results are NaN.
 #pragma once
 
 #include <type_traits>
@@ -61,8 +62,8 @@ namespace kivi {
 namespace {
 
 constexpr int kTcTile = 128;        // tokens
-constexpr int kTcWorkers = 512;
-constexpr int kTcWarps = 18;  // workers, matrix instructions, copies
+constexpr int kTcWorkers = 256;
+constexpr int kTcWarps = 10;  // workers, matrix instructions, copies
 constexpr int kTcThreads = kTcWarps * 32;
 constexpr float kTcSlack = 14.0f;   // log2 units a score may exceed m by
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
@@ -84,28 +85,29 @@ struct TcGeo {
   static constexpr int O_VS = O_VC + 4 * VC;
   static constexpr int O_VZ = O_VS + 4 * VM;
   static constexpr int STAGE = O_VZ + 4 * VM;
-  static constexpr int NST = STAGE <= 20480 ? 5 : 4;
+  static constexpr int NST = 49152 / STAGE < 5 ? 49152 / STAGE : 5;
   // shared memory
   static constexpr int S_RING = 0;
   static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
-  static constexpr int S_P = S_Q + 64 * D * 2;           // 2 x [64 rows][128 tokens]
-  static constexpr int P_B = 64 * 128 * 2;
-  static constexpr int S_RAW = S_P + 2 * P_B;            // raw values [128 tokens][D]
-  static constexpr int S_KSC = S_RAW + 128 * D * 2;      // 2 x 4 groups x D x (hi, lo) halves
-  static constexpr int S_VSC = S_KSC + 2 * 4 * D * 4;    // 2 x 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // 2 x [4 parts][4 groups][64 rows] float
-  static constexpr int S_OFF = S_ZK + 2 * 16 * 64 * 4;   // [16 warps][16 rows]
-  static constexpr int S_WMAX = S_OFF + 16 * 16 * 4;     // [4 groups][64 rows]
+  static constexpr int S_P = S_Q + 64 * D * 2;           // [64 rows][128 tokens]
+  static constexpr int S_RAW = S_P + 64 * 128 * 2;       // raw values [32 tokens][D]
+  static constexpr int S_KSC = S_RAW + 32 * D * 2;       // 4 groups x D x (hi, lo) halves
+  static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 4 groups x 128 x (hi, lo)
+  static constexpr int S_ZK = S_VSC + 4 * 128 * 4;       // [2 parts][4 groups][64 rows] float
+  static constexpr int S_OFF = S_ZK + 2 * 4 * 64 * 4;    // [8 warps][16 rows]
+  static constexpr int S_WMAX = S_OFF + 8 * 16 * 4;      // [4 groups][64 rows]
   static constexpr int S_M = S_WMAX + 4 * 64 * 4;        // [64 rows]
   static constexpr int S_F = S_M + 64 * 4;               // [64 rows]
-  static constexpr int S_LZ = S_F + 64 * 4;              // [4 parts][64 rows][8]
-  static constexpr int S_MASK = S_LZ + 4 * 64 * 8 * 4;   // [256][8] words
+  static constexpr int S_LZ = S_F + 64 * 4;              // [2 parts][64 rows][8]
   // zeros as binary16 in operand order, rows padded against bank conflicts:
-  // keys 4 groups x D, values 8 rows x 128 tokens (4 groups, ones, nothing)
+  // keys 4 groups x D, values 5 rows x 128 tokens (4 groups, ones)
   static constexpr int ZLD = 136;
-  static constexpr int S_ZH = S_MASK + 256 * 8 * 4;
-  static constexpr int S_ZV = S_ZH + 2 * 4 * ZLD * 2;    // 2 x keys', 4 x values'
-  static constexpr int BYTES = S_ZV + 4 * 8 * ZLD * 2;
+  static constexpr int S_ZH = S_LZ + 2 * 64 * 8 * 4;
+  static constexpr int S_ZV = S_ZH + 4 * ZLD * 2;        // 2 x
+  static constexpr int S_MASK = S_ZV + 2 * 5 * ZLD * 2;  // [N][ceil(N / 32)] words
+  static constexpr int BYTES = S_MASK;                   // and the mask
+  static constexpr int MOST = (227 * 1024 + 1024) / 2 - 1024;  // of two blocks on an SM
+  static_assert(NST >= 2 && BYTES + 256 * 8 * 4 + 256 <= MOST, "two blocks share an SM");
 };
 
 // Position of code i of a block of E in the order of the operands: the pair
@@ -287,10 +289,16 @@ __device__ __forceinline__ void tc_ldm(uint32_t (&a)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// Barriers: of the workers (1), and of the block with a vote (2: a thread's `x`).
+// Barriers: of the workers (1), of them and the warp of the matrix instructions (3),
+// and of the block with a vote (2: a thread's `x`).
 __device__ __forceinline__ void tc_sync_workers() {
   tc_fence_before();
   asm volatile("bar.sync 1, %0;" ::"n"(kTcWorkers) : "memory");
+  tc_fence_after();
+}
+__device__ __forceinline__ void tc_sync_scores() {
+  tc_fence_before();
+  asm volatile("bar.sync 3, %0;" ::"n"(kTcWorkers + 32) : "memory");
   tc_fence_after();
 }
 __device__ __forceinline__ bool tc_sync_any(bool x) {
@@ -429,7 +437,7 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-// Units `part`, part + 4, .. (of n) of a lane's words (`stride` words apart) into its
+// Units `part`, part + 2, .. (of n) of a lane's words (`stride` words apart) into its
 // row of the two planes; hi, lo: the parts of the row's scales.
 template <int BITS>
 __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, int stride,
@@ -438,7 +446,7 @@ __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, 
   using U = TcUnit<BITS>;
   constexpr int H = U::kUnit / 16;
 #pragma unroll(H == 2 ? 1 : 2)
-  for (int u = part; u < n; u += 4) {
+  for (int u = part; u < n; u += 2) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
     for (int i = 0; i < U::kUnitW; ++i) w[i] = words[(u * U::kUnitW + i) * stride];
@@ -486,26 +494,27 @@ __device__ __forceinline__ void tc_raw_pairs(const uint4& x, const uint4& y, uin
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
 }
-// 128 raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
+// 32 raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
 // at dp up to n) into rows of D in shared memory, by all workers.  Loads without
 // branches, so that they are under way together; a token that does not exist reads
 // the window's first row.
 template <int D>
 __device__ __forceinline__ void tc_stage_raw(uint4* dst, const __half* wp, const __half* dp,
                                              int first, int r, int n) {
-  constexpr int J = 128 * (D / 8) / kTcWorkers;
+  constexpr int J = (32 * (D / 8) + kTcWorkers - 1) / kTcWorkers;
   const bool al = ((uintptr_t)dp & 15) == 0;
   uint4 x[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int k = threadIdx.x + kTcWorkers * j, i = first + k / (D / 8), c = k % (D / 8) * 8;
+    const int k = (threadIdx.x + kTcWorkers * j) % (32 * (D / 8)), i = first + k / (D / 8);
+    const int c = k % (D / 8) * 8;
     x[j] = *reinterpret_cast<const uint4*>(al && i >= r && i < n ? dp + (i - r) * D + c
                                                                  : wp + (i < r ? i * D + c : c));
     if (i >= n) x[j] = make_uint4(0, 0, 0, 0);
     if (!al && i >= r && i < n) x[j] = tc_raw8(dp + (i - r) * D + c, false);
   }
 #pragma unroll
-  for (int j = 0; j < J; ++j) dst[threadIdx.x + kTcWorkers * j] = x[j];
+  for (int j = 0; j < J; ++j) dst[(threadIdx.x + kTcWorkers * j) % (32 * (D / 8))] = x[j];
 }
 // A lane's raw key row, halved, into its operand row, 16-place pieces c0 .. c0 + N - 1:
 // two runs of 8 channels E / 2 apart each (or two blocks of 8 channels).  Loads as
@@ -529,16 +538,14 @@ __device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* row, bo
     tc_st8(t_hi + 8 * (c0 + j), r);
   }
 }
-// A lane's channel of 128 raw tokens (`v`, rows of D in shared memory), halved, into
-// its operand row: 16-place pieces `part`, part + 4.  Infinities and NaN are left
-// out (they join at the segment's end, for the rows that attend to them); returns
-// whether there were any.
+// 16 places of a lane's channel of 32 raw tokens (`v`, rows of D in shared memory),
+// halved, into its operand row.  Infinities and NaN are left out (they join at the
+// segment's end, for the rows that attend to them); returns whether there were any.
 template <int D, int E>
-__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, int part) {
+__device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, int piece) {
   uint32_t odd = 0;
-#pragma unroll 1
-  for (int c = part; c < 8; c += 4) {
-    const __half* s0 = v + (E >= 16 ? 16 * c / E * E + 16 * c % E / 2 : 16 * c) * D;
+  {
+    const __half* s0 = v + (E >= 16 ? 16 * piece / E * E + 16 * piece % E / 2 : 16 * piece) * D;
     const __half* s1 = s0 + (E >= 16 ? E / 2 : 8) * D;
     uint32_t a[8], b[8];
 #pragma unroll
@@ -556,7 +563,7 @@ __device__ __forceinline__ bool tc_raw_values(uint32_t t_hi, const __half* v, in
       odd |= f;
       q[j] &= ~((f >> 15) * 0xFFFFu);
     }
-    tc_st8(t_hi + 8 * c, q);
+    tc_st8(t_hi, q);
   }
   return odd != 0;
 }
@@ -568,17 +575,18 @@ __device__ __forceinline__ bool tc_uniform(bool x) {
 // Whether rows row0 .. row0 + 15 see drafted token `node`, one bit each.
 __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, int row0, int N) {
   uint32_t bits = 0;
+  const int mw = (N + 31) / 32;
   int q = row0 % N;
 #pragma unroll 1
   for (int e = 0; e < 16; ++e) {
-    bits |= ((mask_s[q * 8 + (node >> 5)] >> (node & 31)) & 1u) << e;
+    bits |= ((mask_s[q * mw + (node >> 5)] >> (node & 31)) & 1u) << e;
     if (++q == N) q = 0;
   }
   return bits;
 }
 
-// Tensor-memory columns: two planes of keys and of values, O^T, two S^T.
-constexpr uint32_t kTK = 0, kTV = 128, kTO = 256, kTS = 320;
+// Tensor-memory columns: two planes of keys, then of values; S^T; O^T.
+constexpr uint32_t kTA = 0, kTS = 128, kTO = 192, kTCols = 256;
 
 // Barriers for what is asynchronous, 8 bytes each, by their number.
 struct TcBar {
@@ -600,7 +608,7 @@ struct TcWalk {
 };
 
 template <int D, int BITS, typename M>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, TreePlan p) {
+__global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, TreePlan p) {
   using Ge = TcGeo<D, BITS, (int)sizeof(M)>;
   constexpr int E = Ge::E, WK = Ge::WK, NJ = Ge::NJ;
   constexpr int KS = D / 16;  // k-slices of the scores
@@ -619,9 +627,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   const int nr = p.rb, nch = nr / 16;
 
   // ---- set-up
-  if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     tc_smem(&s_tmem))
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc_smem(&s_tmem)),
+                 "n"(kTCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -646,8 +655,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     for (int i = 0; i < TcBar::N; ++i) tc_bar_init(bar(i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < 4 * 8 * Ge::ZLD; i += kTcThreads)
-    reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 8 == 4 ? 1.0f : 0.0f);
+  for (int i = tid; i < 2 * 5 * Ge::ZLD; i += kTcThreads)
+    reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 5 == 4 ? 1.0f : 0.0f);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
 
   float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // references
   float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // factors of a rise
-  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [tile parity][part][group][64]
+  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [part][group][64]
   float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [part][64][8]
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     return g;
   };
 
-  if (warp == 17) {
+  if (warp == 9) {
     // ==== copies: lane k < 6 copies a tile's part of array k, in one piece, or one for
     // each page that it touches; a tile's stage is free once the block has passed the
     // barrier of the tile NST before it
@@ -745,10 +754,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     fill();
     while (tc_uniform(walk.left > 0)) {
       const TcSeg g = next_seg(walk);
-      for (int t = g.t0 - 1; t < g.t1; ++t) {  // the block's barriers
-        if (!g.ok) break;
+      for (int t = g.t0; t < g.t1 && g.ok; ++t) {  // the block's barriers
         if (tc_sync_any(false)) tc_sync_any(false);
-        if (t >= g.t0 && t < g.t1s) {
+        if (t < g.t1s) {
           ++done;
           fill();
         }
@@ -756,48 +764,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
     }
     for (int i = max(issued - Ge::NST, 0); i < issued; ++i)  // none is under way at the end
       tc_wait(bar(TcBar::raw + i % Ge::NST), i / Ge::NST, dead);
-  } else if (warp == 16) {
-    // ==== matrix instructions, after each barrier: the scores of the next tile,
-    // the value products of this one
+  } else if (warp == 8) {
+    // ==== matrix instructions
     const bool one = tc_elect();
     const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
-    const uint64_t q_desc = tc_desc(sm0 + Ge::S_Q, 128, D * 16);
-    int it = 0;
+    const uint64_t q_desc = tc_desc(sm0 + Ge::S_Q, 128, D * 16), p_desc = tc_desc(sm0 + Ge::S_P, 128, 2048);
     while (tc_uniform(walk.left > 0)) {
       const TcSeg g = next_seg(walk);
       if (!g.ok) continue;
-      for (int t = g.t0 - 1; t < g.t1; ++t) {
-        if (tc_sync_any(false)) tc_sync_any(false);
-        const int par = __shfl_sync(0xffffffffu, it & 1, 0);  // of tile t + 1
+      for (int t = g.t0; t < g.t1; ++t) {
+        const bool lo = t < g.t1s;
+        tc_sync_scores();
         if (one) {
-          if (t + 1 < g.t1) {
-            const uint32_t d = tmem + kTS + 64 * par;
-            tc_mma_row<KS>(d, tmem + kTK, q_desc, id_s, false);
-            if (t + 1 < g.t1s) tc_mma_row<KS>(d, tmem + kTK + 64, q_desc, id_s, true);
-            tc_commit(bar(TcBar::scores));
-          }
-          if (t >= g.t0) {
-            const uint64_t b = tc_desc(sm0 + Ge::S_P + (par ^ 1) * Ge::P_B, 128, 2048);
-            tc_mma_row<8>(tmem + kTO, tmem + kTV, b, id_o, t > g.t0);
-            if (t < g.t1s) tc_mma_row<8>(tmem + kTO, tmem + kTV + 64, b, id_o, true);
-            tc_commit(bar(TcBar::values));
-          }
+          tc_mma_row<KS>(tmem + kTS, tmem + kTA, q_desc, id_s, false);
+          if (lo) tc_mma_row<KS>(tmem + kTS, tmem + kTA + 64, q_desc, id_s, true);
+          tc_commit(bar(TcBar::scores));
         }
         __syncwarp();
-        if (t + 1 < g.t1) ++it;
+        if (tc_sync_any(false)) tc_sync_any(false);
+        if (one) {
+          tc_mma_row<8>(tmem + kTO, tmem + kTA, p_desc, id_o, t > g.t0);
+          if (lo) tc_mma_row<8>(tmem + kTO, tmem + kTA + 64, p_desc, id_o, true);
+          tc_commit(bar(TcBar::values));
+        }
+        __syncwarp();
       }
     }
   } else {
     // ==== workers
-    const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, quarter of columns
+    const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, half of the columns
     const uint32_t t_q = tmem + ((uint32_t)(q * 32) << 16);
     const int n8 = lane >> 2, kq = (lane & 3) * 2;  // fragments of mma.sync
     const int pk = tc_pos<E>(q * 32 + lane);        // this lane's token in the second product
     const float c1 = 2.0f * a.qscale;
     const TcConst konst = tc_const();
-    __half* ksc0 = reinterpret_cast<__half*>(sm + Ge::S_KSC);
-    __half* vsc0 = reinterpret_cast<__half*>(sm + Ge::S_VSC);
-    __half* zh0 = reinterpret_cast<__half*>(sm + Ge::S_ZH);
+    __half* ksc = reinterpret_cast<__half*>(sm + Ge::S_KSC);
+    __half* vsc = reinterpret_cast<__half*>(sm + Ge::S_VSC);
+    __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
     __half* zv0 = reinterpret_cast<__half*>(sm + Ge::S_ZV);
     float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + warp * 16;
     float* wmax_s = reinterpret_cast<float*>(sm + Ge::S_WMAX);
@@ -839,99 +842,94 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         }
 #pragma unroll 1
         for (int i = tid; i < a.N * mw; i += kTcWorkers)
-          mask_s[i / mw * 8 + i % mw] = a.mask[g.b * a.N * mw + i];
+          mask_s[i] = a.mask[g.b * a.N * mw + i];
         if (tid < 64) m_s[tid] = kTcNone;
       }
       tc_fence_smem();
 
-      // scales and zeros of tile t's keys, or of its values
-      auto set_keys = [&](int t) {
-        if (t >= g.t1s) return;
-        const int st = st0 + t - g.t0, s = st % Ge::NST;
-        const unsigned char* stg = sm + Ge::S_RING + s * Ge::STAGE;
-        __half* zh = zh0 + (t & 1) * 4 * Ge::ZLD;
-        __half* ksc = ksc0 + (t & 1) * 8 * D;
-        tc_wait(bar(TcBar::raw + s), st / Ge::NST, dead);
-        if (tid < 4 * D) {
-          const int gr = tid / D, c = tc_pos<E>(tid % D);
-          zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[tid]));
-          tc_split(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[tid]), &ksc[gr * 2 * D + c],
-                   &ksc[gr * 2 * D + D + c]);
+      // scales and zeros of tile t's keys and values
+      auto set_out = [&](int t) {
+        __half* zv = zv0 + (t & 1) * 5 * Ge::ZLD;
+        const bool raw = t >= g.t1s;
+        const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+        if (!raw) {
+          tc_wait(bar(TcBar::raw + (st0 + t - g.t0) % Ge::NST), (st0 + t - g.t0) / Ge::NST, dead);
+#pragma unroll
+          for (int j = 0; j < (4 * D + kTcWorkers - 1) / kTcWorkers; ++j) {
+            const int i = tid + kTcWorkers * j, gr = i / D, c = tc_pos<E>(i % D);
+            if (i < 4 * D) {
+              zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[i]));
+              tc_split(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[i]), &ksc[gr * 2 * D + c],
+                       &ksc[gr * 2 * D + D + c]);
+            }
+          }
         }
-      };
-      auto set_values = [&](int t) {
-        __half* zv = zv0 + (t & 3) * 8 * Ge::ZLD;
-        __half* vsc = vsc0 + (t & 1) * 1024;
-        if (tid >= 128 * NJ) return;
-        const int tok = tid / NJ, j = tid % NJ, c = tc_pos<E>(tok);
-        float z = 0.f;
-        if (t < g.t1s) {
-          const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-          // tokens that do not exist: 0 (their weight 0 times NaN would not be)
-          const bool have = tok < g.n_q - (long long)t * kTcTile;
-          z = have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[tid]) : 0.f;
-          tc_split(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[tid]) : 0.f,
-                   &vsc[j * 256 + c], &vsc[j * 256 + 128 + c]);
+        const long long left = g.n_q - (long long)t * kTcTile;
+#pragma unroll
+        for (int j = 0; j < (128 * NJ + kTcWorkers - 1) / kTcWorkers; ++j) {
+          const int i = tid + kTcWorkers * j, tok = i / NJ, gr = i % NJ, c = tc_pos<E>(tok);
+          if (i < 128 * NJ) {
+            // tokens that do not exist: 0 (their weight 0 times NaN would not be)
+            const bool have = !raw && tok < left;
+            zv[gr * Ge::ZLD + c] =
+                __float2half_rn(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[i]) : 0.f);
+            tc_split(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[i]) : 0.f,
+                     &vsc[gr * 256 + c], &vsc[gr * 256 + 128 + c]);
+          }
         }
-        zv[j * Ge::ZLD + c] = __float2half_rn(z);
       };
       // keys of tile t into tensor memory, and their zeros' products
-      auto put_keys = [&](int t, int par) {
+      auto put_keys = [&](int t) {
         float zc[4] = {0.f, 0.f, 0.f, 0.f};
         if (t < g.t1s) {
           const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-          const __half* sc = ksc0 + (t & 1) * 8 * D + q * 2 * D;
-          tc_unpack<BITS>(t_q + kTK, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
+          const __half* sc = ksc + q * 2 * D;
+          tc_unpack<BITS>(t_q + kTA, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
                           reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
                           D / TcUnit<BITS>::kUnit, konst);
           if (q < nch) {
-            // sum_d q_d z_gd for rows 16 q .., over a quarter of the channels (this warp's
-            // q counts rows here); lane n8 of a column reads group n8's row, columns 4 .. 7
+            // sum_d q_d z_gd for rows 16 q .., over half of the channels (this warp's q
+            // counts rows here); lane n8 of a column reads group n8's row, columns 4 .. 7
             // are read by nobody
-            const __half* zr = zh0 + (t & 1) * 4 * Ge::ZLD + (n8 & 3) * Ge::ZLD + kq;
+            const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
             const int row = 16 * q + (lane & 15);
             const uint32_t qa = sm0 + Ge::S_Q + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
 #pragma unroll
-            for (int j = 0; j < (KS + 3) / 4; ++j) {
-              const int ks = part + 4 * j;
-              if (ks < KS) {
-                uint32_t av[4];
-                tc_ldm<false>(av, qa + 256 * ks);
-                tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
-                            *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
-              }
+            for (int j = 0; j < KS / 2; ++j) {
+              const int ks = part + 2 * j;
+              uint32_t av[4];
+              tc_ldm<false>(av, qa + 256 * ks);
+              tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                          *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
             }
           }
         } else {
           // raw tokens: the window, then the drafted ones; halved like s
           const int i = (t - g.tq) * kTcTile + q * 32 + lane;
           const __half* src = i < g.r ? wk + i * D : (i < n_raw ? dk + (i - g.r) * D : wk);
-          if (16 * part < D) {
-            tc_raw_keys<E, 1>(t_q + kTK, src, i < n_raw, part);
-            if (D == 128) tc_raw_keys<E, 1>(t_q + kTK, src, i < n_raw, part + 4);
-          }
+          tc_raw_keys<E, D / 32>(t_q + kTA, src, i < n_raw, part * (D / 32));
         }
         if (q < nch && kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
-          float* z = zk_s + ((par * 4 + part) * 4 + kq) * 64 + 16 * q + n8;
+          float* z = zk_s + (part * 4 + kq) * 64 + 16 * q + n8;
           z[0] = zc[0] * a.qscale;
           z[64] = zc[1] * a.qscale;
           z[8] = zc[2] * a.qscale;
           z[72] = zc[3] * a.qscale;
         }
       };
-
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       // sums over tile t's tokens, of the weights and of the values' zeros: rows 16 q ..,
-      // a quarter of the tokens
-      auto sums = [&](int t, int par) {
+      // half of the tokens
+      auto sums = [&](int t) {
         if (q >= nch) return;
-        const __half* zr = zv0 + ((t & 3) * 8 + n8) * Ge::ZLD + kq;
+        // (columns 5 .. 7 are read by nobody)
+        const __half* zr = zv0 + ((t & 1) * 5 + (n8 < 4 ? n8 : 4)) * Ge::ZLD + kq;
         // 8 x 8 blocks (tokens x rows) of weights, transposed on the way
         const int blk = lane >> 3;
-        const uint32_t pa = sm0 + Ge::S_P + par * Ge::P_B + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 +
-                            (lane & 7) * 16;
+        const uint32_t pa = sm0 + Ge::S_P + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 + (lane & 7) * 16;
 #pragma unroll
-        for (int ks = 2 * part; ks < 2 * part + 2; ++ks) {
+        for (int j = 0; j < 4; ++j) {
+          const int ks = 4 * part + j;
           uint32_t av[4];
           tc_ldm<true>(av, pa + ks * 256);
           tc_mma16816(acc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
@@ -941,99 +939,102 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
 
       if (g.ok) {
         tc_sync_workers();
-        set_keys(g.t0);
-        tc_sync_workers();
 #pragma unroll 1
-        for (int t = g.t0 - 1; t < g.t1; ++t) {
-          const int it = it0 + t - g.t0, par = it & 1;
-          const bool raw = t >= g.t1s, more = t + 1 < g.t1;
-          if (t > g.t0) sums(t - 1, par ^ 1);
-          if (t + 2 < g.t1) set_keys(t + 2);
-          if (more) set_values(t + 1);
-          if (t < g.t0) {  // the first keys
-            put_keys(g.t0, par ^ 1);
-            tc_wait_st();
-            tc_sync_any(false);
-            continue;
-          }
-          if (raw)
-            tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv, (t - g.tq) * kTcTile, g.r, n_raw);
-          tc_wait(bar(TcBar::scores), it, dead);
-          tc_fence_after();
-          if (more) put_keys(t + 1, par ^ 1);
-          // ---- weights of rows 16 part .., against the references; `over`: by how much
-          // a score exceeds its own.  The lane's token: in the cache (all rows see it),
-          // drafted, or none
-          const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + q * 32 + lane;
-          const bool in = raw ? i < g.r : i < g.n_q;
-          const int node = raw && i >= g.r && i < n_raw ? (int)(i - g.r) : -1;
-          const uint32_t t_s = t_q + kTS + 64 * par + 16 * part;
-          unsigned char* pb = sm + Ge::S_P + par * Ge::P_B + pk / 8 * 128 + pk % 8 * 16 + part * 4096;
-          uint32_t sees = 0xFFFFu;  // one bit for each row
-          if (!in) sees = node < 0 || part >= nch ? 0u : tc_seen(mask_s, node, g.row0 + 16 * part, a.N);
-          // the zeros' products of the lane's group
-          auto zk = [&](int row) {
-            const float* z = zk_s + (par * 16 + q) * 64 + row;
-            return (z[0] + z[4 * 64]) + (z[8 * 64] + z[12 * 64]);
-          };
-          auto weights = [&]() -> float {
-            if (lane < 16) off_s[lane] = m_s[16 * part + lane] - zk(16 * part + lane);
-            __syncwarp();
-            float v[16], over = -__builtin_huge_valf();
-            tc_ld16(t_s, v);
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-              const float4 o = *reinterpret_cast<const float4*>(off_s + 4 * e4);
-              v[4 * e4] = fmaf(v[4 * e4], c1, -o.x);
-              v[4 * e4 + 1] = fmaf(v[4 * e4 + 1], c1, -o.y);
-              v[4 * e4 + 2] = fmaf(v[4 * e4 + 2], c1, -o.z);
-              v[4 * e4 + 3] = fmaf(v[4 * e4 + 3], c1, -o.w);
-            }
-            if (__any_sync(0xffffffffu, sees != 0xFFFFu)) {  // raw tokens, or the end
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!((sees >> e) & 1u)) v[e] = -__builtin_huge_valf();
-            }
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              over = fmaxf(over, fmaxf(v[e], v[e + 1]));
-              const __half2 h = __floats2half2_rn(tc_ex2(v[e]), tc_ex2(v[e + 1]));
-              w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(pb) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(pb + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
-            return over;
-          };
-          float over = -__builtin_huge_valf();
-          if (part < nch) over = weights();
-          // ---- values
-          if (raw) tc_sync_workers();
-          if (t > g.t0) {
+        for (int t = g.t0; t < g.t1; ++t) {
+          const int it = it0 + t - g.t0;
+          const bool raw = t >= g.t1s;
+          // ---- keys
+          set_out(t);
+          tc_sync_workers();
+          if (t > g.t0) {  // the planes were read, and so were the weights
             tc_wait(bar(TcBar::values), it - 1, dead);
             tc_fence_after();
           }
-          if (q < NJ) {
-            if (!raw) {
-              const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-              const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
-              tc_unpack<BITS>(t_q + kTV, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
-                              reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
-                              128 / TcUnit<BITS>::kUnit, konst);
-            } else if (tc_raw_values<D, E>(t_q + kTV, reinterpret_cast<const __half*>(sm + Ge::S_RAW) + q * 32 + lane,
-                                           part)) {
-              s_odd = 1;
+          put_keys(t);
+          tc_wait_st();
+          tc_sync_scores();
+          // ---- weights of 16-row chunks part, part + 2, against the references; `over`: by
+          // how much a score exceeds its own.  The lane's token: in the cache (all rows see
+          // it), drafted, or none
+          const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + q * 32 + lane;
+          const bool in = raw ? i < g.r : i < g.n_q;
+          const int node = raw && i >= g.r && i < n_raw ? (int)(i - g.r) : -1;
+          auto seen = [&](int ch) -> uint32_t {  // one bit for each row
+            return in ? 0xFFFFu : node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + 16 * ch, a.N);
+          };
+          unsigned char* pb = sm + Ge::S_P + pk / 8 * 128 + pk % 8 * 16;
+          const float* zk = zk_s + q * 64;  // the zeros' products of the lane's group
+          auto weights = [&]() -> float {
+            float over = -__builtin_huge_valf();
+#pragma unroll 1
+            for (int ch = part; ch < nch; ch += 2) {
+              if (lane < 16) {
+                const int row = 16 * ch + lane;
+                off_s[lane] = m_s[row] - (zk[row] + zk[4 * 64 + row]);
+              }
+              __syncwarp();
+              float v[16];
+              tc_ld16(t_q + kTS + 16 * ch, v);
+#pragma unroll
+              for (int e4 = 0; e4 < 4; ++e4) {
+                const float4 o = *reinterpret_cast<const float4*>(off_s + 4 * e4);
+                v[4 * e4] = fmaf(v[4 * e4], c1, -o.x);
+                v[4 * e4 + 1] = fmaf(v[4 * e4 + 1], c1, -o.y);
+                v[4 * e4 + 2] = fmaf(v[4 * e4 + 2], c1, -o.z);
+                v[4 * e4 + 3] = fmaf(v[4 * e4 + 3], c1, -o.w);
+              }
+              __syncwarp();
+              const uint32_t sees = seen(ch);
+              if (__any_sync(0xffffffffu, sees != 0xFFFFu)) {  // raw tokens, or the end
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (!((sees >> e) & 1u)) v[e] = -__builtin_huge_valf();
+              }
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                over = fmaxf(over, fmaxf(v[e], v[e + 1]));
+                const __half2 h = __floats2half2_rn(tc_ex2(v[e]), tc_ex2(v[e + 1]));
+                w[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(pb + ch * 4096) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(pb + ch * 4096 + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
             }
+            return over;
+          };
+          tc_wait(bar(TcBar::scores), it, dead);
+          tc_fence_after();
+          const float over = weights();
+          // ---- values, into the keys' place
+          if (raw) {
+#pragma unroll 1
+            for (int b32 = 0; b32 < 4; ++b32) {
+              tc_sync_workers();
+              tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv, (t - g.tq) * kTcTile + 32 * b32,
+                              g.r, n_raw);
+              tc_sync_workers();
+              if (q < NJ && tc_raw_values<D, E>(t_q + kTA + 16 * b32 + 8 * part,
+                                                reinterpret_cast<const __half*>(sm + Ge::S_RAW) + q * 32 + lane, part))
+                s_odd = 1;
+            }
+          } else if (q < NJ) {
+            const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+            const __half* sc = vsc + q * 256;
+            tc_unpack<BITS>(t_q + kTA, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
+                            reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
+                            128 / TcUnit<BITS>::kUnit, konst);
           }
           tc_wait_st();
           tc_fence_smem();
           const bool rise = tc_uniform(tc_sync_any(over > kTcSlack));
           if (rise) {
             // ---- new references: the maxima of the tile, joined over its groups
-            if (part < nch) {
+#pragma unroll 1
+            for (int ch = part; ch < nch; ch += 2) {
               float v[16];
-              tc_ld16(t_s, v);
-              const float z = lane < 16 ? zk(16 * part + lane) : 0.f;
+              tc_ld16(t_q + kTS + 16 * ch, v);
+              const uint32_t sees = seen(ch);
+              const float z = lane < 16 ? zk[16 * ch + lane] + zk[4 * 64 + 16 * ch + lane] : 0.f;
               float mine = kTcNone;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -1041,7 +1042,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
                 const float m = tc_warp_max((sees >> e) & 1u ? d : kTcNone);
                 if (lane == e) mine = m;
               }
-              if (lane < 16) wmax_s[q * 64 + 16 * part + lane] = mine;
+              if (lane < 16) wmax_s[q * 64 + 16 * ch + lane] = mine;
             }
             tc_sync_workers();
             if (tid < nr) {
@@ -1053,16 +1054,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
               m_s[tid] = mn;
             }
             tc_sync_workers();
-            if (part < nch) {
-              weights();
-              if (t > g.t0) {  // the accumulators so far (their products are done)
+            weights();
+            if (t > g.t0) {  // the accumulators so far (their products are done)
+#pragma unroll 1
+              for (int ch = part; ch < nch; ch += 2) {
                 float v[16];
-                tc_ld16(t_q + kTO + 16 * part, v);
+                tc_ld16(t_q + kTO + 16 * ch, v);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] *= f_s[16 * part + k];
-                tc_st16(t_q + kTO + 16 * part, v);
-                tc_wait_st();
+                for (int k = 0; k < 16; ++k) v[k] *= f_s[16 * ch + k];
+                tc_st16(t_q + kTO + 16 * ch, v);
               }
+              tc_wait_st();
             }
             if (q < nch) {
               const float f0 = f_s[16 * q + n8], f1 = f_s[16 * q + n8 + 8];
@@ -1074,8 +1076,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             tc_fence_smem();
             tc_sync_any(false);
           }
+          sums(t);
         }
-        sums(g.t1 - 1, (it0 + g.t1 - 1 - g.t0) & 1);
         if (q < nch) {
           float* z = lz_s + (part * 64 + 16 * q + n8) * 8 + kq;
           z[0] = acc[0];
@@ -1087,7 +1089,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
       }
       tc_sync_workers();
 
-      // ---- end of a segment: lane = channel, rows 4 part .. of each 16
+      // ---- end of a segment: lane = channel, rows 4 part .. of each 8
       {
         const int ch_d = q * 32 + lane;
         const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
         float* pt = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
         __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
 #pragma unroll 1
-        for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 16) {
+        for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 8) {
           float v[4] = {0.f, 0.f, 0.f, 0.f};
           if (g.ok) tc_ld4(t_q + kTO + e4, v);
 #pragma unroll
@@ -1103,8 +1105,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
             const int row = e4 + e;
             if (row >= g.nrows) break;
             const float* z = lz_s + row * 8;
-            float l = (z[4] + z[512 + 4]) + (z[1024 + 4] + z[1536 + 4]), m = m_s[row];
-            float o = fmaf(2.0f, v[e], (z[q] + z[512 + q]) + (z[1024 + q] + z[1536 + q]));
+            float l = z[4] + z[512 + 4], m = m_s[row];
+            float o = fmaf(2.0f, v[e], z[q] + z[512 + q]);
             // infinite or NaN raw values, of the tokens that the row attends to
 #pragma unroll 1
             for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
@@ -1139,8 +1141,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(TreeArgs a, Tree
   }
 
   __syncthreads();
-  if (warp == 16) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 8) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTCols)
+                 : "memory");
   }
 }
 
