@@ -41,9 +41,10 @@
 // a tile, about 1000 cycles of it).  A block's eight warps walk through a tile
 // together; warp w has lanes 32 (w % 4) .. + 31 of tensor memory and half of the
 // columns.  For each tile:
-//   scales and zeros set out; keys unpacked, and their zeros' products
+//   keys unpacked, and their zeros' products
 //   (a further warp issues the score products)
-//   weights; values unpacked, into the keys' place
+//   the next tile's scales and zeros set out; weights; values unpacked, into the
+//   keys' place
 //   (it issues the value products)
 //   sums over the tile's tokens
 // One more warp issues the copies (cp.async.bulk of each tile's ranges into a ring).
@@ -90,19 +91,21 @@ struct TcGeo {
   static constexpr int S_RING = 0;
   static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
   static constexpr int S_P = S_Q + 64 * D * 2;           // [64 rows][128 tokens]
-  static constexpr int S_RAW = S_P + 64 * 128 * 2;       // raw values [32 tokens][D]
-  static constexpr int S_KSC = S_RAW + 32 * D * 2;       // 4 groups x D x (hi, lo) halves
-  static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 4 * 128 * 4;       // [2 parts][4 groups][64 rows] float
+  // raw values [32 tokens][D]; at the end of a segment the sums, [2 parts][64 rows][8]
+  static constexpr int S_RAW = S_P + 64 * 128 * 2;
+  static constexpr int S_LZ = S_RAW;
+  static constexpr int S_KSC = S_RAW + (32 * D * 2 > 2 * 64 * 8 * 4 ? 32 * D * 2 : 2 * 64 * 8 * 4);
+                                                         // 4 groups x D x (hi, lo) halves
+  static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 2 x 4 groups x 128 x (hi, lo)
+  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // [2 parts][4 groups][64 rows] float
   static constexpr int S_OFF = S_ZK + 2 * 4 * 64 * 4;    // [8 warps][16 rows]
   static constexpr int S_WMAX = S_OFF + 8 * 16 * 4;      // [4 groups][64 rows]
   static constexpr int S_M = S_WMAX + 4 * 64 * 4;        // [64 rows]
   static constexpr int S_F = S_M + 64 * 4;               // [64 rows]
-  static constexpr int S_LZ = S_F + 64 * 4;              // [2 parts][64 rows][8]
   // zeros as binary16 in operand order, rows padded against bank conflicts:
   // keys 4 groups x D, values 5 rows x 128 tokens (4 groups, ones)
   static constexpr int ZLD = 136;
-  static constexpr int S_ZH = S_LZ + 2 * 64 * 8 * 4;
+  static constexpr int S_ZH = S_F + 64 * 4;
   static constexpr int S_ZV = S_ZH + 4 * ZLD * 2;        // 2 x
   static constexpr int S_MASK = S_ZV + 2 * 5 * ZLD * 2;  // [N][ceil(N / 32)] words
   static constexpr int BYTES = S_MASK;                   // and the mask
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     const float c1 = 2.0f * a.qscale;
     const TcConst konst = tc_const();
     __half* ksc = reinterpret_cast<__half*>(sm + Ge::S_KSC);
-    __half* vsc = reinterpret_cast<__half*>(sm + Ge::S_VSC);
+    __half* vsc0 = reinterpret_cast<__half*>(sm + Ge::S_VSC);
     __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
     __half* zv0 = reinterpret_cast<__half*>(sm + Ge::S_ZV);
     float* off_s = reinterpret_cast<float*>(sm + Ge::S_OFF) + warp * 16;
@@ -850,6 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
       // scales and zeros of tile t's keys and values
       auto set_out = [&](int t) {
         __half* zv = zv0 + (t & 1) * 5 * Ge::ZLD;
+        __half* vsc = vsc0 + (t & 1) * 1024;
         const bool raw = t >= g.t1s;
         const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
         if (!raw) {
@@ -938,14 +942,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
       };
 
       if (g.ok) {
+        set_out(g.t0);
         tc_sync_workers();
 #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t) {
           const int it = it0 + t - g.t0;
           const bool raw = t >= g.t1s;
           // ---- keys
-          set_out(t);
-          tc_sync_workers();
           if (t > g.t0) {  // the planes were read, and so were the weights
             tc_wait(bar(TcBar::values), it - 1, dead);
             tc_fence_after();
@@ -953,6 +956,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
           put_keys(t);
           tc_wait_st();
           tc_sync_scores();
+          if (t + 1 < g.t1) set_out(t + 1);
           // ---- weights of 16-row chunks part, part + 2, against the references; `over`: by
           // how much a score exceeds its own.  The lane's token: in the cache (all rows see
           // it), drafted, or none
@@ -1019,7 +1023,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
             }
           } else if (q < NJ) {
             const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-            const __half* sc = vsc + q * 256;
+            const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
             tc_unpack<BITS>(t_q + kTA, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
                             reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
                             128 / TcUnit<BITS>::kUnit, konst);
