@@ -680,18 +680,31 @@ __device__ __forceinline__ CommitSpan commit_span(const CacheView& c, const DevS
   return o;
 }
 
-// Copies row `i` of the path into a row of D elements, by the block's threads
-// (blockDim.x == D).
+// n rows of D elements of the path, from its token i0 on, to slot0 .. of the window, by
+// the block's threads (blockDim.x == D), 16 bytes each where k and v are aligned so.
+// A thread always takes the same channels of every row.
 template <int D, typename T>
 __device__ __forceinline__ void commit_rows(T* kr, T* vr, const T* __restrict__ k,
                                             const T* __restrict__ v, const int* __restrict__ path,
-                                            int slot0, int i0, int n) {
-  const int d = threadIdx.x;
+                                            int slot0, int i0, int n, bool wide) {
+  constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC;  // chunks of a row
+  if (wide) {
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const long long node = path[i0 + j];
-    kr[(long long)(slot0 + j) * D + d] = k[node * D + d];
-    vr[(long long)(slot0 + j) * D + d] = v[node * D + d];
+    for (int j = threadIdx.x / CPR; j < n; j += EPC) {
+      const int d = threadIdx.x % CPR * EPC;
+      const long long node = path[i0 + j];
+      const uint4 x = *reinterpret_cast<const uint4*>(k + node * D + d);
+      const uint4 y = *reinterpret_cast<const uint4*>(v + node * D + d);
+      *reinterpret_cast<uint4*>(kr + (long long)(slot0 + j) * D + d) = x;
+      *reinterpret_cast<uint4*>(vr + (long long)(slot0 + j) * D + d) = y;
+    }
+  } else {
+    for (int j = 0; j < n; ++j) {
+      const int d = threadIdx.x;
+      const long long node = path[i0 + j];
+      kr[(long long)(slot0 + j) * D + d] = k[node * D + d];
+      vr[(long long)(slot0 + j) * D + d] = v[node * D + d];
+    }
   }
 }
 
@@ -706,7 +719,8 @@ template <int D, int BITS, typename T, typename M, bool STAGED>
 __global__ void __launch_bounds__(D, STAGED ? 8 : 1)
     commit_kernel(CacheView c, const T* __restrict__ k, const T* __restrict__ v,
                   const int* __restrict__ path, const int* __restrict__ count, int N, int P,
-                  const DevState* st, int Hkv) {
+                  const DevState* st, int Hkv, int wide) {
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) unsigned char dsm[];
   const long long unit = blockIdx.y, b = unit / Hkv;
   const int* pb = path + b * P;
@@ -722,22 +736,39 @@ __global__ void __launch_bounds__(D, STAGED ? 8 : 1)
   const T* vu = v + unit * N * D;
   // slots r .. r+cnt-1 before the flush, as far as they are this block's
   const int a0 = max(lo, sp.r), a1 = min(hi, min(sp.r + sp.cnt, c.R));
-  if (a0 < a1) commit_rows<D, T>(kr, vr, ku, vu, pb, a0, a0 - sp.r, a1 - a0);
+  if (a0 < a1) commit_rows<D, T>(kr, vr, ku, vu, pb, a0, a0 - sp.r, a1 - a0, wide);
   if (!sp.flush) return;
   // the 32 slots from shared memory: old ones from the window, new ones from k, v
   T* Ks = reinterpret_cast<T*>(dsm);
   T* Vs = Ks + kTile * D;
-#pragma unroll 8
-  for (int t = 0; t < kTile; ++t) {
-    const int d = threadIdx.x, s = lo + t;
-    const int at = STAGED ? stage_idx<D, T>(t, d) : t * D + d;
-    if (s < sp.r) {
-      Ks[at] = kr[(long long)s * D + d];
-      Vs[at] = vr[(long long)s * D + d];
-    } else {
-      const long long node = pb[s - sp.r];
-      Ks[at] = ku[node * D + d];
-      Vs[at] = vu[node * D + d];
+  if (wide) {
+    // D threads, kTile * D / EPC chunks: all of a thread's loads are under way together
+    constexpr int EPC = 16 / (int)sizeof(T), CPR = D / EPC, NCH = kTile / EPC;
+    uint4 x[NCH], y[NCH];
+    const int d = threadIdx.x % CPR * EPC;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int s = lo + threadIdx.x / CPR + EPC * j;
+      const bool old = s < sp.r;
+      const long long row = old ? s : pb[s - sp.r];
+      x[j] = *reinterpret_cast<const uint4*>((old ? kr : ku) + row * D + d);
+      y[j] = *reinterpret_cast<const uint4*>((old ? vr : vu) + row * D + d);
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int t = threadIdx.x / CPR + EPC * j;
+      const int at = STAGED ? stage_idx<D, T>(t, d) : t * D + d;
+      *reinterpret_cast<uint4*>(Ks + at) = x[j];
+      *reinterpret_cast<uint4*>(Vs + at) = y[j];
+    }
+  } else {
+    for (int t = 0; t < kTile; ++t) {
+      const int d = threadIdx.x, s = lo + t;
+      const int at = STAGED ? stage_idx<D, T>(t, d) : t * D + d;
+      const bool old = s < sp.r;
+      const long long row = old ? s : pb[s - sp.r];
+      Ks[at] = (old ? kr : ku)[row * D + d];
+      Vs[at] = (old ? vr : vu)[row * D + d];
     }
   }
   if constexpr (STAGED) {
@@ -753,18 +784,18 @@ __global__ void __launch_bounds__(D, STAGED ? 8 : 1)
     uint8_t* ck = dsm + 2 * kTile * D * sizeof(T);
     quantize_tile<D, BITS, T, M, 0, true>(c, unit, Ks, Vs, sp.n_q + lo, ck, ck + kTile * D);
   }
-  // what follows the flush starts the window anew (a block's threads write
-  // other elements of a slot than they read above: the tile is in shared
-  // memory by now, behind a barrier)
+  // what follows the flush starts the window anew (the tile is in shared memory by
+  // now, behind a barrier)
   const int f0 = lo, f1 = min(hi, sp.r + sp.cnt - c.R);
-  if (f0 < f1) commit_rows<D, T>(kr, vr, ku, vu, pb, f0, c.R - sp.r + f0, f1 - f0);
+  if (f0 < f1) commit_rows<D, T>(kr, vr, ku, vu, pb, f0, c.R - sp.r + f0, f1 - f0, wide);
 }
 
-// After commit_kernel: advance every sequence that took its path; one that
-// could not gets status 1.
+// After commit_kernel (its launch overlaps that kernel, which it then waits for):
+// advance every sequence that took its path; one that could not gets status 1.
 __global__ void advance_commit_kernel(CacheView c, const int* __restrict__ path,
                                       const int* __restrict__ count, int N, int P, DevState* st,
                                       long long B) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (long long b = blockIdx.x * (long long)blockDim.x + threadIdx.x; b < B;
        b += (long long)gridDim.x * blockDim.x) {
     const CommitSpan sp = commit_span(c, st[b], count[b], P, b);
@@ -788,17 +819,26 @@ cudaError_t commit_t(const CacheView& c, int units, int Hkv, const void* k, cons
                      const int* path, const int* count, int N, int P, DevState* st,
                      cudaStream_t s) {
   const dim3 grid((unsigned)(c.R / kTile), (unsigned)units);
+  const int wide = (((uintptr_t)k | (uintptr_t)v | (uintptr_t)c.k_res | (uintptr_t)c.v_res) & 15u) == 0;
   if (c.k_out == 0 && c.v_out == 0)
     commit_kernel<D, BITS, T, M, true><<<grid, D, StagedSmem<D, T>::BYTES, s>>>(
-        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv);
+        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv, wide);
   else
     commit_kernel<D, BITS, T, M, false><<<grid, D, 2 * kTile * D * (sizeof(T) + 1), s>>>(
-        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv);
-  cudaError_t e = cudaGetLastError();
+        c, (const T*)k, (const T*)v, path, count, N, P, st, Hkv, wide);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int B = units / Hkv;
-  advance_commit_kernel<<<(B + 127) / 128, 128, 0, s>>>(c, path, count, N, P, st, B);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((B + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, advance_commit_kernel, c, path, count, N, P, st, (long long)B);
 }
 
 template <int BITS, typename T, typename M>

@@ -54,19 +54,37 @@ __global__ void __launch_bounds__(D / (16 / (int)sizeof(T)) * 8)
   if (base < n_q) {
     long long su, stl;
     if (!store_tile(c, unit, tile, &su, &stl)) return;
-    const long long row = stl * kTile + q0;
-    float s[CH], z[CH];
+    using Lt = Layout<D, BITS>;
+    const long long row = stl * kTile + q0, Ts = store_tokens(c);
+    // all loads before the first store, which the compiler would not move them across
+    const uint32_t* ku = c.k_codes + su * Lt::k_codes_unit(Ts);
+    const long long mo = su * Lt::v_meta_unit(Ts) + row * Lt::NJ + ch0 / kGv;
+    float s[CH], z[CH], vs[4], vz[4];
+    uint32_t kw[4][Lt::WB], vw[Lt::WB][CH];
     key_meta<D, BITS, M, CH>(c, su, row, ch0, s, z);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      key_words<D, BITS, CH>(ku, row + i, ch0, kw[i]);
+      vs[i] = to_f32(static_cast<const M*>(c.v_scale)[mo + i * Lt::NJ]);
+      vz[i] = to_f32(static_cast<const M*>(c.v_zero)[mo + i * Lt::NJ]);
+    }
+    value_words<D, BITS, CH>(c.v_codes + su * Lt::v_codes_unit(Ts), row, ch0, vw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const long long t = base + q0 + i;
-      if (t >= t0 && t < end) {
-        float x[CH];
-        key_values<D, BITS, M, CH>(c, su, row + i, ch0, s, z, x);
-        store_row<T, CH>(Ko + t * D, x, wide);
-        value_values<D, BITS, M, CH>(c, su, row + i, ch0, x);
-        store_row<T, CH>(Vo + t * D, x, wide);
-      }
+      if (t < t0 || t >= end) continue;
+      int code[CH];
+      float x[CH];
+      key_codes<D, BITS, CH>(kw[i], ch0, code);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) x[e] = fmaf((float)code[e], s[e], z[e]);
+      key_kept<D, CH>(c, su, row + i, ch0, x);
+      store_row<T, CH>(Ko + t * D, x, wide);
+      value_codes<D, BITS, CH>(vw, row + i, code);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) x[e] = fmaf((float)code[e], vs[i], vz[i]);
+      value_kept<D, CH>(c, su, row + i, ch0, x);
+      store_row<T, CH>(Vo + t * D, x, wide);
     }
   } else {
     const T* kr = static_cast<const T*>(c.k_res) + unit * c.R * D + ch0;

@@ -18,117 +18,148 @@ namespace kivi {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 4;  // rows of a thread under way at a time
 
-// Block: tokens blockIdx.x * TB ..; the table of its cosines and sines is made
-// once and used by all heads.  D / CH lanes hold a row, 16 bytes each.
+// Block: tokens blockIdx.x * TB .., head rows blockIdx.y, + gridDim.y, .. of them in
+// rounds.  The table of the tokens' cosines and sines is made once and used by all
+// heads.  D / CH lanes hold a row, 16 bytes each; four rows' loads are issued
+// before any is worked on.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int TB) {
   constexpr int CH = 16 / (int)sizeof(T);
-  constexpr int LPR = D / CH;  // lanes of a row
-  extern __shared__ float2 cs[];  // [TB][rot / 2]
-  const long long tokens = (long long)a.B * a.N;
-  const long long tok0 = (long long)blockIdx.x * TB;
+  constexpr int LPR = D / CH;                // lanes of a row
+  constexpr int RPB = kRopeThreads / LPR;    // rows of a round
+  extern __shared__ float2 cs[];             // [TB][rot / 2]
+  const int tokens = a.B * a.N;
+  const int tok0 = blockIdx.x * TB;
   const int half = a.rot / 2;
+  const int H = a.Hq + 2 * a.Hkv;
+  const int lane = threadIdx.x % LPR, ch0 = lane * CH;
+  const int rows = min(TB, tokens - tok0) * H;
+  const T* in = static_cast<const T*>(a.qkv);
+  // this thread's rows: i, i + step, ..; as token tl and head h
+  const int step = RPB * gridDim.y;
+  const int i0 = blockIdx.y * RPB + threadIdx.x / LPR;
+  int tl = i0 / H, h = i0 % H;
+  auto next = [&](int& t, int& x) {
+    x += step;
+    while (x >= H) {
+      x -= H;
+      ++t;
+    }
+  };
+  uint4 raw[kRopeRows];
+  auto load = [&](int i, int t, int x) {
+    int ti = i;
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+      raw[r] = make_uint4(0, 0, 0, 0);
+      if (ti < rows)
+        raw[r] = *reinterpret_cast<const uint4*>(in + (long long)(tok0 + t) * a.stride + x * D + ch0);
+      ti += step;
+      next(t, x);
+    }
+  };
+  load(i0, tl, h);
   for (int i = threadIdx.x; i < TB * half; i += kRopeThreads) {
-    const int p = i % half;
-    const long long tok = tok0 + i / half;
+    const int p = i % half, tok = tok0 + i / half;
     if (tok >= tokens) break;
-    int ax = 0;
-    while (ax + 1 < a.axes && p >= a.section_end[ax]) ++ax;
+    // (ends behind the last section are rot / 2, beyond every pair)
+    const int ax = (p >= a.section_end[0]) + (p >= a.section_end[1]) + (p >= a.section_end[2]);
     constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
-    const double turns = (double)a.pos[ax * tokens + tok] * a.inv_freq[p] * kTurn;
+    const double turns = (double)a.pos[(long long)ax * tokens + tok] * a.inv_freq[p] * kTurn;
     float sn, cn;
     sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
     cs[i] = make_float2(cn, sn);
   }
-  __syncthreads();
-  const int H = a.Hq + 2 * a.Hkv;
-  const int lane = threadIdx.x % LPR, ch0 = lane * CH;
-  const T* in = static_cast<const T*>(a.qkv);
   float wq[CH], wk[CH];
 #pragma unroll
   for (int e = 0; e < CH; ++e) {
     wq[e] = a.qw ? to_f32(static_cast<const T*>(a.qw)[ch0 + e]) : 1.0f;
     wk[e] = a.kw ? to_f32(static_cast<const T*>(a.kw)[ch0 + e]) : 1.0f;
   }
+  const bool lo = ch0 < half, in_rot = ch0 < a.rot;
+  // pair (p, p + half): half is a multiple of CH, so the partner channels are those
+  // of one other lane
+  const int other = a.interleaved || !in_rot ? lane : (lo ? lane + half / CH : lane - half / CH);
+  const int t0 = a.interleaved ? ch0 / 2 : (lo ? ch0 : ch0 - half);  // in the table
+  const int tok_b = tok0 / a.N, tok_n = tok0 % a.N;
+  __syncthreads();
+
   // every thread of a warp runs the same number of rounds (shuffles inside)
-  const int rows = TB * H;
-  constexpr int RPB = kRopeThreads / LPR;
-  for (int i0 = 0; i0 < rows; i0 += RPB) {
-    const int i = i0 + threadIdx.x / LPR;
-    const int tl = i / H, h = i % H;
-    const long long tok = tok0 + tl;
-    const bool live = i < rows && tok < tokens;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4*>(in + tok * a.stride + (long long)h * D + ch0);
-    const long long b = tok / a.N, n = tok % a.N;
-    float x[CH];
+  for (int base = blockIdx.y * RPB; base < rows; base += kRopeRows * step) {
+    int ti = base + threadIdx.x / LPR;
 #pragma unroll
-    for (int e = 0; e < CH; ++e) x[e] = to_f32(reinterpret_cast<const T*>(&raw)[e]);
-    const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
-    if (a.qw || a.kw) {
-      float ss = 0.f;
+    for (int r = 0; r < kRopeRows; ++r) {
+      const bool live = ti < rows;
+      float x[CH];
 #pragma unroll
-      for (int e = 0; e < CH; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < CH; ++e) x[e] = to_f32(reinterpret_cast<const T*>(&raw[r])[e]);
+      const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
+      if (a.qw || a.kw) {
+        float ss = 0.f;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if ((isq && a.qw) || (isk && a.kw)) {
-        const float rs = rsqrtf(ss / (float)D + a.eps);
+        for (int e = 0; e < CH; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) x[e] = x[e] * rs * (isq ? wq[e] : wk[e]);
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if ((isq && a.qw) || (isk && a.kw)) {
+          const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+          for (int e = 0; e < CH; ++e) x[e] = x[e] * rs * (isq ? wq[e] : wk[e]);
+        }
       }
+      const float2* t = cs + (live ? tl : 0) * half + t0;
+      float y[CH];
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < CH; e += 2) {
+          const float2 f = in_rot ? t[e / 2] : make_float2(1.f, 0.f);
+          y[e] = x[e] * f.x - x[e + 1] * f.y;
+          y[e + 1] = x[e + 1] * f.x + x[e] * f.y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+          const float o = __shfl_sync(0xffffffffu, x[e], other, LPR);
+          const float2 f = in_rot ? t[e] : make_float2(1.f, 0.f);
+          y[e] = fmaf(lo ? -o : o, f.y, x[e] * f.x);
+        }
+      }
+      if (live) {
+        uint4 res = raw[r];  // values are laid out as they are
+        if (isq || isk) {
+          T o[CH];
+#pragma unroll
+          for (int e = 0; e < CH; ++e) o[e] = from_f32<T>(in_rot ? y[e] : x[e]);
+          res = *reinterpret_cast<const uint4*>(o);
+        }
+        int b = tok_b, n = tok_n + tl;
+        while (n >= a.N) {
+          n -= a.N;
+          ++b;
+        }
+        T* dst = isq ? static_cast<T*>(a.q) + (((long long)b * a.Hq + h) * a.N + n) * D
+                     : (isk ? static_cast<T*>(a.k) + (((long long)b * a.Hkv + h - a.Hq) * a.N + n) * D
+                            : static_cast<T*>(a.v) + (((long long)b * a.Hkv + h - a.Hq - a.Hkv) * a.N + n) * D);
+        *reinterpret_cast<uint4*>(dst + ch0) = res;
+      }
+      ti += step;
+      next(tl, h);
     }
-    const float2* t = cs + tl * half;
-    float y[CH];
-    if (a.interleaved) {
-#pragma unroll
-      for (int e = 0; e < CH; e += 2) {
-        const int p = (ch0 + e) / 2;
-        const float2 f = (live && ch0 < a.rot) ? t[p] : make_float2(1.f, 0.f);
-        y[e] = x[e] * f.x - x[e + 1] * f.y;
-        y[e + 1] = x[e + 1] * f.x + x[e] * f.y;
-      }
-      if (ch0 >= a.rot) {  // not turned (a zero times an infinity would spoil it)
-#pragma unroll
-        for (int e = 0; e < CH; ++e) y[e] = x[e];
-      }
-    } else {
-      // pair (p, p + half): half is a multiple of CH, so the partner channels
-      // are those of one other lane
-      const bool lo = ch0 < half, in_rot = ch0 < a.rot;
-      const int other = !in_rot ? lane : (lo ? lane + half / CH : lane - half / CH);
-#pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        const float o = __shfl_sync(0xffffffffu, x[e], other, LPR);
-        const float2 f = (live && in_rot) ? t[(lo ? ch0 : ch0 - half) + e] : make_float2(1.f, 0.f);
-        y[e] = lo ? x[e] * f.x - o * f.y : x[e] * f.x + o * f.y;
-        if (!in_rot) y[e] = x[e];
-      }
-    }
-    if (!live) continue;
-    T* dst;
-    if (isq)
-      dst = static_cast<T*>(a.q) + ((b * a.Hq + h) * a.N + n) * D;
-    else if (isk)
-      dst = static_cast<T*>(a.k) + ((b * a.Hkv + (h - a.Hq)) * a.N + n) * D;
-    else
-      dst = static_cast<T*>(a.v) + ((b * a.Hkv + (h - a.Hq - a.Hkv)) * a.N + n) * D;
-    if (isq || isk) {
-      T o[CH];
-#pragma unroll
-      for (int e = 0; e < CH; ++e) o[e] = from_f32<T>(y[e]);
-      raw = *reinterpret_cast<const uint4*>(o);
-    }
-    *reinterpret_cast<uint4*>(dst + ch0) = raw;
+    if (base + kRopeRows * step < rows) load(ti, tl, h);
   }
 }
 
 template <int D, typename T>
 cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
-  const long long tokens = (long long)a.B * a.N;
-  const int TB = 2;
-  const long long blocks = (tokens + TB - 1) / TB;
-  rope_kernel<D, T><<<(unsigned)blocks, kRopeThreads, TB * (a.rot / 2) * sizeof(float2), s>>>(a, TB);
+  const int tokens = a.B * a.N;
+  constexpr int RPB = kRopeThreads * 16 / (int)sizeof(T) / D;
+  // enough tokens: four a block; few: one, its heads spread over blocks that take one
+  // round each (each makes the token's table again)
+  const int TB = tokens >= 2048 ? 4 : 1;
+  const int H = a.Hq + 2 * a.Hkv, spread = (H + RPB - 1) / RPB;
+  const dim3 grid((unsigned)((tokens + TB - 1) / TB), TB == 4 ? 1 : (unsigned)min(spread, 65535));
+  rope_kernel<D, T><<<grid, kRopeThreads, TB * (a.rot / 2) * sizeof(float2), s>>>(a, TB);
   return cudaGetLastError();
 }
 

@@ -48,6 +48,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   __syncthreads();
   const long long W = tree_range(p, s_total);
   const long long c0 = s_first / W, c1 = (s_first + q.ut - 1) / W;
+  // launched while the split kernel runs, which every block waits for (a grid that
+  // ended before it would let the stream's next kernel overtake it)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // written by its only CTA
   const int rows = a.gq * a.N;
   const long long stride = tree_part(p, D);
@@ -81,16 +84,27 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   }
 }
 
+template <int D, typename T>
+cudaError_t merge_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hkv * p.n_rb), (unsigned)((p.rb + kMergeRows - 1) / kMergeRows));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, T>, a, p);
+}
 template <typename T>
 cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  const dim3 grid((unsigned)((long long)a.B * a.Hkv * p.n_rb), (unsigned)((p.rb + kMergeRows - 1) / kMergeRows));
   switch (a.D) {
-    case 32: tree_merge_kernel<32, T><<<grid, kMergeThreads, 0, s>>>(a, p); break;
-    case 64: tree_merge_kernel<64, T><<<grid, kMergeThreads, 0, s>>>(a, p); break;
-    case 128: tree_merge_kernel<128, T><<<grid, kMergeThreads, 0, s>>>(a, p); break;
-    default: return cudaErrorInvalidValue;
+    case 32: return merge_t<32, T>(a, p, s);
+    case 64: return merge_t<64, T>(a, p, s);
+    case 128: return merge_t<128, T>(a, p, s);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
   constexpr int OV = OC >= 4 ? 4 : OC;           // adjacent channels of a thread
   constexpr int ON = OC / OV;
   static_assert(kTT == kTile && kTT == kG, "a tile is a key group");
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) float sm[];
   __shared__ TreeAt s_at;
   const int tid = threadIdx.x;
@@ -108,17 +109,28 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
           poison = true;  // the same for the whole block
           break;
         }
+        using Lt = Layout<D, BITS>;
+        const long long row = stl * kTT + tk, Ts = store_tokens(a.c);
+        const uint32_t* ku = a.c.k_codes + su * Lt::k_codes_unit(Ts);
+        const uint32_t* vu = a.c.v_codes + su * Lt::v_codes_unit(Ts);
+        const long long mo = su * Lt::v_meta_unit(Ts) + row * Lt::NJ + ch / kGv;
         float s[4], z[4];
-        key_meta<D, BITS, float, 4>(a.c, su, stl * kTT, ch, s, z);
+        key_meta<D, BITS, float, 4>(a.c, su, row, ch, s, z);
 #pragma unroll
         for (int i = 0; i < TPT; ++i) {
-          float v[4];
-          key_values<D, BITS, float, 4>(a.c, su, stl * kTT + tk + i, ch, s, z, v);
+          uint32_t kw[Lt::WB], vw[Lt::WB][4];
+          int c[4];
+          key_words<D, BITS, 4>(ku, row + i, ch, kw);
+          key_codes<D, BITS, 4>(kw, ch, c);
           *reinterpret_cast<float4*>(sm + SM::K + (tk + i) * SM::LD + ch) =
-              make_float4(v[0], v[1], v[2], v[3]);
-          value_values<D, BITS, float, 4>(a.c, su, stl * kTT + tk + i, ch, v);
+              make_float4(fmaf((float)c[0], s[0], z[0]), fmaf((float)c[1], s[1], z[1]),
+                          fmaf((float)c[2], s[2], z[2]), fmaf((float)c[3], s[3], z[3]));
+          const float vs = a.c.v_scale_f()[mo + i * Lt::NJ], vz = a.c.v_zero_f()[mo + i * Lt::NJ];
+          value_words<D, BITS, 4>(vu, row + i, ch, vw);
+          value_codes<D, BITS, 4>(vw, row + i, c);
           *reinterpret_cast<float4*>(sm + SM::V + (tk + i) * D + ch) =
-              make_float4(v[0], v[1], v[2], v[3]);
+              make_float4(fmaf((float)c[0], vs, vz), fmaf((float)c[1], vs, vz),
+                          fmaf((float)c[2], vs, vz), fmaf((float)c[3], vs, vz));
         }
       } else {
         const long long first = (t - tq) * kTT;

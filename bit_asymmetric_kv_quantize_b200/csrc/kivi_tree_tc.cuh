@@ -630,6 +630,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
   const int nr = p.rb, nch = nr / 16;
 
   // ---- set-up
+  asm volatile("griddepcontrol.launch_dependents;");
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      tc_smem(&s_tmem)),
