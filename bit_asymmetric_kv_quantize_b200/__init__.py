@@ -11,7 +11,9 @@ Method: "KIVI: A Tuning-Free Asymmetric 2bit Quantization for KV Cache"
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -177,6 +179,15 @@ def buffer_sizes(B, Hkv, D, bits, capacity, R=128, G=32, Gv=32, dtype=torch.floa
     return dict(zip(BUFFER_NAMES, list(out)))
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """The context of a device; none where it is current already (the usual case, and some
+    microseconds cheaper)."""
+    return _SAME_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
 class KiviCache:
     """One layer's KIVI cache on a CUDA device.
 
@@ -222,6 +233,7 @@ class KiviCache:
         self._ws_dev: Optional[torch.Tensor] = None
         self._staging: Optional[torch.Tensor] = None
         self._ws_tree: Optional[torch.Tensor] = None
+        self._tree_need: dict = {}  # workspace bytes by (N, Hq)
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         self.shapes = {
@@ -478,8 +490,11 @@ class KiviCache:
         if out is None:
             out = torch.empty_like(q)
         po = self._arg(out, (self.B, Hq, N, self.D), "out")
-        with torch.cuda.device(self.device):
-            need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
+        need = self._tree_need.get((N, Hq))
+        if need is None:
+            with _on(self.device):
+                need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
+            self._tree_need[N, Hq] = need
         if self._ws_tree is None or self._ws_tree.numel() < need:
             self._ws_tree = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
         return (pq, pk, pv, mask.data_ptr(), N, Hq), po, out
@@ -490,7 +505,7 @@ class KiviCache:
         q, out [B][Hq][N][D]; k, v [B][Hkv][N][D]; mask int32 [B][N][ceil(N / 32)], bit j of
         node i's words set where it attends to node j (see tree_mask)."""
         args, po, out = self._tree_args(q, k, v, mask, out)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             _check(lib().kivi_tree_decode(ctypes.byref(self._c), *args, float(softmax_scale), po,
                                           self._ws_tree.data_ptr(), self._ws_tree.numel(),
                                           self._stream()), "kivi_tree_decode")
@@ -501,7 +516,7 @@ class KiviCache:
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """tree_decode of a ragged batch, every sequence over its own tokens."""
         args, po, out = self._tree_args(q, k, v, mask, out)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             _check(lib().kivi_ragged_tree_decode(ctypes.byref(self._c), self._state_arg(st), *args,
                                                  float(softmax_scale), po,
                                                  self._ws_tree.data_ptr(), self._ws_tree.numel(),
@@ -528,7 +543,7 @@ class KiviCache:
                     or not t.is_contiguous()):
                 raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {shape} on "
                                  f"{self.device}")
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             _check(lib().kivi_ragged_tree_commit(ctypes.byref(self._c), self._state_arg(st), pk, pv,
                                                  N, path.data_ptr(), count.data_ptr(), P,
                                                  self._stream()), "kivi_ragged_tree_commit")
@@ -543,7 +558,7 @@ class KiviCache:
                     V: Optional[torch.Tensor] = None):
         """Tokens t0 .. t0+T-1 as numbers: (K, V), each [B][Hkv][T][D] (kivi_read_tokens)."""
         pk, pv, K, V = self._read_out(T, K, V)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             _check(lib().kivi_read_tokens(ctypes.byref(self._c), t0, T, pk, pv, self._stream()),
                    "kivi_read_tokens")
         return K, V
@@ -553,7 +568,7 @@ class KiviCache:
         """read_tokens of a ragged batch; tokens that a sequence does not have are left as they
         were in K and V (zeros in those made here)."""
         pk, pv, K, V = self._read_out(T, K, V)
-        with torch.cuda.device(self.device):
+        with _on(self.device):
             _check(lib().kivi_ragged_read_tokens(ctypes.byref(self._c), self._state_arg(st), t0, T,
                                                  pk, pv, self._stream()),
                    "kivi_ragged_read_tokens")
@@ -601,6 +616,7 @@ class PagedKiviCache(KiviCache):
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
         self._ws_tree: Optional[torch.Tensor] = None
+        self._tree_need: dict = {}  # workspace bytes by (N, Hq)
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         P = num_pages
@@ -636,6 +652,12 @@ def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32).to(parents.device)
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_shape(B, N, Hq, Hkv, D, dtype, rot, axes, sections, interleaved, eps) -> KiviRope:
+    return KiviRope(B, N, Hq, Hkv, D, dtype, rot, axes, (ctypes.c_int * 4)(*sections), interleaved,
+                    eps)
+
+
 def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, Hq: int,
                  Hkv: int, q_weight: Optional[torch.Tensor] = None,
                  k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, sections=None,
@@ -659,33 +681,35 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Ten
     if positions.dim() == 2:
         positions = positions[None]
     axes = positions.shape[0] if positions.dim() == 3 else 0
-    if (positions.device != qkv.device or positions.dtype != torch.int64 or not 1 <= axes <= 4
+    device = qkv.device
+    if (positions.device != device or positions.dtype != torch.int64 or not 1 <= axes <= 4
             or tuple(positions.shape[1:]) != (B, N) or not positions.is_contiguous()):
         raise ValueError(f"positions: expected a contiguous int64 tensor of shape ({B}, {N}) or "
                          f"(axes, {B}, {N}) on {qkv.device}")
-    if (inv_freq.device != qkv.device or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
+    if (inv_freq.device != device or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1
             or not inv_freq.is_contiguous()):
-        raise ValueError(f"inv_freq: expected a contiguous float64 vector on {qkv.device}")
+        raise ValueError(f"inv_freq: expected a contiguous float64 vector on {device}")
     rot = 2 * inv_freq.shape[0]
     sections = [rot // 2] if sections is None else [int(x) for x in sections]
     if len(sections) != axes:
         raise ValueError(f"sections: expected one number for each of the {axes} axes")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.device != qkv.device or w.dtype != qkv.dtype
+        if w is not None and (w.device != device or w.dtype != qkv.dtype
                               or tuple(w.shape) != (D,) or not w.is_contiguous()):
             raise ValueError(f"{name}: expected a contiguous {qkv.dtype} vector of {D} on "
-                             f"{qkv.device}")
+                             f"{device}")
     shapes = ((B, Hq, N, D), (B, Hkv, N, D), (B, Hkv, N, D))
     if out is None:
-        out = tuple(torch.empty(s, dtype=qkv.dtype, device=qkv.device) for s in shapes)
-    for t, s in zip(out, shapes):
-        if (t.device != qkv.device or t.dtype != qkv.dtype or tuple(t.shape) != s
-                or not t.is_contiguous()):
-            raise ValueError(f"out: expected contiguous {qkv.dtype} tensors of shapes {shapes} on "
-                             f"{qkv.device}")
-    p = KiviRope(B, N, Hq, Hkv, D, _dtype_code(qkv.dtype), rot, axes,
-                 (ctypes.c_int * 4)(*sections), int(bool(interleaved)), float(eps))
-    with torch.cuda.device(qkv.device):
+        out = tuple(qkv.new_empty(s) for s in shapes)
+    else:
+        for t, s in zip(out, shapes, strict=True):
+            if (t.device != device or t.dtype != qkv.dtype or tuple(t.shape) != s
+                    or not t.is_contiguous()):
+                raise ValueError(f"out: expected contiguous {qkv.dtype} tensors of shapes {shapes} "
+                                 f"on {device}")
+    p = _rope_shape(B, N, Hq, Hkv, D, _dtype_code(qkv.dtype), rot, axes, tuple(sections),
+                    int(bool(interleaved)), float(eps))
+    with _on(qkv.device):
         _check(lib().kivi_qk_norm_rope(
             ctypes.byref(p), qkv.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(),
             q_weight.data_ptr() if q_weight is not None else None,

@@ -20,146 +20,187 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 4;  // rows of a thread under way at a time
 
-// Block: tokens blockIdx.x * TB .., head rows blockIdx.y, + gridDim.y, .. of them in
-// rounds.  The table of the tokens' cosines and sines is made once and used by all
-// heads.  D / CH lanes hold a row, 16 bytes each; four rows' loads are issued
-// before any is worked on.
-template <int D, typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int TB) {
-  constexpr int CH = 16 / (int)sizeof(T);
-  constexpr int LPR = D / CH;                // lanes of a row
-  constexpr int RPB = kRopeThreads / LPR;    // rows of a round
-  extern __shared__ float2 cs[];             // [TB][rot / 2]
-  const int tokens = a.B * a.N;
-  const int tok0 = blockIdx.x * TB;
-  const int half = a.rot / 2;
-  const int H = a.Hq + 2 * a.Hkv;
-  const int lane = threadIdx.x % LPR, ch0 = lane * CH;
-  const int rows = min(TB, tokens - tok0) * H;
-  const T* in = static_cast<const T*>(a.qkv);
-  // this thread's rows: i, i + step, ..; as token tl and head h
-  const int step = RPB * gridDim.y;
-  const int i0 = blockIdx.y * RPB + threadIdx.x / LPR;
-  int tl = i0 / H, h = i0 % H;
-  auto next = [&](int& t, int& x) {
-    x += step;
-    while (x >= H) {
-      x -= H;
-      ++t;
+// Four adjacent elements, loaded and stored as one piece.
+template <typename T>
+struct Four;
+template <>
+struct Four<__half> {
+  uint2 v;
+  __device__ __forceinline__ void widen(float* x) const {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
+  }
+  __device__ __forceinline__ void round(const float* x) {
+    const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+    v.x = *reinterpret_cast<const uint32_t*>(&a);
+    v.y = *reinterpret_cast<const uint32_t*>(&b);
+  }
+};
+template <>
+struct Four<float> {
+  float4 v;
+  __device__ __forceinline__ void widen(float* x) const {
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  }
+  __device__ __forceinline__ void round(const float* x) {
+    v = make_float4(x[0], x[1], x[2], x[3]);
+  }
+};
+
+// The rows of one kind (queries, keys or values): nh heads of each of the block's
+// tokens, D / 8 lanes a row.  A lane holds two pieces of four channels at ca and cb: both
+// halves of its four pairs, so that no value has to cross lanes for the turn.  Four
+// rows' loads are issued before any is worked on.  w: the norm's weight, or null.
+template <int D, typename T, bool INTER, bool TURN>
+__device__ __forceinline__ void rope_rows(const RopeArgs& a, const T* in, T* out,
+                                          const T* __restrict__ w, int nh, int tok0, int ntok,
+                                          int ca, int cb, bool turns, const float4* cs) {
+  constexpr int LPR = D / 8, RPB = kRopeThreads / LPR;
+  const int rows = ntok * nh, step = RPB * gridDim.y, half = a.rot / 2;
+  float wa[4], wb[4];
+  if (TURN && w != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      wa[e] = to_f32(w[ca + e]);
+      wb[e] = to_f32(w[cb + e]);
     }
-  };
-  uint4 raw[kRopeRows];
-  auto load = [&](int i, int t, int x) {
-    int ti = i;
+  }
+  // a row as token tl of the block and head h
+  int i = blockIdx.y * RPB + threadIdx.x / LPR;
+  int tl = i / nh, h = i % nh;
+  const int dt = step / nh, dh = step % nh;
+  // every thread of a warp runs the same number of rounds (shuffles inside)
+  for (int base = blockIdx.y * RPB; base < rows; base += kRopeRows * step) {
+    Four<T> xa[kRopeRows], xb[kRopeRows];
+    int rt[kRopeRows], rh[kRopeRows];
 #pragma unroll
     for (int r = 0; r < kRopeRows; ++r) {
-      raw[r] = make_uint4(0, 0, 0, 0);
-      if (ti < rows)
-        raw[r] = *reinterpret_cast<const uint4*>(in + (long long)(tok0 + t) * a.stride + x * D + ch0);
-      ti += step;
-      next(t, x);
+      rt[r] = i < rows ? tl : -1;
+      rh[r] = h;
+      if (i < rows) {
+        const T* src = in + (long long)(tok0 + tl) * a.stride + h * D;
+        xa[r] = *reinterpret_cast<const Four<T>*>(src + ca);
+        xb[r] = *reinterpret_cast<const Four<T>*>(src + cb);
+      } else {
+        xa[r].v = xb[r].v = {};
+      }
+      i += step;
+      h += dh;
+      tl += dt + (h >= nh);
+      if (h >= nh) h -= nh;
     }
-  };
-  load(i0, tl, h);
-  for (int i = threadIdx.x; i < TB * half; i += kRopeThreads) {
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+      const int t = max(rt[r], 0);
+      if (TURN) {  // values are laid out as they are
+        float x[4], y[4];
+        xa[r].widen(x);
+        xb[r].widen(y);
+        if (w != nullptr) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = fmaf(y[e], y[e], fmaf(x[e], x[e], ss));
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = x[e] * rs * wa[e];
+            y[e] = y[e] * rs * wb[e];
+          }
+        }
+        if (turns) {
+          const float4* f = cs + t * (half / 2);
+          const float4 f0 = f[0], f1 = f[1];
+          const float c[4] = {f0.x, f0.z, f1.x, f1.z}, sn[4] = {f0.y, f0.w, f1.y, f1.w};
+          if (INTER) {  // pairs (0, 1), (2, 3) of each piece
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float* p = e < 2 ? x + 2 * e : y + 2 * (e - 2);
+              const float u = p[0], v = p[1];
+              p[0] = fmaf(-v, sn[e], u * c[e]);
+              p[1] = fmaf(u, sn[e], v * c[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float u = x[e], v = y[e];
+              x[e] = fmaf(-v, sn[e], u * c[e]);
+              y[e] = fmaf(u, sn[e], v * c[e]);
+            }
+          }
+        }
+        xa[r].round(x);
+        xb[r].round(y);
+      }
+      if (rt[r] >= 0) {
+        const int tok = tok0 + t, b = tok / a.N, n = tok - b * a.N;
+        T* dst = out + (((long long)b * nh + rh[r]) * a.N + n) * D;
+        *reinterpret_cast<Four<T>*>(dst + ca) = xa[r];
+        *reinterpret_cast<Four<T>*>(dst + cb) = xb[r];
+      }
+    }
+  }
+}
+
+// Block: tokens blockIdx.x * TB ..; gridDim.y blocks share their rows.  The table of
+// the tokens' cosines and sines is made once and used by all heads.  What bounds it:
+// DRAM, after the instructions of the turn (one warp instruction for every 5 bytes
+// at first, for every 12 with pairs in one lane).
+template <int D, typename T, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int TB) {
+  extern __shared__ float4 cs[];  // [TB][rot / 2] (cosine, sine)
+  const int tokens = a.B * a.N, tok0 = blockIdx.x * TB, ntok = min(TB, tokens - tok0);
+  const int half = a.rot / 2;
+  for (int i = threadIdx.x; i < ntok * half; i += kRopeThreads) {
     const int p = i % half, tok = tok0 + i / half;
-    if (tok >= tokens) break;
     // (ends behind the last section are rot / 2, beyond every pair)
     const int ax = (p >= a.section_end[0]) + (p >= a.section_end[1]) + (p >= a.section_end[2]);
     constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
     const double turns = (double)a.pos[(long long)ax * tokens + tok] * a.inv_freq[p] * kTurn;
     float sn, cn;
     sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
-    cs[i] = make_float2(cn, sn);
+    reinterpret_cast<float2*>(cs)[i] = make_float2(cn, sn);
   }
-  float wq[CH], wk[CH];
-#pragma unroll
-  for (int e = 0; e < CH; ++e) {
-    wq[e] = a.qw ? to_f32(static_cast<const T*>(a.qw)[ch0 + e]) : 1.0f;
-    wk[e] = a.kw ? to_f32(static_cast<const T*>(a.kw)[ch0 + e]) : 1.0f;
-  }
-  const bool lo = ch0 < half, in_rot = ch0 < a.rot;
-  // pair (p, p + half): half is a multiple of CH, so the partner channels are those
-  // of one other lane
-  const int other = a.interleaved || !in_rot ? lane : (lo ? lane + half / CH : lane - half / CH);
-  const int t0 = a.interleaved ? ch0 / 2 : (lo ? ch0 : ch0 - half);  // in the table
-  const int tok_b = tok0 / a.N, tok_n = tok0 % a.N;
   __syncthreads();
-
-  // every thread of a warp runs the same number of rounds (shuffles inside)
-  for (int base = blockIdx.y * RPB; base < rows; base += kRopeRows * step) {
-    int ti = base + threadIdx.x / LPR;
-#pragma unroll
-    for (int r = 0; r < kRopeRows; ++r) {
-      const bool live = ti < rows;
-      float x[CH];
-#pragma unroll
-      for (int e = 0; e < CH; ++e) x[e] = to_f32(reinterpret_cast<const T*>(&raw[r])[e]);
-      const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
-      if (a.qw || a.kw) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < CH; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if ((isq && a.qw) || (isk && a.kw)) {
-          const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-          for (int e = 0; e < CH; ++e) x[e] = x[e] * rs * (isq ? wq[e] : wk[e]);
-        }
-      }
-      const float2* t = cs + (live ? tl : 0) * half + t0;
-      float y[CH];
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < CH; e += 2) {
-          const float2 f = in_rot ? t[e / 2] : make_float2(1.f, 0.f);
-          y[e] = x[e] * f.x - x[e + 1] * f.y;
-          y[e + 1] = x[e + 1] * f.x + x[e] * f.y;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < CH; ++e) {
-          const float o = __shfl_sync(0xffffffffu, x[e], other, LPR);
-          const float2 f = in_rot ? t[e] : make_float2(1.f, 0.f);
-          y[e] = fmaf(lo ? -o : o, f.y, x[e] * f.x);
-        }
-      }
-      if (live) {
-        uint4 res = raw[r];  // values are laid out as they are
-        if (isq || isk) {
-          T o[CH];
-#pragma unroll
-          for (int e = 0; e < CH; ++e) o[e] = from_f32<T>(in_rot ? y[e] : x[e]);
-          res = *reinterpret_cast<const uint4*>(o);
-        }
-        int b = tok_b, n = tok_n + tl;
-        while (n >= a.N) {
-          n -= a.N;
-          ++b;
-        }
-        T* dst = isq ? static_cast<T*>(a.q) + (((long long)b * a.Hq + h) * a.N + n) * D
-                     : (isk ? static_cast<T*>(a.k) + (((long long)b * a.Hkv + h - a.Hq) * a.N + n) * D
-                            : static_cast<T*>(a.v) + (((long long)b * a.Hkv + h - a.Hq - a.Hkv) * a.N + n) * D);
-        *reinterpret_cast<uint4*>(dst + ch0) = res;
-      }
-      ti += step;
-      next(tl, h);
-    }
-    if (base + kRopeRows * step < rows) load(ti, tl, h);
-  }
+  // rot is a multiple of 16: a lane's channels turn all or not at all
+  const int lane = threadIdx.x % (D / 8);
+  const bool turns = lane < a.rot / 8;
+  const bool split = turns && !INTER;
+  const int ca = split ? 4 * lane : 8 * lane, cb = split ? half + 4 * lane : 8 * lane + 4;
+  const float4* f = cs + 2 * lane;  // pairs 4 lane .. 4 lane + 3
+  const T* in = static_cast<const T*>(a.qkv);
+  rope_rows<D, T, INTER, true>(a, in, static_cast<T*>(a.q), static_cast<const T*>(a.qw), a.Hq, tok0,
+                               ntok, ca, cb, turns, f);
+  rope_rows<D, T, INTER, true>(a, in + a.Hq * D, static_cast<T*>(a.k), static_cast<const T*>(a.kw),
+                               a.Hkv, tok0, ntok, ca, cb, turns, f);
+  rope_rows<D, T, INTER, false>(a, in + (a.Hq + a.Hkv) * D, static_cast<T*>(a.v), (const T*)nullptr,
+                                a.Hkv, tok0, ntok, 8 * lane, 8 * lane + 4, false, f);
 }
 
 template <int D, typename T>
 cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
   const int tokens = a.B * a.N;
-  constexpr int RPB = kRopeThreads * 16 / (int)sizeof(T) / D;
-  // enough tokens: four a block; few: one, its heads spread over blocks that take one
-  // round each (each makes the token's table again)
-  const int TB = tokens >= 2048 ? 4 : 1;
-  const int H = a.Hq + 2 * a.Hkv, spread = (H + RPB - 1) / RPB;
-  const dim3 grid((unsigned)((tokens + TB - 1) / TB), TB == 4 ? 1 : (unsigned)min(spread, 65535));
-  rope_kernel<D, T><<<grid, kRopeThreads, TB * (a.rot / 2) * sizeof(float2), s>>>(a, TB);
+  constexpr int RPB = kRopeThreads * 8 / D;
+  // eight tokens a block where that still gives every SM a block (the rows of a
+  // kind then fill the block's rounds: 517 x 6 tokens of 20 heads took 22 us with two
+  // tokens a block); fewer for few tokens; one, its heads spread over blocks that take
+  // one round each (each makes the token's table again), for a decode step's
+  const int TB = tokens >= 1184 ? 8 : tokens >= 592 ? 4 : tokens >= 296 ? 2 : 1;
+  const int spread = (a.Hq + RPB - 1) / RPB;
+  const dim3 grid((unsigned)((tokens + TB - 1) / TB), TB > 1 ? 1 : (unsigned)min(spread, 65535));
+  const size_t bytes = TB * (a.rot / 2) * sizeof(float2);
+  if (a.interleaved)
+    rope_kernel<D, T, true><<<grid, kRopeThreads, bytes, s>>>(a, TB);
+  else
+    rope_kernel<D, T, false><<<grid, kRopeThreads, bytes, s>>>(a, TB);
   return cudaGetLastError();
 }
 

@@ -119,8 +119,8 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.rb = rows <= 16 ? 16 : 64;
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 32;
-    p.ctas = sms * (p.rb == 16 ? 4 : 2);
-    p.min_w = 4;
+    p.ctas = sms * (p.rb == 16 ? 4 : 3);
+    p.min_w = 2;
   } else {
     p.n_rb = (rows + 63) / 64;
     p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;
