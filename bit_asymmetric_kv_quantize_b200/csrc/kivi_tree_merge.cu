@@ -6,11 +6,13 @@ namespace kivi {
 namespace {
 
 constexpr int kMergeRows = 8;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 32 * kMergeRows;
 
-// Block (group, 8 rows of it): for each row the segments' partials
-// (m_s, l_s, acc_s), M = max m_s: out = sum 2^(m_s - M) acc_s / sum 2^(m_s - M) l_s;
-// a row that attended to nothing (all l_s = 0) is 0.
+// Block (group, 8 rows of it), a warp for each row: of the segments' partials (m_s,
+// l_s, acc_s), M = max m_s and weights 2^(m_s - M) first, then
+// out = sum 2^(m_s - M) acc_s / sum 2^(m_s - M) l_s with all loads independent of each
+// other (a long cache of few heads has a partial of every CTA).  A row that
+// attended to nothing (all l_s = 0) is 0.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, TreePlan p) {
   const long long gpb = (long long)a.Hkv * p.n_rb;
@@ -52,36 +54,59 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   // ended before it would let the stream's next kernel overtake it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // written by its only CTA
-  const int rows = a.gq * a.N;
+  const int rows = a.gq * a.N, n = (int)(c1 - c0 + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kMergeRows + warp;
+  if (row >= p.rb || rb * p.rb + row >= rows) return;
   const long long stride = tree_part(p, D);
-  T* out = static_cast<T*>(a.out) + ((b * a.Hkv + h) * (long long)rows + (long long)rb * p.rb) * D;
-  constexpr int C4 = D / 4;
-  for (int i = threadIdx.x; i < kMergeRows * C4; i += kMergeThreads) {
-    const int row = blockIdx.y * kMergeRows + i / C4, d = i % C4 * 4;
-    if (row >= p.rb || rb * p.rb + row >= rows) continue;
-    float M = -__builtin_huge_valf(), den = 0.f;
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long c = c0; c <= c1; ++c) {
-      const float* P = a.part + (2 * c + (c == c0)) * stride;
-      const float m = __ldcg(P + 2 * row), l = __ldcg(P + 2 * row + 1);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(P + 2 * p.rb + (long long)row * D + d));
-      if (l == 0.f) continue;
-      const float Mn = fmaxf(M, m);
-      const float e0 = M == Mn ? 1.f : exp2f(M - Mn), e1 = m == Mn ? 1.f : exp2f(m - Mn);
-      den = den * e0 + l * e1;
-      num.x = num.x * e0 + v.x * e1;
-      num.y = num.y * e0 + v.y * e1;
-      num.z = num.z * e0 + v.z * e1;
-      num.w = num.w * e0 + v.w * e1;
-      M = Mn;
-    }
-    const float inv = 1.f / den;
-    T* o = out + (long long)row * D + d;
-    o[0] = from_f32<T>(den == 0.f ? 0.f : num.x * inv);
-    o[1] = from_f32<T>(den == 0.f ? 0.f : num.y * inv);
-    o[2] = from_f32<T>(den == 0.f ? 0.f : num.z * inv);
-    o[3] = from_f32<T>(den == 0.f ? 0.f : num.w * inv);
+  // partial s: slot 1 of the first CTA, slot 0 of the others
+  const float* P = a.part + 2 * c0 * stride;
+  auto at = [&](int s) { return P + (s == 0 ? stride : 2LL * s * stride); };
+  extern __shared__ float w_s[];  // [8 rows][partials]
+  float* w = w_s + warp * n;
+  float M = -__builtin_huge_valf();
+  for (int s = lane; s < n; s += 32) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(s)) + row);
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
   }
+  M = warp_max(M);
+  float den = 0.f;
+  for (int s = lane; s < n; s += 32) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(s)) + row);
+    const float e = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+    w[s] = e;
+    den = fmaf(e, ml.y, den);
+  }
+  den = warp_sum(den);
+  __syncwarp();
+  constexpr int LPR = D / 4, SPL = 32 / LPR;  // lanes of a row, and how many share the partials
+  const int d = lane % LPR * 4;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = lane / LPR; s < n; s += SPL) {
+    const float e = w[s];
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(at(s) + 2 * p.rb + (long long)row * D + d));
+    if (e != 0.f) {
+      num.x = fmaf(e, v.x, num.x);
+      num.y = fmaf(e, v.y, num.y);
+      num.z = fmaf(e, v.z, num.z);
+      num.w = fmaf(e, v.w, num.w);
+    }
+  }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+    num.x += __shfl_xor_sync(0xffffffffu, num.x, o);
+    num.y += __shfl_xor_sync(0xffffffffu, num.y, o);
+    num.z += __shfl_xor_sync(0xffffffffu, num.z, o);
+    num.w += __shfl_xor_sync(0xffffffffu, num.w, o);
+  }
+  if (lane >= LPR) return;
+  T* o = static_cast<T*>(a.out) + ((b * a.Hkv + h) * (long long)rows + (long long)rb * p.rb + row) * D + d;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  o[0] = from_f32<T>(num.x * inv);
+  o[1] = from_f32<T>(num.y * inv);
+  o[2] = from_f32<T>(num.z * inv);
+  o[3] = from_f32<T>(num.w * inv);
 }
 
 template <int D, typename T>
@@ -92,6 +117,7 @@ cudaError_t merge_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hkv * p.n_rb), (unsigned)((p.rb + kMergeRows - 1) / kMergeRows));
   cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = (size_t)kMergeRows * p.ctas * sizeof(float);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -120,7 +146,7 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 32;
     p.ctas = sms * (p.rb == 16 ? 4 : 3);
-    p.min_w = 2;
+    p.min_w = 1;
   } else {
     p.n_rb = (rows + 63) / 64;
     p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;

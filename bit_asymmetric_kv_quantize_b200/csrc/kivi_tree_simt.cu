@@ -17,6 +17,19 @@ namespace kivi {
 namespace {
 
 constexpr int kThreads = 128;
+
+// Two binary32 lanes in one instruction (the packed .f32x2 arithmetic of sm_100),
+// each rounded like its scalar counterpart.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 constexpr int kTT = 32;  // = one key group
 
 template <int D, int RB>
@@ -155,11 +168,12 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
       }
       __syncthreads();
       // ---- scores
-      float sc[SR][SC];
+      // (each as two sums, over the even and the odd channels)
+      float2 s2[SR][SC];
 #pragma unroll
       for (int i = 0; i < SR; ++i)
 #pragma unroll
-        for (int j = 0; j < SC; ++j) sc[i][j] = 0.f;
+        for (int j = 0; j < SC; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         float4 qv[SR], kv[SC];
@@ -173,12 +187,15 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
         for (int i = 0; i < SR; ++i)
 #pragma unroll
           for (int j = 0; j < SC; ++j) {
-            sc[i][j] = fmaf(qv[i].x, kv[j].x, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].y, kv[j].y, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].z, kv[j].z, sc[i][j]);
-            sc[i][j] = fmaf(qv[i].w, kv[j].w, sc[i][j]);
+            s2[i][j] = fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), s2[i][j]);
+            s2[i][j] = fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), s2[i][j]);
           }
       }
+      float sc[SR][SC];
+#pragma unroll
+      for (int i = 0; i < SR; ++i)
+#pragma unroll
+        for (int j = 0; j < SC; ++j) sc[i][j] = s2[i][j].x + s2[i][j].y;
       // ---- masks: drafted tokens that a node does not see, and the end
       if (raw) {
 #pragma unroll
@@ -243,14 +260,23 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
             for (int e = 0; e < OV; ++e)
               vv[g * OV + e] = sm[SM::V + tk2 * D + g * (D / ON) + oc0 + e];
 #pragma unroll
-          for (int i = 0; i < OR; ++i)
+          for (int i = 0; i < OR; ++i) {
+            // a drafted token that the node does not see has weight 0 whatever its
+            // values are: 0 * inf must not reach the sum
+            if (decltype(guard)::value && pv[i] == 0.f) continue;
+            if constexpr (OC % 2 == 0) {
 #pragma unroll
-            for (int j = 0; j < OC; ++j) {
-              // a drafted token that the node does not see has weight 0 whatever
-              // its values are: 0 * inf must not reach the sum
-              if (decltype(guard)::value && pv[i] == 0.f) continue;
-              acc[i][j] = fmaf(pv[i], vv[j], acc[i][j]);
+              for (int j = 0; j < OC; j += 2) {
+                const float2 r = fma2(make_float2(pv[i], pv[i]), make_float2(vv[j], vv[j + 1]),
+                                      make_float2(acc[i][j], acc[i][j + 1]));
+                acc[i][j] = r.x;
+                acc[i][j + 1] = r.y;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < OC; ++j) acc[i][j] = fmaf(pv[i], vv[j], acc[i][j]);
             }
+          }
         }
       };
       if (raw)
