@@ -188,6 +188,11 @@ def _on(device: torch.device):
     return _SAME_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+def _raw_stream(device: torch.device) -> int:
+    """torch's current stream of a device, without an object made for it."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 class KiviCache:
     """One layer's KIVI cache on a CUDA device.
 
@@ -508,7 +513,7 @@ class KiviCache:
         with _on(self.device):
             _check(lib().kivi_tree_decode(ctypes.byref(self._c), *args, float(softmax_scale), po,
                                           self._ws_tree.data_ptr(), self._ws_tree.numel(),
-                                          self._stream()), "kivi_tree_decode")
+                                          _raw_stream(self.device)), "kivi_tree_decode")
         return out
 
     def ragged_tree_decode(self, st: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -520,7 +525,7 @@ class KiviCache:
             _check(lib().kivi_ragged_tree_decode(ctypes.byref(self._c), self._state_arg(st), *args,
                                                  float(softmax_scale), po,
                                                  self._ws_tree.data_ptr(), self._ws_tree.numel(),
-                                                 self._stream()), "kivi_ragged_tree_decode")
+                                                 _raw_stream(self.device)), "kivi_ragged_tree_decode")
         return out
 
     def _state_arg(self, st: torch.Tensor) -> int:
@@ -546,7 +551,7 @@ class KiviCache:
         with _on(self.device):
             _check(lib().kivi_ragged_tree_commit(ctypes.byref(self._c), self._state_arg(st), pk, pv,
                                                  N, path.data_ptr(), count.data_ptr(), P,
-                                                 self._stream()), "kivi_ragged_tree_commit")
+                                                 _raw_stream(self.device)), "kivi_ragged_tree_commit")
 
     def _read_out(self, T: int, K, V):
         shape = (self.B, self.Hkv, max(int(T), 0), self.D)
@@ -559,7 +564,7 @@ class KiviCache:
         """Tokens t0 .. t0+T-1 as numbers: (K, V), each [B][Hkv][T][D] (kivi_read_tokens)."""
         pk, pv, K, V = self._read_out(T, K, V)
         with _on(self.device):
-            _check(lib().kivi_read_tokens(ctypes.byref(self._c), t0, T, pk, pv, self._stream()),
+            _check(lib().kivi_read_tokens(ctypes.byref(self._c), t0, T, pk, pv, _raw_stream(self.device)),
                    "kivi_read_tokens")
         return K, V
 
@@ -570,7 +575,7 @@ class KiviCache:
         pk, pv, K, V = self._read_out(T, K, V)
         with _on(self.device):
             _check(lib().kivi_ragged_read_tokens(ctypes.byref(self._c), self._state_arg(st), t0, T,
-                                                 pk, pv, self._stream()),
+                                                 pk, pv, _raw_stream(self.device)),
                    "kivi_ragged_read_tokens")
         return K, V
 
@@ -709,12 +714,12 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Ten
                                  f"on {device}")
     p = _rope_shape(B, N, Hq, Hkv, D, _dtype_code(qkv.dtype), rot, axes, tuple(sections),
                     int(bool(interleaved)), float(eps))
-    with _on(qkv.device):
+    with _on(device):
         _check(lib().kivi_qk_norm_rope(
             ctypes.byref(p), qkv.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(),
             q_weight.data_ptr() if q_weight is not None else None,
             k_weight.data_ptr() if k_weight is not None else None,
-            *(t.data_ptr() for t in out), torch.cuda.current_stream(qkv.device).cuda_stream),
+            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(device)),
             "kivi_qk_norm_rope")
     return tuple(out)
 

@@ -15,6 +15,8 @@
 // and replayed in any order on one workspace.
 #pragma once
 
+#include <atomic>
+
 #include "kivi_draft.cuh"
 
 namespace kivi {
@@ -101,6 +103,21 @@ __device__ __forceinline__ TreeAt tree_find(const TreeArgs& a, const TreePlan& p
 __device__ __forceinline__ long long tree_range(const TreePlan& p, long long total) {
   const long long w = (total + p.ctas - 1) / p.ctas;
   return w < p.min_w ? p.min_w : w;
+}
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device; asked for
+// once per device (`done`, one flag for each).
+constexpr int kTreeDevices = 128;
+template <typename K>
+cudaError_t tree_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kTreeDevices;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 // The kernels: binary32 caches on CUDA cores, fp16 ones on the tensor cores

@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
 template <int D, int BITS, int RB>
 cudaError_t tree_r(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
   constexpr int bytes = SimtSmem<D, RB>::FLOATS * 4;
-  const cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<D, BITS, RB>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<bool> done[kTreeDevices];
+  const cudaError_t e = tree_smem(tree_simt_kernel<D, BITS, RB>, bytes, done);
   if (e != cudaSuccess) return e;
   tree_simt_kernel<D, BITS, RB><<<p.ctas, kThreads, bytes, s>>>(a, p);
   return cudaGetLastError();

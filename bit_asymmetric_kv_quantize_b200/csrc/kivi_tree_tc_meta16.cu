@@ -8,9 +8,9 @@ namespace {
 template <int D, int BITS>
 cudaError_t tc_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
   const int bytes = a.N * ((a.N + 31) / 32) * 4 + TcGeo<D, BITS, (int)sizeof(__half)>::BYTES;
-  const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D, BITS, __half>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             TcGeo<D, BITS, (int)sizeof(__half)>::MOST);
+  static std::atomic<bool> done[kTreeDevices];
+  const cudaError_t e =
+      tree_smem(tree_tc_kernel<D, BITS, __half>, TcGeo<D, BITS, (int)sizeof(__half)>::MOST, done);
   if (e != cudaSuccess) return e;
   tree_tc_kernel<D, BITS, __half><<<p.ctas, kTcThreads, bytes, s>>>(a, p);
   return cudaGetLastError();
