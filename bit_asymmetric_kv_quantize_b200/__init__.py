@@ -238,6 +238,7 @@ class KiviCache:
         self._ws_dev: Optional[torch.Tensor] = None
         self._staging: Optional[torch.Tensor] = None
         self._ws_tree: Optional[torch.Tensor] = None
+        self._ws_tree_kept: list = []  # outgrown ones, which captured graphs may still use
         self._tree_need: dict = {}  # workspace bytes by (N, Hq)
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
@@ -501,6 +502,8 @@ class KiviCache:
                 need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
             self._tree_need[N, Hq] = need
         if self._ws_tree is None or self._ws_tree.numel() < need:
+            if self._ws_tree is not None:
+                self._ws_tree_kept.append(self._ws_tree)
             self._ws_tree = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
         return (pq, pk, pv, mask.data_ptr(), N, Hq), po, out
 
@@ -508,7 +511,8 @@ class KiviCache:
                     softmax_scale: float, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Attention of N drafted tokens over the cache and each other (kivi_tree_decode):
         q, out [B][Hq][N][D]; k, v [B][Hkv][N][D]; mask int32 [B][N][ceil(N / 32)], bit j of
-        node i's words set where it attends to node j (see tree_mask)."""
+        node i's words set where it attends to node j (see tree_mask).  The cache's tree calls
+        share one workspace: on several streams at a time they take one cache object each."""
         args, po, out = self._tree_args(q, k, v, mask, out)
         with _on(self.device):
             _check(lib().kivi_tree_decode(ctypes.byref(self._c), *args, float(softmax_scale), po,
@@ -621,6 +625,7 @@ class PagedKiviCache(KiviCache):
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
         self._ws_tree: Optional[torch.Tensor] = None
+        self._ws_tree_kept: list = []  # outgrown ones, which captured graphs may still use
         self._tree_need: dict = {}  # workspace bytes by (N, Hq)
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity

@@ -30,9 +30,11 @@
 // rounding.  Scores, maxima, sums and accumulators are binary32.
 //
 // Running maximum: a row's reference m is raised only when a score of a tile
-// exceeds it by more than 14 (in units of log2): weights up to 2^14 lose nothing
-// in binary16 or in the binary32 sums.  The weights of a tile are formed with the
-// references as they are while the excess is watched; one vote tells whether
+// exceeds it by more than 15 (in units of log2), and then to 8 below the tile's
+// maximum: weights up to 2^15 lose nothing in binary16 or in the binary32 sums, and
+// one 2^-25 of the largest, which binary16 would take for 0 beside a 1, still
+// counts (a long cache has many of them).  The weights of a tile are formed with
+// the references as they are while the excess is watched; one vote tells whether
 // that held, and the rare tile where it did not raises the references, rescales
 // O^T in tensor memory and forms its weights again.
 //
@@ -66,7 +68,8 @@ constexpr int kTcTile = 128;        // tokens
 constexpr int kTcWorkers = 256;
 constexpr int kTcWarps = 10;  // workers, matrix instructions, copies
 constexpr int kTcThreads = kTcWarps * 32;
-constexpr float kTcSlack = 14.0f;   // log2 units a score may exceed m by
+constexpr float kTcSlack = 15.0f;   // log2 units a score may exceed m by
+constexpr float kTcBelow = 8.0f;    // and those by which a rise leaves m below the maximum
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
 
 // ---- layouts ---------------------------------------------------------------
@@ -1053,7 +1056,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
             if (tid < nr) {
               const float old = m_s[tid];
               const float mn = fmaxf(fmaxf(fmaxf(wmax_s[tid], wmax_s[64 + tid]),
-                                           fmaxf(wmax_s[128 + tid], wmax_s[192 + tid])),
+                                           fmaxf(wmax_s[128 + tid], wmax_s[192 + tid])) - kTcBelow,
                                      old);
               f_s[tid] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
               m_s[tid] = mn;

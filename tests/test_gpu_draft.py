@@ -188,6 +188,26 @@ def test_tree_large_scores():
         check_tree(c, st, 2, 6, scale=0.0)
 
 
+def test_tree_many_small_weights_beside_a_large_one():
+    """One token far above thousands that follow it, each 2^-25 of its weight: together they count.
+    Their weights stand in binary16 at 2^-17 or above (steps of 2^-24: each off by at most 2^-8
+    of itself), the output is rounded to binary16 (2^-11), the scores are as in tree_reference
+    (3 * 2^-17 * 17.3 of a factor): within 1 % in all."""
+    for dtype in (torch.float16, torch.float32):
+        B, Hkv, D, T = 8, 8, 32, 4096
+        c = kivi.KiviCache(B, Hkv, D, 2, T + 32, R=32, dtype=dtype)
+        K = torch.zeros(B, Hkv, T, D, device="cuda", dtype=dtype)
+        K[:, :, 0] = 25 * math.log(2) / D
+        V = torch.full_like(K, 64.0)
+        V[:, :, 0] = 0
+        c.prefill(K, V)
+        q = torch.ones(B, Hkv, 3, D, device="cuda", dtype=dtype)
+        none = torch.zeros(B, 3, 1, dtype=torch.int32, device="cuda")
+        out = c.tree_decode(q, q, q, none, 1.0)
+        ref, _ = tree_reference(c, None, q, q, q, none, 1.0)
+        assert ((out.cpu().double() - ref).abs() <= 0.01 * ref).all()
+
+
 def test_tree_refused_sequences_give_nan():
     lens = [40, 300, 200]
     c, st = make_cache(8, 3, 2, 64, 2, lens, store="paged")
@@ -250,6 +270,26 @@ def test_tree_is_the_same_each_time_and_in_graphs(dtype):
     st.copy_(st2)
     graphs[0].replay()
     assert torch.equal(o1, w1)
+
+
+def test_tree_workspace_of_a_captured_graph_stays():
+    """A later call with a larger tree takes a larger workspace; a graph captured before it still
+    writes its partials into its own."""
+    c, st = make_cache(12, 1, 1, 64, 2, 4000)
+    q, k, v = draft(5, c, 1, 9)
+    m = random_tree(1, 1, 9)
+    want = tree(c, st, q, k, v, m, 0.1)
+    out = torch.zeros_like(q)
+    size = c._ws_tree.numel()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tree(c, st, q, k, v, m, 0.1, out=out)
+    check_tree(c, st, 1, 60)
+    others = [torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all(bool((o == 0xA5).all()) for o in others)
 
 
 def test_tree_on_another_stream():
