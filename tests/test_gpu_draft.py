@@ -190,9 +190,10 @@ def test_tree_large_scores():
 
 def test_tree_many_small_weights_beside_a_large_one():
     """One token far above thousands that follow it, each 2^-25 of its weight: together they count.
-    Their weights stand in binary16 at 2^-17 or above (steps of 2^-24: each off by at most 2^-8
-    of itself), the output is rounded to binary16 (2^-11), the scores are as in tree_reference
-    (3 * 2^-17 * 17.3 of a factor): within 1 % in all."""
+    The score between them, 25 ln 2 = 17.33, is off by 17.33 * 2^-11 = 0.0085 (its key is rounded to
+    binary16), so a weight that stands in binary16 at 2^-21 or above lies within 0.85 % of a whole
+    number of its steps of 2^-24 and is rounded to that; the output is rounded to binary16
+    (2^-11), the scores are as in tree_reference (3 * 2^-17 * 17.33): within 1 % in all."""
     for dtype in (torch.float16, torch.float32):
         B, Hkv, D, T = 8, 8, 32, 4096
         c = kivi.KiviCache(B, Hkv, D, 2, T + 32, R=32, dtype=dtype)
