@@ -27,6 +27,7 @@ struct TreePlan {
   int n_rb;    // row blocks of a KV head
   int ctas;    // CTAs of the split kernel
   int min_w;   // shortest range
+  int parts;   // tensor cores: groups of four warps in a block
 };
 
 __host__ __device__ inline long long tree_slots(const TreePlan& p) { return 2LL * p.ctas; }

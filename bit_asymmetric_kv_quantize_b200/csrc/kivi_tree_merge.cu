@@ -147,12 +147,15 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.tt = 32;
     p.ctas = sms * (p.rb == 16 ? 4 : 3);
     p.min_w = 1;
+    p.parts = 0;
   } else {
-    p.n_rb = (rows + 63) / 64;
+    p.parts = rows <= 64 ? 2 : 4;
+    const int most = 32 * p.parts;
+    p.n_rb = (rows + most - 1) / most;
     p.rb = ((rows + p.n_rb - 1) / p.n_rb + 15) / 16 * 16;
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 128;
-    p.ctas = 2 * sms;
+    p.ctas = p.parts == 2 ? 2 * sms : sms;
     p.min_w = 1;
   }
   return p;

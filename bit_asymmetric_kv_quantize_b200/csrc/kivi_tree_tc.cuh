@@ -16,18 +16,24 @@
 //
 // Numbers.  A stored key is c s + z.  Rounded to binary16 it would move a score
 // by |q||K| 2^-12, more than everything else here together (key channels with
-// large values have large z), so it is carried exactly to about 2^-18:
-//   c s = c s_hi + c s_lo, s_hi the leading 7 bits of s: c s_hi is exact in
-//   binary16 for c < 16, c s_lo is rounded at 2^-18 of c s; two products;
-//   sum_d q_d z_d, the same for the 32 tokens of a group, is formed apart (z is
-//   one of the cache's fp16 inputs, so it is exact in binary16) by mma.sync and
-//   joins the score in binary32.
-// Values alike: sum_t p_t z_t of each value group apart.  With them, as one
-// more column of ones, the sum of the weights.  s is halved (a binary16 s_hi of
-// a 1-bit group of the widest range would overflow), so raw keys and values
-// are halved too and the results doubled in binary32.  The weights p are
-// rounded to binary16 once, relative 2^-12 on average like the output's own
-// rounding.  Scores, maxima, sums and accumulators are binary32.
+// large values have large z), so it is carried to about 2^-18:
+//   c s + z = c' s + z', c' = c - (2^bits - 1) / 2, z' = z + (2^bits - 1) / 2 s;
+//   c' s = c' s_hi + c' s_lo, s_hi the leading 7 bits of s: c' s_hi is exact in
+//   binary16, c' s_lo is rounded at 2^-18 of c' s; two products;
+//   sum_d q_d z'_d, the same for the 32 tokens of a group, is formed apart (z'
+//   as the sum of two binary16 numbers) by mma.sync and joins the score in
+//   binary32.
+// Values alike: sum_t p_t z'_t of each value group apart.  With them, as one
+// more column of ones, the sum of the weights.
+// Why the codes are centered: the tensor cores cut each accumulation off toward
+// zero.  With c itself all addends of a sum over tokens are positive, and the cuts
+// add up (the results of a 16384-token GQA layer were off by 1.3e-4 on average, as
+// much as a binary16 output's rounding); the sums of c' stay near zero.
+// s is halved (a binary16 s_hi of a 1-bit group of the widest range would
+// overflow), so raw keys and values are halved too and the results doubled in
+// binary32.  The weights p are rounded to binary16 once, relative 2^-12 on
+// average like the output's own rounding.  Scores, maxima, sums and accumulators
+// are binary32.
 //
 // Running maximum: a row's reference m is raised only when a score of a tile
 // exceeds it by more than 15 (in units of log2), and then to 4 below the tile's
@@ -68,16 +74,20 @@ namespace kivi {
 namespace {
 
 constexpr int kTcTile = 128;        // tokens
-constexpr int kTcWorkers = 256;
-constexpr int kTcWarps = 10;  // workers, matrix instructions, copies
-constexpr int kTcThreads = kTcWarps * 32;
+// Threads of a block of PARTS x 4 workers, one warp for the matrix instructions and one
+// for the copies.
+template <int PARTS>
+constexpr int kTcThreads = (4 * PARTS + 2) * 32;
 constexpr float kTcSlack = 15.0f;   // log2 units a score may exceed m by
 constexpr float kTcBelow = 4.0f;    // and those by which a rise leaves m below the maximum
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
 
 // ---- layouts ---------------------------------------------------------------
-template <int D, int BITS, int MB>
+template <int D, int BITS, int MB, int PARTS>
 struct TcGeo {
+  static constexpr int ROWS = 32 * PARTS;                // rows of a block at most
+  static constexpr int WARPS = 4 * PARTS, WORKERS = 32 * WARPS;
+  static constexpr int RT = 16 * PARTS;                  // raw tokens staged at a time
   using Lt = Layout<D, BITS>;
   static constexpr int E = Lt::E, WB = Lt::WB, WK = Lt::WK, NJ = Lt::NJ;
   // a stage of the ring: 4 subtiles of 32 tokens, array after array
@@ -92,31 +102,37 @@ struct TcGeo {
   static constexpr int O_VS = O_VC + 4 * VC;
   static constexpr int O_VZ = O_VS + 4 * VM;
   static constexpr int STAGE = O_VZ + 4 * VM;
-  static constexpr int NST = 49152 / STAGE < 5 ? 49152 / STAGE : 5;
+  static constexpr int RING = PARTS == 2 ? 49152 : 98304;
+  static constexpr int NST = RING / STAGE < 5 ? RING / STAGE : 5;
   // shared memory
   static constexpr int S_RING = 0;
-  static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [64 rows][D]
-  static constexpr int S_P = S_Q + 64 * D * 2;           // [64 rows][128 tokens]
-  // raw values [32 tokens][D]; at the end of a segment the sums, [2 parts][64 rows][8]
-  static constexpr int S_RAW = S_P + 64 * 128 * 2;
+  static constexpr int S_Q = S_RING + NST * STAGE;       // B operand, [ROWS][D]
+  static constexpr int S_P = S_Q + ROWS * D * 2;         // [ROWS][128 tokens]
+  // raw values [RT tokens][D]; at the end of a segment the sums, [PARTS][ROWS][8]
+  static constexpr int S_RAW = S_P + ROWS * 128 * 2;
   static constexpr int S_LZ = S_RAW;
-  static constexpr int S_KSC = S_RAW + (32 * D * 2 > 2 * 64 * 8 * 4 ? 32 * D * 2 : 2 * 64 * 8 * 4);
+  static constexpr int LZ = PARTS * ROWS * 8 * 4;
+  static constexpr int S_KSC = S_RAW + (RT * D * 2 > LZ ? RT * D * 2 : LZ);
                                                          // 4 groups x D x (hi, lo) halves
   static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 2 x 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // [2 parts][4 groups][64 rows] float
-  static constexpr int S_OFF = S_ZK + 2 * 4 * 64 * 4;    // [8 warps][16 rows]
-  static constexpr int S_WMAX = S_OFF + 8 * 16 * 4;      // [4 groups][64 rows]
-  static constexpr int S_M = S_WMAX + 4 * 64 * 4;        // [64 rows]
-  static constexpr int S_F = S_M + 64 * 4;               // [64 rows]
+  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // [PARTS][4 groups][ROWS] float
+  static constexpr int S_OFF = S_ZK + PARTS * 4 * ROWS * 4;  // [WARPS][16 rows]
+  static constexpr int S_WMAX = S_OFF + WARPS * 16 * 4;  // [4 groups][ROWS]
+  static constexpr int S_M = S_WMAX + 4 * ROWS * 4;      // [ROWS]
+  static constexpr int S_F = S_M + ROWS * 4;             // [ROWS]
   // zeros as binary16 in operand order, rows padded against bank conflicts:
-  // keys 4 groups x D, values 5 rows x 128 tokens (4 groups, ones)
+  // (high parts, low parts): keys 2 x 4 groups x D, values 9 rows x 128 tokens (high
+  // parts of 4 groups, ones, low parts of 4 groups)
   static constexpr int ZLD = 136;
-  static constexpr int S_ZH = S_F + 64 * 4;
-  static constexpr int S_ZV = S_ZH + 4 * ZLD * 2;        // 2 x
-  static constexpr int S_MASK = S_ZV + 2 * 5 * ZLD * 2;  // [N][ceil(N / 32)] words
+  static constexpr int S_ZH = S_F + ROWS * 4;
+  static constexpr int S_ZV = S_ZH + 8 * ZLD * 2;        // 2 x
+  static constexpr int S_MASK = S_ZV + 2 * 9 * ZLD * 2;  // [N][ceil(N / 32)] words
   static constexpr int BYTES = S_MASK;                   // and the mask
-  static constexpr int MOST = (227 * 1024 + 1024) / 2 - 1024;  // of two blocks on an SM
-  static_assert(NST >= 2 && BYTES + 256 * 8 * 4 + 256 <= MOST, "two blocks share an SM");
+  // of two blocks on an SM, or of one
+  static constexpr int MOST = PARTS == 2 ? (227 * 1024 + 1024) / 2 - 1024 : 227 * 1024 - 1024;
+  // (up to 64 rows are up to 64 nodes)
+  static constexpr int MASK = PARTS == 2 ? 64 * 2 * 4 : 256 * 8 * 4;
+  static_assert(NST >= 2 && BYTES + MASK + 256 <= MOST, "the blocks of an SM share it");
 };
 
 // Position of code i of a block of E in the order of the operands: the pair
@@ -300,16 +316,19 @@ __device__ __forceinline__ void tc_ldm(uint32_t (&a)[4], uint32_t addr) {
 }
 // Barriers: of the workers (1), of them and the warp of the matrix instructions (3),
 // and of the block with a vote (2: a thread's `x`).
+template <int PARTS>
 __device__ __forceinline__ void tc_sync_workers() {
   tc_fence_before();
-  asm volatile("bar.sync 1, %0;" ::"n"(kTcWorkers) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(kTcThreads<PARTS> - 64) : "memory");
   tc_fence_after();
 }
+template <int PARTS>
 __device__ __forceinline__ void tc_sync_scores() {
   tc_fence_before();
-  asm volatile("bar.sync 3, %0;" ::"n"(kTcWorkers + 32) : "memory");
+  asm volatile("bar.sync 3, %0;" ::"n"(kTcThreads<PARTS> - 32) : "memory");
   tc_fence_after();
 }
+template <int PARTS>
 __device__ __forceinline__ bool tc_sync_any(bool x) {
   uint32_t r;
   tc_fence_before();
@@ -317,7 +336,7 @@ __device__ __forceinline__ bool tc_sync_any(bool x) {
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "barrier.cta.red.or.pred.aligned q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kTcThreads)
+      : "r"((uint32_t)x), "n"(kTcThreads<PARTS>)
       : "memory");
   tc_fence_after();
   return r != 0;
@@ -325,10 +344,11 @@ __device__ __forceinline__ bool tc_sync_any(bool x) {
 
 // ---- codes as binary16 ---------------------------------------------------------
 // The eight pairs of registers 8 q .. 8 q + 7 of a lane (16 codes in operand
-// order) as exact binary16 integers.  A pair (i, i + E/2) of a word has its
-// codes in the two 16-bit halves, at bit BITS * i of each; a mask leaves it at
-// bit e < 10 of the half, 0x6400 | (c << e) is 1024 + c 2^e, and one fused
-// multiply-add by 2^-e gives c.
+// order) as exact binary16 numbers c' = c - (2^BITS - 1) / 2.  A pair (i, i + E/2)
+// of a word has its codes in the two 16-bit halves, at bit BITS * i of each; a shift
+// and a mask leave it at bit e of the half, 1 <= e, e + BITS <= 10; 0x6400 | (c << e) is
+// 1024 + c 2^e, and one fused multiply-add by 2^-e gives c' (2^(10 - e) plus the
+// center is a binary16 number from e = 1 on).
 __device__ __forceinline__ uint32_t tc_hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -340,31 +360,36 @@ __device__ __forceinline__ uint32_t tc_hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 // The constants stand in registers that the compiler does not see through: it would
-// form them again for each pair (an instruction each, a third of the unpacking).
+// form them again for each pair, an instruction each.
 struct TcConst {
-  uint32_t magic;           // 1024 in both halves
-  uint32_t inv[10], off[10];  // 2^-e and -2^(10 - e)
+  uint32_t magic;             // 1024 in both halves
+  uint32_t inv[10], off[10];  // 2^-e and -(2^(10 - e) + center)
 };
+template <int BITS>
 __device__ __forceinline__ TcConst tc_const() {
   TcConst k;
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k.magic));
 #pragma unroll
   for (int e = 1; e < 10; ++e) {
     k.inv[e] = ((15u - e) << 10) * 0x00010001u;
-    k.off[e] = (0x8000u | (25u - e) << 10) * 0x00010001u;
+    k.off[e] = (0x8000u | (25u - e) << 10 | ((1u << BITS) - 1u) << (e - 1)) * 0x00010001u;
     asm volatile("" : "+r"(k.inv[e]), "+r"(k.off[e]));
   }
   return k;
 }
-// (x & m) | magic, then 1024 + c 2^e to c.
-template <int E_BIT>
+// (x & m) | magic, then 1024 + c 2^e to c'.
+template <int BITS, int E_BIT>
 __device__ __forceinline__ uint32_t tc_code(uint32_t x, uint32_t m, const TcConst& k) {
   uint32_t d, y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(m), "r"(k.magic));
-  if constexpr (E_BIT == 0)
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(y), "r"(0xE400E400u));
-  else
+  if constexpr (E_BIT == 0) {  // 3 bits only: -1024, -3.5
+    static_assert(BITS == 3, "the other formats begin at bit 1");
+    asm("{\n\t.reg .b32 z;\n\tadd.rn.f16x2 z, %1, %2;\n\tadd.rn.f16x2 %0, z, %3;\n\t}"
+        : "=r"(d)
+        : "r"(y), "r"(0xE400E400u), "r"(0xC300C300u));
+  } else {
     d = tc_hfma2(y, k.inv[E_BIT], k.off[E_BIT]);
+  }
   return d;
 }
 // Pair I of a block whose words are w[0 .. WB).
@@ -375,12 +400,15 @@ __device__ __forceinline__ uint32_t tc_pair(const uint32_t* w, const TcConst& k)
     constexpr uint32_t m = 0x00010001u << e;
     const uint32_t p = ((w[0] >> sh) & m) | (((w[1] >> sh) << 1) & (m << 1)) |
                        (((w[2] >> sh) << 2) & (m << 2));
-    return tc_code<e>(p, 0xFFFFFFFFu, k);
+    return tc_code<3, e>(p, 0xFFFFFFFFu, k);
   } else {
-    constexpr int per = 10 / BITS;  // pairs whose codes end below bit 10 of the half
-    constexpr int sh = I / per * per * BITS, e = I % per * BITS;
+    constexpr int per = 9 / BITS;  // pairs of one shift
+    constexpr int at = I / per * per * BITS, e = 1 + I % per * BITS;
     constexpr uint32_t m = ((1u << BITS) - 1u) * 0x00010001u << e;
-    return tc_code<e>(sh ? w[0] >> sh : w[0], m, k);
+    if constexpr (at == 0)
+      return tc_code<BITS, e>(w[0] << 1, m, k);
+    else
+      return tc_code<BITS, e>(w[0] >> (at - 1), m, k);
   }
 }
 // What a loop over a lane's words takes at a time: kUnit codes in kUnitW words.
@@ -420,6 +448,13 @@ __device__ __forceinline__ void tc_split(float s, __half* hi, __half* lo) {
   *hi = __float2half_rn(h);
   *lo = __float2half_rn(s - __half2float(*hi));
 }
+// z' = z + s * center, the codes' center, in two binary16 parts.
+template <int BITS>
+__device__ __forceinline__ void tc_center(float s, float z, __half* hi, __half* lo) {
+  const float x = fmaf(s, 0.5f * ((1 << BITS) - 1), z);
+  *hi = __float2half_rn(x);
+  *lo = __float2half_rn(x - __half2float(*hi));
+}
 // 16 codes times their scales (8 pairs of s_hi and of s_lo from shared memory, one
 // address for the whole warp) into the two planes.
 __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uint32_t (&c)[8],
@@ -446,16 +481,16 @@ __device__ __forceinline__ void tc_put16(uint32_t t_hi, uint32_t t_lo, const uin
   r[7] = tc_hmul2(c[7], f.w);
   tc_st8(t_lo, r);
 }
-// Units `part`, part + 2, .. (of n) of a lane's words (`stride` words apart) into its
+// Units `part`, part + PARTS, .. (of n) of a lane's words (`stride` words apart) into its
 // row of the two planes; hi, lo: the parts of the row's scales.
-template <int BITS>
+template <int BITS, int PARTS>
 __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, int stride,
                                           const uint4* hi, const uint4* lo, int part, int n,
                                           const TcConst& k) {
   using U = TcUnit<BITS>;
   constexpr int H = U::kUnit / 16;
 #pragma unroll(H == 2 ? 1 : 2)
-  for (int u = part; u < n; u += 2) {
+  for (int u = part; u < n; u += PARTS) {
     uint32_t w[U::kUnitW], c[8];
 #pragma unroll
     for (int i = 0; i < U::kUnitW; ++i) w[i] = words[(u * U::kUnitW + i) * stride];
@@ -503,19 +538,19 @@ __device__ __forceinline__ void tc_raw_pairs(const uint4& x, const uint4& y, uin
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = tc_hmul2(r[j], 0x38003800u);
 }
-// 32 raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
+// RT raw tokens from `first` on (the window's r tokens at wp, then the drafted ones
 // at dp up to n) into rows of D in shared memory, by all workers.  Loads without
 // branches, so that they are under way together; a token that does not exist reads
 // the window's first row.
-template <int D>
+template <int D, int RT, int WORKERS>
 __device__ __forceinline__ void tc_stage_raw(uint4* dst, const __half* wp, const __half* dp,
                                              int first, int r, int n) {
-  constexpr int J = (32 * (D / 8) + kTcWorkers - 1) / kTcWorkers;
+  constexpr int J = (RT * (D / 8) + WORKERS - 1) / WORKERS;
   const bool al = ((uintptr_t)dp & 15) == 0;
   uint4 x[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int k = (threadIdx.x + kTcWorkers * j) % (32 * (D / 8)), i = first + k / (D / 8);
+    const int k = (threadIdx.x + WORKERS * j) % (RT * (D / 8)), i = first + k / (D / 8);
     const int c = k % (D / 8) * 8;
     x[j] = *reinterpret_cast<const uint4*>(al && i >= r && i < n ? dp + (i - r) * D + c
                                                                  : wp + (i < r ? i * D + c : c));
@@ -523,7 +558,7 @@ __device__ __forceinline__ void tc_stage_raw(uint4* dst, const __half* wp, const
     if (!al && i >= r && i < n) x[j] = tc_raw8(dp + (i - r) * D + c, false);
   }
 #pragma unroll
-  for (int j = 0; j < J; ++j) dst[(threadIdx.x + kTcWorkers * j) % (32 * (D / 8))] = x[j];
+  for (int j = 0; j < J; ++j) dst[(threadIdx.x + WORKERS * j) % (RT * (D / 8))] = x[j];
 }
 // A lane's raw key row, halved, into its operand row, 16-place pieces c0 .. c0 + N - 1:
 // two runs of 8 channels E / 2 apart each (or two blocks of 8 channels).  Loads as
@@ -547,7 +582,7 @@ __device__ __forceinline__ void tc_raw_keys(uint32_t t_hi, const __half* row, bo
     tc_st8(t_hi + 8 * (c0 + j), r);
   }
 }
-// 16 places of a lane's channel of 32 raw tokens (`v`, rows of D in shared memory),
+// 16 places of a lane's channel of the staged raw tokens (`v`, rows of D in shared memory),
 // halved, into its operand row.  Infinities and NaN are left out (they join at the
 // segment's end, for the rows that attend to them); returns whether there were any.
 template <int D, int E>
@@ -594,8 +629,14 @@ __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, in
   return bits;
 }
 
-// Tensor-memory columns: two planes of keys, then of values; S^T; O^T.
-constexpr uint32_t kTA = 0, kTS = 128, kTO = 192, kTCols = 256;
+// Tensor-memory columns: two planes of keys; two of values (the same ones where two
+// blocks share tensor memory); S^T; O^T.
+template <int PARTS>
+struct TcCols {
+  static constexpr bool APART = PARTS == 4;
+  static constexpr uint32_t A = 0, V = APART ? 128 : 0, S = V + 128, O = S + 32 * PARTS,
+                            N = O + 32 * PARTS;
+};
 
 // Barriers for what is asynchronous, 8 bytes each, by their number.
 struct TcBar {
@@ -616,9 +657,13 @@ struct TcWalk {
   int h, rb, t;
 };
 
-template <int D, int BITS, typename M>
-__global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, TreePlan p) {
-  using Ge = TcGeo<D, BITS, (int)sizeof(M)>;
+template <int D, int BITS, typename M, int PARTS>
+__global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
+    tree_tc_kernel(TreeArgs a, TreePlan p) {
+  using Ge = TcGeo<D, BITS, (int)sizeof(M), PARTS>;
+  using Col = TcCols<PARTS>;
+  constexpr int ROWS = Ge::ROWS, WORKERS = Ge::WORKERS, RT = Ge::RT;
+  constexpr int RC = ROWS / 64;  // 16-row chunks of a warp in the products of the zeros
   constexpr int E = Ge::E, WK = Ge::WK, NJ = Ge::NJ;
   constexpr int KS = D / 16;  // k-slices of the scores
   extern __shared__ __align__(128) unsigned char sm[];
@@ -637,10 +682,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
 
   // ---- set-up
   asm volatile("griddepcontrol.launch_dependents;");
-  if (warp == 8) {
+  if (warp == Ge::WARPS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      tc_smem(&s_tmem)),
-                 "n"(kTCols)
+                 "n"(Col::N)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -665,8 +710,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     for (int i = 0; i < TcBar::N; ++i) tc_bar_init(bar(i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < 2 * 5 * Ge::ZLD; i += kTcThreads)
-    reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 5 == 4 ? 1.0f : 0.0f);
+  for (int i = tid; i < 2 * 9 * Ge::ZLD; i += kTcThreads<PARTS>)
+    reinterpret_cast<__half*>(sm + Ge::S_ZV)[i] = __float2half_rn(i / Ge::ZLD % 9 == 4 ? 1.0f : 0.0f);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -675,8 +720,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
 
   float* m_s = reinterpret_cast<float*>(sm + Ge::S_M);    // references
   float* f_s = reinterpret_cast<float*>(sm + Ge::S_F);    // factors of a rise
-  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [part][group][64]
-  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [part][64][8]
+  float* zk_s = reinterpret_cast<float*>(sm + Ge::S_ZK);  // [part][group][ROWS]
+  float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [part][ROWS][8]
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
   // A range ends within a group at most at its own end: segments after the first
@@ -718,7 +763,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     return g;
   };
 
-  if (warp == 9) {
+  if (warp == Ge::WARPS + 1) {
     // ==== copies: lane k < 6 copies a tile's part of array k, in one piece, or one for
     // each page that it touches; a tile's stage is free once the block has passed the
     // barrier of the tile NST before it
@@ -765,7 +810,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     while (tc_uniform(walk.left > 0)) {
       const TcSeg g = next_seg(walk);
       for (int t = g.t0; t < g.t1 && g.ok; ++t) {  // the block's barriers
-        if (tc_sync_any(false)) tc_sync_any(false);
+        if (tc_sync_any<PARTS>(false)) tc_sync_any<PARTS>(false);
         if (t < g.t1s) {
           ++done;
           fill();
@@ -774,7 +819,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     }
     for (int i = max(issued - Ge::NST, 0); i < issued; ++i)  // none is under way at the end
       tc_wait(bar(TcBar::raw + i % Ge::NST), i / Ge::NST, dead);
-  } else if (warp == 8) {
+  } else if (warp == Ge::WARPS) {
     // ==== matrix instructions
     const bool one = tc_elect();
     const uint32_t id_s = tc_idesc(nr, false), id_o = tc_idesc(nr, true);
@@ -784,17 +829,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
       if (!g.ok) continue;
       for (int t = g.t0; t < g.t1; ++t) {
         const bool lo = t < g.t1s;
-        tc_sync_scores();
+        tc_sync_scores<PARTS>();
         if (one) {
-          tc_mma_row<KS>(tmem + kTS, tmem + kTA, q_desc, id_s, false);
-          if (lo) tc_mma_row<KS>(tmem + kTS, tmem + kTA + 64, q_desc, id_s, true);
+          tc_mma_row<KS>(tmem + Col::S, tmem + Col::A, q_desc, id_s, false);
+          if (lo) tc_mma_row<KS>(tmem + Col::S, tmem + Col::A + 64, q_desc, id_s, true);
           tc_commit(bar(TcBar::scores));
         }
         __syncwarp();
-        if (tc_sync_any(false)) tc_sync_any(false);
+        if (tc_sync_any<PARTS>(false)) tc_sync_any<PARTS>(false);
         if (one) {
-          tc_mma_row<8>(tmem + kTO, tmem + kTA, p_desc, id_o, t > g.t0);
-          if (lo) tc_mma_row<8>(tmem + kTO, tmem + kTA + 64, p_desc, id_o, true);
+          tc_mma_row<8>(tmem + Col::O, tmem + Col::V, p_desc, id_o, t > g.t0);
+          if (lo) tc_mma_row<8>(tmem + Col::O, tmem + Col::V + 64, p_desc, id_o, true);
           tc_commit(bar(TcBar::values));
         }
         __syncwarp();
@@ -802,12 +847,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
     }
   } else {
     // ==== workers
-    const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, half of the columns
+    const int q = warp & 3, part = warp >> 2;  // lanes of tensor memory, share of the columns
     const uint32_t t_q = tmem + ((uint32_t)(q * 32) << 16);
     const int n8 = lane >> 2, kq = (lane & 3) * 2;  // fragments of mma.sync
     const int pk = tc_pos<E>(q * 32 + lane);        // this lane's token in the second product
     const float c1 = 2.0f * a.qscale;
-    const TcConst konst = tc_const();
+    const TcConst konst = tc_const<BITS>();
     __half* ksc = reinterpret_cast<__half*>(sm + Ge::S_KSC);
     __half* vsc0 = reinterpret_cast<__half*>(sm + Ge::S_VSC);
     __half* zh = reinterpret_cast<__half*>(sm + Ge::S_ZH);
@@ -828,7 +873,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
       if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
         const long long i1 = min(g.t1 * 4LL, g.n_q / kTile);
 #pragma unroll 1
-        for (long long i = g.t0 * 4LL + tid; i < i1; i += kTcWorkers) {
+        for (long long i = g.t0 * 4LL + tid; i < i1; i += WORKERS) {
           long long su, stl;
           if (!store_tile(a.c, g.unit, i, &su, &stl)) s_poison[seg & 1] = 1;
         }
@@ -838,7 +883,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
         const bool al = ((uintptr_t)qp & 15) == 0;
         // operand order along channels; rows that do not exist are 0
 #pragma unroll 2
-        for (int i = tid; i < nr * (D / 8); i += kTcWorkers) {
+        for (int i = tid; i < nr * (D / 8); i += WORKERS) {
           const int row = i / (D / 8), c0 = i % (D / 8) * 8;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (row < g.nrows) x = tc_raw8(qp + row * D + c0, al);
@@ -851,66 +896,69 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
           }
         }
 #pragma unroll 1
-        for (int i = tid; i < a.N * mw; i += kTcWorkers)
+        for (int i = tid; i < a.N * mw; i += WORKERS)
           mask_s[i] = a.mask[g.b * a.N * mw + i];
-        if (tid < 64) m_s[tid] = kTcNone;
+        if (tid < ROWS) m_s[tid] = kTcNone;
       }
       tc_fence_smem();
 
       // scales and zeros of tile t's keys and values
       auto set_out = [&](int t) {
-        __half* zv = zv0 + (t & 1) * 5 * Ge::ZLD;
+        __half* zv = zv0 + (t & 1) * 9 * Ge::ZLD;
         __half* vsc = vsc0 + (t & 1) * 1024;
         const bool raw = t >= g.t1s;
         const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
         if (!raw) {
           tc_wait(bar(TcBar::raw + (st0 + t - g.t0) % Ge::NST), (st0 + t - g.t0) / Ge::NST, dead);
 #pragma unroll
-          for (int j = 0; j < (4 * D + kTcWorkers - 1) / kTcWorkers; ++j) {
-            const int i = tid + kTcWorkers * j, gr = i / D, c = tc_pos<E>(i % D);
+          for (int j = 0; j < (4 * D + WORKERS - 1) / WORKERS; ++j) {
+            const int i = tid + WORKERS * j, gr = i / D, c = tc_pos<E>(i % D);
             if (i < 4 * D) {
-              zh[gr * Ge::ZLD + c] = __float2half_rn(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[i]));
-              tc_split(to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[i]), &ksc[gr * 2 * D + c],
-                       &ksc[gr * 2 * D + D + c]);
+              const float s = to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[i]);
+              tc_center<BITS>(s, to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[i]),
+                              &zh[gr * Ge::ZLD + c], &zh[(4 + gr) * Ge::ZLD + c]);
+              tc_split(s, &ksc[gr * 2 * D + c], &ksc[gr * 2 * D + D + c]);
             }
           }
         }
         const long long left = g.n_q - (long long)t * kTcTile;
 #pragma unroll
-        for (int j = 0; j < (128 * NJ + kTcWorkers - 1) / kTcWorkers; ++j) {
-          const int i = tid + kTcWorkers * j, tok = i / NJ, gr = i % NJ, c = tc_pos<E>(tok);
+        for (int j = 0; j < (128 * NJ + WORKERS - 1) / WORKERS; ++j) {
+          const int i = tid + WORKERS * j, tok = i / NJ, gr = i % NJ, c = tc_pos<E>(tok);
           if (i < 128 * NJ) {
             // tokens that do not exist: 0 (their weight 0 times NaN would not be)
             const bool have = !raw && tok < left;
-            zv[gr * Ge::ZLD + c] =
-                __float2half_rn(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[i]) : 0.f);
-            tc_split(have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[i]) : 0.f,
-                     &vsc[gr * 256 + c], &vsc[gr * 256 + 128 + c]);
+            const float s = have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[i]) : 0.f;
+            tc_center<BITS>(s, have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[i]) : 0.f,
+                            &zv[gr * Ge::ZLD + c], &zv[(5 + gr) * Ge::ZLD + c]);
+            tc_split(s, &vsc[gr * 256 + c], &vsc[gr * 256 + 128 + c]);
           }
         }
       };
       // keys of tile t into tensor memory, and their zeros' products
       auto put_keys = [&](int t) {
-        float zc[4] = {0.f, 0.f, 0.f, 0.f};
+        float zc[RC][4] = {};
         if (t < g.t1s) {
           const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
           const __half* sc = ksc + q * 2 * D;
-          tc_unpack<BITS>(t_q + kTA, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
-                          reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
-                          D / TcUnit<BITS>::kUnit, konst);
-          if (q < nch) {
-            // sum_d q_d z_gd for rows 16 q .., over half of the channels (this warp's q
-            // counts rows here); lane n8 of a column reads group n8's row, columns 4 .. 7
-            // are read by nobody
-            const __half* zr = zh + (n8 & 3) * Ge::ZLD + kq;
-            const int row = 16 * q + (lane & 15);
+          tc_unpack<BITS, PARTS>(t_q + Col::A, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
+                                 reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
+                                 D / TcUnit<BITS>::kUnit, konst);
+          // sum_d q_d z'_gd for rows 16 q .. (and 64 further on), over this part's channels
+          // (the warp's q counts rows here); columns: the groups' high parts, their low parts
+          const __half* zr = zh + n8 * Ge::ZLD + kq;
+#pragma unroll
+          for (int c = 0; c < RC; ++c) {
+            if (q + 4 * c >= nch) break;
+            const int row = 16 * (q + 4 * c) + (lane & 15);
             const uint32_t qa = sm0 + Ge::S_Q + row / 8 * (D * 16) + (lane >> 4) * 128 + row % 8 * 16;
 #pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-              const int ks = part + 2 * j;
+            for (int j = 0; j < (KS + PARTS - 1) / PARTS; ++j) {
+              const int ks = part + PARTS * j;
+              if (KS < PARTS && ks >= KS) break;
               uint32_t av[4];
               tc_ldm<false>(av, qa + 256 * ks);
-              tc_mma16816(zc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+              tc_mma16816(zc[c], av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
                           *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
             }
           }
@@ -918,53 +966,101 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
           // raw tokens: the window, then the drafted ones; halved like s
           const int i = (t - g.tq) * kTcTile + q * 32 + lane;
           const __half* src = i < g.r ? wk + i * D : (i < n_raw ? dk + (i - g.r) * D : wk);
-          tc_raw_keys<E, D / 32>(t_q + kTA, src, i < n_raw, part * (D / 32));
+          constexpr int N = D / 16 < PARTS ? 1 : D / 16 / PARTS;
+          if (part * N < D / 16) tc_raw_keys<E, N>(t_q + Col::A, src, i < n_raw, part * N);
         }
-        if (q < nch && kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
-          float* z = zk_s + (part * 4 + kq) * 64 + 16 * q + n8;
-          z[0] = zc[0] * a.qscale;
-          z[64] = zc[1] * a.qscale;
-          z[8] = zc[2] * a.qscale;
-          z[72] = zc[3] * a.qscale;
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+          if (q + 4 * c >= nch) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) zc[c][e] += __shfl_xor_sync(0xffffffffu, zc[c][e], 2);
+          // (all lanes go through all chunks: shuffles above)
+          if (kq < 4) {  // lane: rows n8, n8 + 8; groups kq, kq + 1
+            float* z = zk_s + (part * 4 + kq) * ROWS + 16 * (q + 4 * c) + n8;
+            z[0] = zc[c][0] * a.qscale;
+            z[ROWS] = zc[c][1] * a.qscale;
+            z[8] = zc[c][2] * a.qscale;
+            z[ROWS + 8] = zc[c][3] * a.qscale;
+          }
         }
       };
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      // sums over tile t's tokens, of the weights and of the values' zeros: rows 16 q ..,
-      // half of the tokens
+      float acc[RC][4] = {};
+      // sums over tile t's tokens, of the weights and of the values' zeros: rows 16 q .. (and
+      // 64 further on), this part's tokens
       auto sums = [&](int t) {
-        if (q >= nch) return;
-        // (columns 5 .. 7 are read by nobody)
-        const __half* zr = zv0 + ((t & 1) * 5 + (n8 < 4 ? n8 : 4)) * Ge::ZLD + kq;
+        // (columns 5 .. 7 are read by nobody); a second product adds the low parts
+        const __half* zr = zv0 + ((t & 1) * 9 + (n8 < 4 ? n8 : 4)) * Ge::ZLD + kq;
+        const __half* zl = zv0 + ((t & 1) * 9 + 5 + (n8 & 3)) * Ge::ZLD + kq;
+        const uint32_t keep = n8 < 4 ? 0xFFFFFFFFu : 0u;
         // 8 x 8 blocks (tokens x rows) of weights, transposed on the way
         const int blk = lane >> 3;
         const uint32_t pa = sm0 + Ge::S_P + q * 4096 + (blk & 1) * 2048 + (blk >> 1) * 128 + (lane & 7) * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ks = 4 * part + j;
-          uint32_t av[4];
-          tc_ldm<true>(av, pa + ks * 256);
-          tc_mma16816(acc, av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
-                      *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+        for (int c = 0; c < RC; ++c) {
+          if (q + 4 * c >= nch) break;
+#pragma unroll
+          for (int j = 0; j < 8 / PARTS; ++j) {
+            const int ks = 8 / PARTS * part + j;
+            uint32_t av[4];
+            tc_ldm<true>(av, pa + c * 4 * 4096 + ks * 256);
+            tc_mma16816(acc[c], av, *reinterpret_cast<const uint32_t*>(zr + 16 * ks),
+                        *reinterpret_cast<const uint32_t*>(zr + 16 * ks + 8));
+            tc_mma16816(acc[c], av, *reinterpret_cast<const uint32_t*>(zl + 16 * ks) & keep,
+                        *reinterpret_cast<const uint32_t*>(zl + 16 * ks + 8) & keep);
+          }
         }
+      };
+      // values of tile t into tensor memory
+      auto put_values = [&](int t) {
+        if (t >= g.t1s) {
+#pragma unroll 1
+          for (int n = 0; n < kTcTile / RT; ++n) {
+            tc_sync_workers<PARTS>();
+            tc_stage_raw<D, RT, WORKERS>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv,
+                                         (t - g.tq) * kTcTile + RT * n, g.r, n_raw);
+            tc_sync_workers<PARTS>();
+            if (q < NJ && tc_raw_values<D, E>(t_q + Col::V + RT / 2 * n + 8 * part,
+                                              reinterpret_cast<const __half*>(sm + Ge::S_RAW) + q * 32 + lane, part))
+              s_odd = 1;
+          }
+        } else if (q < NJ) {
+          const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
+          const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
+          tc_unpack<BITS, PARTS>(t_q + Col::V, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
+                                 reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
+                                 128 / TcUnit<BITS>::kUnit, konst);
+        }
+      };
+      auto zeros = [&](const float* zk, int row) -> float {  // zk: of a group; over the parts
+        float z = zk[row];
+#pragma unroll
+        for (int e = 1; e < PARTS; ++e) z += zk[e * 4 * ROWS + row];
+        return z;
       };
 
       if (g.ok) {
         set_out(g.t0);
-        tc_sync_workers();
+        tc_sync_workers<PARTS>();
 #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t) {
           const int it = it0 + t - g.t0;
           const bool raw = t >= g.t1s;
           // ---- keys
-          if (t > g.t0) {  // the planes were read, and so were the weights
+          auto done_values = [&]() {  // the planes were read, and so were the weights
+            if (t == g.t0) return;
             tc_wait(bar(TcBar::values), it - 1, dead);
             tc_fence_after();
-          }
+          };
+          if (!Col::APART) done_values();
           put_keys(t);
           tc_wait_st();
-          tc_sync_scores();
+          tc_sync_scores<PARTS>();
           if (t + 1 < g.t1) set_out(t + 1);
-          // ---- weights of 16-row chunks part, part + 2, against the references; `over`: by
+          if (Col::APART) {
+            done_values();
+            put_values(t);
+          }
+          // ---- weights of 16-row chunks part, part + PARTS, against the references; `over`: by
           // how much a score exceeds its own.  The lane's token: in the cache (all rows see
           // it), drafted, or none
           const long long i = (long long)(raw ? t - g.tq : t) * kTcTile + q * 32 + lane;
@@ -974,18 +1070,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
             return in ? 0xFFFFu : node < 0 ? 0u : tc_seen(mask_s, node, g.row0 + 16 * ch, a.N);
           };
           unsigned char* pb = sm + Ge::S_P + pk / 8 * 128 + pk % 8 * 16;
-          const float* zk = zk_s + q * 64;  // the zeros' products of the lane's group
+          const float* zk = zk_s + q * ROWS;  // the zeros' products of the lane's group
           auto weights = [&]() -> float {
             float over = -__builtin_huge_valf();
 #pragma unroll 1
-            for (int ch = part; ch < nch; ch += 2) {
+            for (int ch = part; ch < nch; ch += PARTS) {
               if (lane < 16) {
                 const int row = 16 * ch + lane;
-                off_s[lane] = m_s[row] - (zk[row] + zk[4 * 64 + row]);
+                off_s[lane] = m_s[row] - zeros(zk, row);
               }
               __syncwarp();
               float v[16];
-              tc_ld16(t_q + kTS + 16 * ch, v);
+              tc_ld16(t_q + Col::S + 16 * ch, v);
 #pragma unroll
               for (int e4 = 0; e4 < 4; ++e4) {
                 const float4 o = *reinterpret_cast<const float4*>(off_s + 4 * e4);
@@ -1016,36 +1112,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
           tc_wait(bar(TcBar::scores), it, dead);
           tc_fence_after();
           const float over = weights();
-          // ---- values, into the keys' place
-          if (raw) {
-#pragma unroll 1
-            for (int b32 = 0; b32 < 4; ++b32) {
-              tc_sync_workers();
-              tc_stage_raw<D>(reinterpret_cast<uint4*>(sm + Ge::S_RAW), wv, dv, (t - g.tq) * kTcTile + 32 * b32,
-                              g.r, n_raw);
-              tc_sync_workers();
-              if (q < NJ && tc_raw_values<D, E>(t_q + kTA + 16 * b32 + 8 * part,
-                                                reinterpret_cast<const __half*>(sm + Ge::S_RAW) + q * 32 + lane, part))
-                s_odd = 1;
-            }
-          } else if (q < NJ) {
-            const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-            const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
-            tc_unpack<BITS>(t_q + kTA, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
-                            reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
-                            128 / TcUnit<BITS>::kUnit, konst);
-          }
+          if (!Col::APART) put_values(t);
           tc_wait_st();
           tc_fence_smem();
-          const bool rise = tc_uniform(tc_sync_any(over > kTcSlack));
+          const bool rise = tc_uniform(tc_sync_any<PARTS>(over > kTcSlack));
           if (rise) {
             // ---- new references: the maxima of the tile, joined over its groups
 #pragma unroll 1
-            for (int ch = part; ch < nch; ch += 2) {
+            for (int ch = part; ch < nch; ch += PARTS) {
               float v[16];
-              tc_ld16(t_q + kTS + 16 * ch, v);
+              tc_ld16(t_q + Col::S + 16 * ch, v);
               const uint32_t sees = seen(ch);
-              const float z = lane < 16 ? zk[16 * ch + lane] + zk[4 * 64 + 16 * ch + lane] : 0.f;
+              const float z = lane < 16 ? zeros(zk, 16 * ch + lane) : 0.f;
               float mine = kTcNone;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -1053,54 +1131,58 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
                 const float m = tc_warp_max((sees >> e) & 1u ? d : kTcNone);
                 if (lane == e) mine = m;
               }
-              if (lane < 16) wmax_s[q * 64 + 16 * ch + lane] = mine;
+              if (lane < 16) wmax_s[q * ROWS + 16 * ch + lane] = mine;
             }
-            tc_sync_workers();
+            tc_sync_workers<PARTS>();
             if (tid < nr) {
               const float old = m_s[tid];
-              const float mn = fmaxf(fmaxf(fmaxf(wmax_s[tid], wmax_s[64 + tid]),
-                                           fmaxf(wmax_s[128 + tid], wmax_s[192 + tid])) - kTcBelow,
+              const float mn = fmaxf(fmaxf(fmaxf(wmax_s[tid], wmax_s[ROWS + tid]),
+                                           fmaxf(wmax_s[2 * ROWS + tid], wmax_s[3 * ROWS + tid])) - kTcBelow,
                                      old);
               f_s[tid] = old == kTcNone ? 0.0f : tc_ex2(old - mn);
               m_s[tid] = mn;
             }
-            tc_sync_workers();
+            tc_sync_workers<PARTS>();
             weights();
             if (t > g.t0) {  // the accumulators so far (their products are done)
 #pragma unroll 1
-              for (int ch = part; ch < nch; ch += 2) {
+              for (int ch = part; ch < nch; ch += PARTS) {
                 float v[16];
-                tc_ld16(t_q + kTO + 16 * ch, v);
+                tc_ld16(t_q + Col::O + 16 * ch, v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] *= f_s[16 * ch + k];
-                tc_st16(t_q + kTO + 16 * ch, v);
+                tc_st16(t_q + Col::O + 16 * ch, v);
               }
               tc_wait_st();
             }
-            if (q < nch) {
-              const float f0 = f_s[16 * q + n8], f1 = f_s[16 * q + n8 + 8];
-              acc[0] *= f0;
-              acc[1] *= f0;
-              acc[2] *= f1;
-              acc[3] *= f1;
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {
+              if (q + 4 * c >= nch) break;
+              const float* f = f_s + 16 * (q + 4 * c) + n8;
+              acc[c][0] *= f[0];
+              acc[c][1] *= f[0];
+              acc[c][2] *= f[8];
+              acc[c][3] *= f[8];
             }
             tc_fence_smem();
-            tc_sync_any(false);
+            tc_sync_any<PARTS>(false);
           }
           sums(t);
         }
-        if (q < nch) {
-          float* z = lz_s + (part * 64 + 16 * q + n8) * 8 + kq;
-          z[0] = acc[0];
-          z[1] = acc[1];
-          z[64] = acc[2];
-          z[65] = acc[3];
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+          if (q + 4 * c >= nch) break;
+          float* z = lz_s + (part * ROWS + 16 * (q + 4 * c) + n8) * 8 + kq;
+          z[0] = acc[c][0];
+          z[1] = acc[c][1];
+          z[64] = acc[c][2];
+          z[65] = acc[c][3];
         }
         tc_wait(bar(TcBar::values), it0 + g.t1 - 1 - g.t0, dead);
       }
-      tc_sync_workers();
+      tc_sync_workers<PARTS>();
 
-      // ---- end of a segment: lane = channel, rows 4 part .. of each 8
+      // ---- end of a segment: lane = channel, rows 4 part .. of each 4 PARTS
       {
         const int ch_d = q * 32 + lane;
         const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
@@ -1108,16 +1190,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
         float* pt = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
         __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
 #pragma unroll 1
-        for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 8) {
+        for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 4 * PARTS) {
           float v[4] = {0.f, 0.f, 0.f, 0.f};
-          if (g.ok) tc_ld4(t_q + kTO + e4, v);
+          if (g.ok) tc_ld4(t_q + Col::O + e4, v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int row = e4 + e;
             if (row >= g.nrows) break;
             const float* z = lz_s + row * 8;
-            float l = z[4] + z[512 + 4], m = m_s[row];
-            float o = fmaf(2.0f, v[e], z[q] + z[512 + q]);
+            float l = z[4], m = m_s[row], zs = z[q];
+#pragma unroll
+            for (int i = 1; i < PARTS; ++i) {
+              l += z[i * ROWS * 8 + 4];
+              zs += z[i * ROWS * 8 + q];
+            }
+            float o = fmaf(2.0f, v[e], zs);
             // infinite or NaN raw values, of the tokens that the row attends to
 #pragma unroll 1
             for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
@@ -1147,13 +1234,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_tc_kernel(TreeArgs a, Tree
         it0 += g.t1 - g.t0;
         st0 += max(g.t1s - g.t0, 0);
       }
-      tc_sync_workers();
+      tc_sync_workers<PARTS>();
     }
   }
 
   __syncthreads();
-  if (warp == 8) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTCols)
+  if (warp == Ge::WARPS) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Col::N)
                  : "memory");
   }
 }

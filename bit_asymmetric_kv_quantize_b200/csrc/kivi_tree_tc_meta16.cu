@@ -5,15 +5,19 @@
 namespace kivi {
 namespace {
 
+template <int D, int BITS, int PARTS>
+cudaError_t tc_p(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
+  using Ge = TcGeo<D, BITS, (int)sizeof(__half), PARTS>;
+  const int bytes = a.N * ((a.N + 31) / 32) * 4 + Ge::BYTES;
+  static std::atomic<bool> done[kTreeDevices];
+  const cudaError_t e = tree_smem(tree_tc_kernel<D, BITS, __half, PARTS>, Ge::MOST, done);
+  if (e != cudaSuccess) return e;
+  tree_tc_kernel<D, BITS, __half, PARTS><<<p.ctas, kTcThreads<PARTS>, bytes, s>>>(a, p);
+  return cudaGetLastError();
+}
 template <int D, int BITS>
 cudaError_t tc_t(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
-  const int bytes = a.N * ((a.N + 31) / 32) * 4 + TcGeo<D, BITS, (int)sizeof(__half)>::BYTES;
-  static std::atomic<bool> done[kTreeDevices];
-  const cudaError_t e =
-      tree_smem(tree_tc_kernel<D, BITS, __half>, TcGeo<D, BITS, (int)sizeof(__half)>::MOST, done);
-  if (e != cudaSuccess) return e;
-  tree_tc_kernel<D, BITS, __half><<<p.ctas, kTcThreads, bytes, s>>>(a, p);
-  return cudaGetLastError();
+  return p.parts == 2 ? tc_p<D, BITS, 2>(a, p, s) : tc_p<D, BITS, 4>(a, p, s);
 }
 template <int BITS>
 cudaError_t tc_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {

@@ -209,6 +209,34 @@ def test_tree_many_small_weights_beside_a_large_one():
         assert ((out.cpu().double() - ref).abs() <= 0.01 * ref).all()
 
 
+@pytest.mark.parametrize("N", [3, 80])
+def test_tree_long_sums_do_not_drift(N):
+    """Equal weights (powers of two, so exact) over a long cache whose values are spread around zero:
+    the mean is small beside the codes' products, and cuts toward zero at each step of a sum would
+    pull it down.  Off by at most, with c' s + z' a stored value and c' its code about the
+    center: half a step of the output; 2^-17 of |c' s| for the two parts of s; and for the sums of
+    c' s (two parts), of z' and of the weights 2^-23 of the largest partial sum at each of their
+    n / 16 steps."""
+    B, D, T = 32 if N == 80 else 64, 32, 16384
+    c, st = make_cache(17, B, 2, D, 2, T, R=32)
+    c.view("k_codes").zero_()
+    for n in ("k_scale", "k_zero", "k_res"):
+        c.view(n).zero_()
+    q, k, v = draft(1, c, 1, N)
+    none = torch.zeros(B, N, (N + 31) // 32, dtype=torch.int32, device="cuda")
+    out = c.tree_decode(q, k, v, none, 1.0).cpu().double()
+    for b in (0, B // 2 - 1, B - 1):
+        _, V = tokens(c, b, c.n_q, c.r)
+        z = torch.zeros_like(V)
+        z[:, : c.n_q] = (c.view("v_zero")[b].double() + 1.5 * c.view("v_scale")[b].double())[:, : c.n_q].cpu()
+        ref = V.mean(1)
+        steps = T / 16 * 2.0 ** -23
+        tol = (2.0 ** -11 * ref.abs() + 2.0 ** -17 * (V - z).abs().mean(1)
+               + steps * ref.abs() + 2 * steps * (V - z).cumsum(1).abs().amax(1) / T
+               + steps * z.cumsum(1).abs().amax(1) / T)
+        assert ((out[b] - ref[:, None]).abs() <= tol[:, None]).all()
+
+
 def test_tree_refused_sequences_give_nan():
     lens = [40, 300, 200]
     c, st = make_cache(8, 3, 2, 64, 2, lens, store="paged")
