@@ -151,9 +151,12 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& a, const T* in, T* out
 }
 
 // Block: tokens blockIdx.x * TB ..; gridDim.y blocks share their rows.  The table of
-// the tokens' cosines and sines is made once and used by all heads.  What bounds it:
-// DRAM, after the instructions of the turn (one warp instruction for every 5 bytes
-// at first, for every 12 with pairs in one lane).
+// the tokens' cosines and sines is made once and used by all heads.
+// Bound by issue (64 % of the slots) and DRAM together: 4 x 8191 tokens of 48 heads
+// (32 + 2 x 8, D 128, binary16, three axes) take 183 us, 4.4 TB/s of a copy's 6.5.  Both
+// halves of a pair in one lane took it from 288 us (a shuffle for each value), four
+// rows' loads in flight from 345.  A decode step's 16 tokens take 5 us, which is a
+// launch, the binary64 angles and one round of loads.
 template <int D, typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int TB) {
   extern __shared__ float4 cs[];  // [TB][rot / 2] (cosine, sine)

@@ -5,7 +5,8 @@
 // (row = query head within the group * N + node), so the cache is read once
 // for all of them.  RB rows make a row block.  A (sequence, KV head, row
 // block) is a group; its tiles are those of the sequence's quantized tokens,
-// then of its window, then of the drafted tokens, TT tokens each.  All groups'
+// then of its raw ones (the window and, straight behind it, the drafted
+// tokens), TT tokens each.  All groups'
 // tiles, end to end, are cut into equal ranges of W, one per CTA, whatever the
 // lengths are, so a ragged batch keeps all CTAs busy.  A group that falls into
 // one range is written out at once; of any other, each CTA leaves a partial

@@ -11,7 +11,9 @@ constexpr int kMergeThreads = 32 * kMergeRows;
 // Block (group, 8 rows of it), a warp for each row: of the segments' partials (m_s,
 // l_s, acc_s), M = max m_s and weights 2^(m_s - M) first, then
 // out = sum 2^(m_s - M) acc_s / sum 2^(m_s - M) l_s with all loads independent of each
-// other (a long cache of few heads has a partial of every CTA).  A row that
+// other: bound by their latency (a long cache of few heads has a partial of every CTA;
+// one binary32 head of 20011 tokens, 444 partials, takes 32 us in all, 41 with each
+// partial weighed as it came).  A row that
 // attended to nothing (all l_s = 0) is 0.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, TreePlan p) {
@@ -135,9 +137,11 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 
 }  // namespace
 
-// The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all
-// fit.  Tensor cores: up to 64 rows a block, more in blocks of equal size (each
-// unpacks the cache again); two blocks of threads per SM.
+// The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all fit
+// (four blocks on an SM instead of three).  Tensor cores: up to 64 rows two blocks of
+// threads on an SM, more in row blocks of equal size up to 128 rows, one block on an SM
+// (both sides measured: kivi_tree_tc.cuh).  The shortest range is one tile: longer ones
+// leave SMs idle where a cache is short.
 static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
   const int rows = gq * N;
   TreePlan p;

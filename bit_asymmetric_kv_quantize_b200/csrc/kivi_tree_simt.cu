@@ -7,7 +7,15 @@
 // One pass, tile by tile: running maximum and sum of each row, accumulators
 // rescaled when the maximum rises.  A tile of 32 tokens is turned into
 // numbers in shared memory once for all rows of the block; scores and
-// accumulators are register tiles of a matrix product.
+// accumulators are register tiles of a matrix product, in packed binary32 pairs.
+// There is no binary32 matrix instruction, and binary16 operands would lose what a
+// binary32 cache is kept for.
+// What bounds it: latency.  6 x 4 heads of up to 2999 tokens at 3 bits, 39 rows,
+// take 50 us; the arithmetic alone (39 rows in a block of 64) would take 11 us at 75
+// TFLOP/s, but a block has four warps, three
+// blocks an SM (216 registers a thread hold the tiles), and 32 % of the issue
+// slots are used: each waits for its tile's words (0.9 warps a scheduler's issue) and
+// for shared memory (0.8).
 #include <type_traits>
 
 #include "kivi_dequant.cuh"

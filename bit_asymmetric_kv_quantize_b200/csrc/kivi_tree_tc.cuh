@@ -47,15 +47,11 @@
 // is watched; one vote tells whether that held, and the tile where it did not raises
 // the references, rescales O^T in tensor memory and forms its weights again.
 //
-// Two blocks of threads share an SM, so that one computes while the other waits for
-// its matrix instructions or for tensor memory's store port (unpacking writes 128 KB
-// a tile, about 1000 cycles of it).  A block's eight warps walk through a tile
-// together; warp w has lanes 32 (w % 4) .. + 31 of tensor memory and half of the
-// columns.  For each tile:
+// A block's warps walk through a tile together; warp w has lanes 32 (w % 4) .. + 31
+// of tensor memory and a share of the columns.  For each tile:
 //   keys unpacked, and their zeros' products
 //   (a further warp issues the score products)
-//   the next tile's scales and zeros set out; weights; values unpacked, into the
-//   keys' place
+//   the next tile's scales and zeros set out; weights; values unpacked
 //   (it issues the value products)
 //   sums over the tile's tokens
 // One more warp issues the copies (cp.async.bulk of each tile's ranges into a ring).
@@ -64,6 +60,26 @@
 // the instruction cache.  Waits on copies and matrix instructions are bounded: one
 // that runs out marks the block dead, whose further waits return soon and whose
 // results are NaN.
+//
+// Two forms (PARTS: groups of four warps).  Up to 64 rows: two blocks of 8 workers on
+// an SM, so that one computes while the other waits for its matrix instructions or for
+// tensor memory's store port (unpacking writes 128 KB a tile, about 1000 cycles of
+// it); a block has 256 columns of tensor memory, values take the keys' place.  From 65
+// rows on: one block of 16 workers and up to 128 rows, which unpacks the cache once
+// where two row blocks would do it twice; the values have planes of their own and
+// are unpacked while the score products run.  Measured on 8 sequences x 32 heads of 4096
+// tokens at 2 bits, two blocks against one of 16 workers: 8 rows 119 and 174 us, 32
+// rows 139 and 185, 64 rows 180 and 217; 80 rows (2 x 48) 295 and 249, 128 rows (2 x 64)
+// 338 and 293, 160 rows (3 x 64, 2 x 80) 507 and 498.
+//
+// What bounds it: neither DRAM (5 to 15 % of its rate) nor the matrix instructions (8
+// to 26 % of their pipe), but the unpacking of codes into tensor memory and the
+// barriers between a tile's steps: half of the issue slots are used, most stalls are
+// waits at barriers (1.8 to 2.6 of the 8 to 9 warps a scheduler's issue waits for).
+// A 4096-token layer of 8 x 32 heads with 16 nodes takes 123 us (1.2 TB/s of the cache,
+// 70 TFLOP/s of the products), a 16384-token GQA layer of 16 x 8 heads, 96 rows,
+// 445 us (232 TFLOP/s), a paged batch of 24 x 8 heads to 6000 tokens at 4 bits, 244
+// rows, 502 us (185 TFLOP/s).
 #pragma once
 
 #include <type_traits>
