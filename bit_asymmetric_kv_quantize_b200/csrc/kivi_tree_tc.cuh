@@ -131,7 +131,9 @@ struct TcGeo {
   static constexpr int S_KSC = S_RAW + (RT * D * 2 > LZ ? RT * D * 2 : LZ);
                                                          // 4 groups x D x (hi, lo) halves
   static constexpr int S_VSC = S_KSC + 4 * D * 4;        // 2 x 4 groups x 128 x (hi, lo)
-  static constexpr int S_ZK = S_VSC + 2 * 4 * 128 * 4;   // [PARTS][4 groups][ROWS] float
+  // (a group's row is padded: a warp's stores of one token's groups meet other banks)
+  static constexpr int VLD = 272;
+  static constexpr int S_ZK = S_VSC + 2 * 4 * VLD * 2;   // [PARTS][4 groups][ROWS] float
   static constexpr int S_OFF = S_ZK + PARTS * 4 * ROWS * 4;  // [WARPS][16 rows]
   static constexpr int S_WMAX = S_OFF + WARPS * 16 * 4;  // [4 groups][ROWS]
   static constexpr int S_M = S_WMAX + 4 * ROWS * 4;      // [ROWS]
@@ -514,6 +516,50 @@ __device__ __forceinline__ void tc_unpack(uint32_t t_hi, const uint32_t* words, 
     tc_put16(t_hi + 8 * H * u, t_hi + 8 * H * u + 64, c, hi + 2 * H * u, lo + 2 * H * u);
     if constexpr (H == 2) {
       tc_codes16<BITS, 1>(w, c, k);
+      tc_put16(t_hi + 16 * u + 8, t_hi + 16 * u + 72, c, hi + 4 * u + 2, lo + 4 * u + 2);
+    }
+  }
+}
+// The same for a token's key words, which are adjacent: a part takes adjacent units and
+// loads their words in pieces as wide as they are aligned (word by word, the lanes' rows
+// of WK words would meet in a few banks).
+template <int D, int BITS, int PARTS>
+__device__ __forceinline__ void tc_unpack_keys(uint32_t t_hi, const uint32_t* row, const uint4* hi,
+                                               const uint4* lo, int part, const TcConst& k) {
+  using U = TcUnit<BITS>;
+  constexpr int H = U::kUnit / 16, n = D / U::kUnit, per = n < PARTS ? 1 : n / PARTS;
+  constexpr int NW = per * U::kUnitW;
+  if (part * per >= n) return;
+  uint32_t w[NW];
+  const uint32_t* src = row + part * NW;
+  if constexpr (NW % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NW; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src + i);
+      w[i] = x.x;
+      w[i + 1] = x.y;
+      w[i + 2] = x.z;
+      w[i + 3] = x.w;
+    }
+  } else if constexpr (NW % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < NW; i += 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src + i);
+      w[i] = x.x;
+      w[i + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = src[i];
+  }
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const int u = part * per + j;
+    uint32_t c[8];
+    tc_codes16<BITS, 0>(w + j * U::kUnitW, c, k);
+    tc_put16(t_hi + 8 * H * u, t_hi + 8 * H * u + 64, c, hi + 2 * H * u, lo + 2 * H * u);
+    if constexpr (H == 2) {
+      tc_codes16<BITS, 1>(w + j * U::kUnitW, c, k);
       tc_put16(t_hi + 16 * u + 8, t_hi + 16 * u + 72, c, hi + 4 * u + 2, lo + 4 * u + 2);
     }
   }
@@ -921,7 +967,7 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
       // scales and zeros of tile t's keys and values
       auto set_out = [&](int t) {
         __half* zv = zv0 + (t & 1) * 9 * Ge::ZLD;
-        __half* vsc = vsc0 + (t & 1) * 1024;
+        __half* vsc = vsc0 + (t & 1) * 4 * Ge::VLD;
         const bool raw = t >= g.t1s;
         const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
         if (!raw) {
@@ -947,7 +993,7 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
             const float s = have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[i]) : 0.f;
             tc_center<BITS>(s, have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[i]) : 0.f,
                             &zv[gr * Ge::ZLD + c], &zv[(5 + gr) * Ge::ZLD + c]);
-            tc_split(s, &vsc[gr * 256 + c], &vsc[gr * 256 + 128 + c]);
+            tc_split(s, &vsc[gr * Ge::VLD + c], &vsc[gr * Ge::VLD + 128 + c]);
           }
         }
       };
@@ -957,9 +1003,9 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
         if (t < g.t1s) {
           const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
           const __half* sc = ksc + q * 2 * D;
-          tc_unpack<BITS, PARTS>(t_q + Col::A, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK, 1,
-                                 reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part,
-                                 D / TcUnit<BITS>::kUnit, konst);
+          tc_unpack_keys<D, BITS, PARTS>(
+              t_q + Col::A, reinterpret_cast<const uint32_t*>(stg + Ge::O_KC + q * Ge::KC) + lane * WK,
+              reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + D), part, konst);
           // sum_d q_d z'_gd for rows 16 q .. (and 64 further on), over this part's channels
           // (the warp's q counts rows here); columns: the groups' high parts, their low parts
           const __half* zr = zh + n8 * Ge::ZLD + kq;
@@ -1041,7 +1087,7 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
           }
         } else if (q < NJ) {
           const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-          const __half* sc = vsc0 + (t & 1) * 1024 + q * 256;
+          const __half* sc = vsc0 + (t & 1) * 4 * Ge::VLD + q * Ge::VLD;
           tc_unpack<BITS, PARTS>(t_q + Col::V, reinterpret_cast<const uint32_t*>(stg + Ge::O_VC) + q * 32 + lane, D,
                                  reinterpret_cast<const uint4*>(sc), reinterpret_cast<const uint4*>(sc + 128), part,
                                  128 / TcUnit<BITS>::kUnit, konst);
