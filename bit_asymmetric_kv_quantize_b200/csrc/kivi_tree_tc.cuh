@@ -459,19 +459,24 @@ __device__ __forceinline__ void tc_codes16(const uint32_t* w, uint32_t (&c)[8], 
     c[7] = tc_pair<BITS, 8 * HALF + 7>(w, k);
   }
 }
-// Half of s in two binary16 parts: its leading 7 bits, and the rest.
-__device__ __forceinline__ void tc_split(float s, __half* hi, __half* lo) {
-  s *= 0.5f;
-  const float h = __uint_as_float(__float_as_uint(s) & 0xFFFE0000u);
-  *hi = __float2half_rn(h);
-  *lo = __float2half_rn(s - __half2float(*hi));
-}
-// z' = z + s * center, the codes' center, in two binary16 parts.
+// Two scales, halved, in two binary16 parts each (the leading 7 bits, and the rest), and
+// their z' = z + s * center in two parts: operand pairs at c of four rows.
 template <int BITS>
-__device__ __forceinline__ void tc_center(float s, float z, __half* hi, __half* lo) {
-  const float x = fmaf(s, 0.5f * ((1 << BITS) - 1), z);
-  *hi = __float2half_rn(x);
-  *lo = __float2half_rn(x - __half2float(*hi));
+__device__ __forceinline__ void tc_scales(float2 s, float2 z, __half* s_hi, __half* s_lo,
+                                          __half* z_hi, __half* z_lo) {
+  constexpr float kCenter = 0.5f * ((1 << BITS) - 1);
+  const float2 x = make_float2(fmaf(s.x, kCenter, z.x), fmaf(s.y, kCenter, z.y));
+  const __half2 zh = __floats2half2_rn(x.x, x.y);
+  const float2 zf = __half22float2(zh);
+  *reinterpret_cast<__half2*>(z_hi) = zh;
+  *reinterpret_cast<__half2*>(z_lo) = __floats2half2_rn(x.x - zf.x, x.y - zf.y);
+  s.x *= 0.5f;
+  s.y *= 0.5f;
+  const __half2 sh = __floats2half2_rn(__uint_as_float(__float_as_uint(s.x) & 0xFFFE0000u),
+                                       __uint_as_float(__float_as_uint(s.y) & 0xFFFE0000u));
+  const float2 sf = __half22float2(sh);
+  *reinterpret_cast<__half2*>(s_hi) = sh;
+  *reinterpret_cast<__half2*>(s_lo) = __floats2half2_rn(s.x - sf.x, s.y - sf.y);
 }
 // 16 codes times their scales (8 pairs of s_hi and of s_lo from shared memory, one
 // address for the whole warp) into the two planes.
@@ -964,36 +969,38 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
       }
       tc_fence_smem();
 
-      // scales and zeros of tile t's keys and values
+      // scales and zeros of tile t's keys (2 D pairs of channels, of 4 groups) and values
+      // (64 NJ pairs of tokens)
       auto set_out = [&](int t) {
         __half* zv = zv0 + (t & 1) * 9 * Ge::ZLD;
         __half* vsc = vsc0 + (t & 1) * 4 * Ge::VLD;
         const bool raw = t >= g.t1s;
         const unsigned char* stg = sm + Ge::S_RING + (st0 + t - g.t0) % Ge::NST * Ge::STAGE;
-        if (!raw) {
-          tc_wait(bar(TcBar::raw + (st0 + t - g.t0) % Ge::NST), (st0 + t - g.t0) / Ge::NST, dead);
-#pragma unroll
-          for (int j = 0; j < (4 * D + WORKERS - 1) / WORKERS; ++j) {
-            const int i = tid + WORKERS * j, gr = i / D, c = tc_pos<E>(i % D);
-            if (i < 4 * D) {
-              const float s = to_f32(reinterpret_cast<const M*>(stg + Ge::O_KS)[i]);
-              tc_center<BITS>(s, to_f32(reinterpret_cast<const M*>(stg + Ge::O_KZ)[i]),
-                              &zh[gr * Ge::ZLD + c], &zh[(4 + gr) * Ge::ZLD + c]);
-              tc_split(s, &ksc[gr * 2 * D + c], &ksc[gr * 2 * D + D + c]);
-            }
-          }
-        }
+        if (!raw) tc_wait(bar(TcBar::raw + (st0 + t - g.t0) % Ge::NST), (st0 + t - g.t0) / Ge::NST, dead);
         const long long left = g.n_q - (long long)t * kTcTile;
 #pragma unroll
-        for (int j = 0; j < (128 * NJ + WORKERS - 1) / WORKERS; ++j) {
-          const int i = tid + WORKERS * j, tok = i / NJ, gr = i % NJ, c = tc_pos<E>(tok);
-          if (i < 128 * NJ) {
+        for (int j = 0; j < (4 * D + WORKERS - 1) / WORKERS; ++j) {
+          const int i = tid + WORKERS * j;
+          if (i < 2 * D) {
+            const int gr = i / (D / 2), p = i % (D / 2);
+            const int c = 2 * p, d = p / (E / 2) * E + p % (E / 2);  // the pair (d, d + E / 2)
+            const M* sp = reinterpret_cast<const M*>(stg + Ge::O_KS) + gr * D + d;
+            const M* zp = reinterpret_cast<const M*>(stg + Ge::O_KZ) + gr * D + d;
+            if (!raw)
+              tc_scales<BITS>(make_float2(to_f32(sp[0]), to_f32(sp[E / 2])),
+                              make_float2(to_f32(zp[0]), to_f32(zp[E / 2])), &ksc[gr * 2 * D + c],
+                              &ksc[gr * 2 * D + D + c], &zh[gr * Ge::ZLD + c], &zh[(4 + gr) * Ge::ZLD + c]);
+          } else if (i < 4 * D) {
+            const int m = i - 2 * D, gr = m % NJ, p = m / NJ;
+            const int c = 2 * p, tok = p / (E / 2) * E + p % (E / 2);
+            const M* sp = reinterpret_cast<const M*>(stg + Ge::O_VS) + tok * NJ + gr;
+            const M* zp = reinterpret_cast<const M*>(stg + Ge::O_VZ) + tok * NJ + gr;
             // tokens that do not exist: 0 (their weight 0 times NaN would not be)
-            const bool have = !raw && tok < left;
-            const float s = have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VS)[i]) : 0.f;
-            tc_center<BITS>(s, have ? to_f32(reinterpret_cast<const M*>(stg + Ge::O_VZ)[i]) : 0.f,
-                            &zv[gr * Ge::ZLD + c], &zv[(5 + gr) * Ge::ZLD + c]);
-            tc_split(s, &vsc[gr * Ge::VLD + c], &vsc[gr * Ge::VLD + 128 + c]);
+            const bool h0 = !raw && tok < left, h1 = !raw && tok + E / 2 < left;
+            tc_scales<BITS>(make_float2(h0 ? to_f32(sp[0]) : 0.f, h1 ? to_f32(sp[E / 2 * NJ]) : 0.f),
+                            make_float2(h0 ? to_f32(zp[0]) : 0.f, h1 ? to_f32(zp[E / 2 * NJ]) : 0.f),
+                            &vsc[gr * Ge::VLD + c], &vsc[gr * Ge::VLD + 128 + c], &zv[gr * Ge::ZLD + c],
+                            &zv[(5 + gr) * Ge::ZLD + c]);
           }
         }
       };
