@@ -505,8 +505,8 @@ KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq
  * is infinite or NaN; a node that attends to nothing (an empty cache and an
  * empty mask) gets 0.  The cache may be empty.  It is only read: see
  * kivi_ragged_tree_commit.
- * Any element alignment of q, k, v and out is accepted.  Two launches,
- * capturable in a CUDA graph.
+ * Any element alignment of q, k, v and out is accepted; out overlaps no input.
+ * Two launches, capturable in a CUDA graph.
  * Sums, the softmax and its statistics are binary32 for both dtypes; with
  * fp16 inputs the stored codes' products and the weights p_t pass through
  * binary16 matrix operands as the kernel's comments say.
@@ -596,7 +596,7 @@ typedef struct {
  * positions keep their angles, to about |a| 2^-51).  q_weight, k_weight: device [D] or NULL.
  * q: device, [B][Hq][N][D]; k, v: device, [B][Hkv][N][D] -- what the tree
  * calls and kivi_quantize_prefill take, and with N = 1 what the decode calls
- * take.  One launch.
+ * take.  The outputs overlap neither qkv nor each other.  One launch.
  * Errors: KIVI_ERR_ARG (null pointer; qkv, q, k or v not 16-byte aligned;
  * stride below a row or no multiple of 16 bytes; sizes below 1; sections that
  * do not sum to rot / 2; eps negative), KIVI_ERR_UNSUPPORTED (D, rot, axes,

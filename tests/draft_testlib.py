@@ -8,7 +8,8 @@ Tolerances (derived, not fitted).  With u = 2^-24 (half a step of binary32, rela
     e_s = scale * sum_d |q_d K_d| * (D + 8) u: D additions, and a few roundings for the product,
     the scale (folded with log2 e into q) and K = c s + z.  On matrix operands of binary16 a
     stored key c s + z is carried as c s_hi + c s_lo + z with a relative error of c s below
-    2^-17 (s_hi has 7 bits, s_lo 11 more, their products are exact or rounded at 2^-18), so e_s
+    2^-17 (s_hi has 7 bits, s_lo 11 more, their products are exact or rounded at 2^-18; codes about
+    their center are smaller, and their zeros, two binary16 parts, are kept to 2^-22), so e_s
     grows by scale * sum_d |q_d| (|K_d| + |z_d|) 2^-17 <= scale * sum_d |q_d| 3 max|K_d| 2^-17.
   - a weight exp(s - max) is then off by a factor within exp(+-2 e_s) (its own score's error and the
     maximum's) times 1 + 8u (exp2 and its argument, |s - max| <= 128 before it underflows adds

@@ -334,6 +334,25 @@ def test_tree_on_another_stream():
     assert torch.equal(got, want)
 
 
+def test_tree_calls_at_once_on_two_streams():
+    """Two caches, trees of both block forms under way together: neither result changes."""
+    work = []
+    for seed, N in ((31, 20), (32, 90), (33, 5)):
+        c, st = make_cache(seed, 4, 8, 32, 2, 3000)
+        q, k, v = draft(seed, c, 1, N)
+        m = random_tree(seed, 4, N)
+        work.append((c, st, q, k, v, m, tree(c, st, q, k, v, m, 0.2), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[] for _ in work]
+    for _ in range(10):
+        for (c, st, q, k, v, m, _, s), g in zip(work, got):
+            with torch.cuda.stream(s):
+                g.append(tree(c, st, q, k, v, m, 0.2))
+    torch.cuda.synchronize()
+    for w, g in zip(work, got):
+        assert all(torch.equal(x, w[6]) for x in g)
+
+
 def test_tree_of_one_node_is_append_and_decode():
     """A chain of one node is the next token: the result of kivi_append_decode, within both bars."""
     c, st = make_cache(14, 2, 4, 128, 2, 600, R=128)
