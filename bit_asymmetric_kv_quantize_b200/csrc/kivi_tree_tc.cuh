@@ -29,6 +29,8 @@
 // zero.  With c itself all addends of a sum over tokens are positive, and the cuts
 // add up (the results of a 16384-token GQA layer were off by 1.3e-4 on average, as
 // much as a binary16 output's rounding); the sums of c' stay near zero.
+// A scale below binary16's normal range keeps fewer bits: c' s is off by at most
+// 15 * 2^-25 < 2^-21 there.
 // s is halved (a binary16 s_hi of a 1-bit group of the widest range would
 // overflow), so raw keys and values are halved too and the results doubled in
 // binary32.  The weights p are rounded to binary16 once, relative 2^-12 on
