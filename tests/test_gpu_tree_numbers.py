@@ -1,0 +1,200 @@
+"""Numbers of the attention of drafted tokens: references that rise in the middle of a range, scores
+far apart, weights far below the largest, the largest tree.
+Against 64-bit sums over the bytes that the cache holds (draft_testlib.tokens)."""
+import math
+
+import pytest
+import torch
+
+import bit_asymmetric_kv_quantize_b200 as kivi
+from draft_testlib import U, sees, tokens
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+
+
+def weigh(c, b, h, gq, q, k, v, mask, scale):
+    """Row h of sequence b in 64 bits: (out, sum p |V|, scores, l, max |V|), p = exp(s - max) / l."""
+    K, V = tokens(c, b, c.n_q, c.r)
+    K = torch.cat([K, k[b].cpu().double()], 1)[h // gq]
+    V = torch.cat([V, v[b].cpu().double()], 1)[h // gq]
+    N = q.shape[2]
+    m = torch.cat([torch.ones(N, c.n_q + c.r, dtype=torch.bool), sees(mask[b:b + 1], N)[0]], 1)
+    s = torch.where(m, q[b, h].cpu().double() @ K.T * scale, -math.inf)
+    p = torch.exp(s - s.amax(1, keepdim=True))
+    l = p.sum(1, keepdim=True)
+    p = p / l
+    return p @ V, p @ V.abs(), s, l, V.abs().max()
+
+
+def split_of(c, rows, N):
+    """Tiles of a CTA's range in the tensor-core kernel, for one row block and equal lengths."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = -(-c.n_q // 128) + -(-(c.r + N) // 128)
+    return -(-c.B * c.Hkv * tiles // (2 * sms if rows <= 64 else sms))
+
+
+@pytest.mark.parametrize("heights", [(12,), (12, 24)])
+@pytest.mark.parametrize("N", [9, 40, 80])
+def test_tree_reference_rises_within_a_range(N, heights):
+    """Tokens 12 (and 24) log2 units above the many others stand in known tiles of every range, so that the
+    sums over its first tiles are rescaled there, for the even rows only.  The lower tokens stay a
+    tenth of the sum: for one height, one token against some hundred of weight 2^-12; for two, 64 tokens
+    at 12 in one tile and one token at 24 two tiles on, 2^-12 each of it (1.6 % together).
+    Bound: as in tree_reference of draft_testlib, where a key is carried to 2^-17 of its group's range
+    and 2^-22 of its middle (3 * 2^-17 max|K| is above both)."""
+    B, Hkv, D, T = 32, 2, 32, 2990
+    g = torch.Generator().manual_seed(N)
+    c = kivi.KiviCache(B, Hkv, D, 2, 3200, R=32)
+    K = torch.zeros(B, Hkv, T, D)
+    K[..., 0] = torch.rand(B, Hkv, T, generator=g) - 0.5
+    V = 0.25 * torch.randn(B, Hkv, T, D, generator=g) + 1.0
+    if len(heights) == 1:
+        high = {128 * t + 37: heights[0] for t in range(1, 23, 3)}
+    else:
+        high = {128 * t + 2 * i: heights[0] for t in range(0, 23, 4) for i in range(64)}
+        high |= {128 * t + 37: heights[1] for t in range(2, 23, 4)}
+    at = torch.tensor(list(high))
+    K[:, :, at, 1] = torch.tensor(list(high.values()), dtype=torch.float)
+    V[:, :, at] = -1.0 if len(heights) == 1 else torch.where(K[:, :, at, 1:2] == heights[1], -1.0, 3.0)
+    c.prefill(K.half().cuda(), V.half().cuda())
+    assert split_of(c, N, N) >= 4
+    q = torch.zeros(B, Hkv, N, D)
+    q[..., 0] = 1.0
+    q[:, :, ::2, 1] = math.log(2)
+    q = q.half().cuda()
+    k, v = (0.3 * torch.randn(B, Hkv, N, D, generator=g).half().cuda() for _ in "kv")
+    mask = kivi.tree_mask((torch.arange(N) - 2).clamp(min=-1).expand(B, N)).cuda()
+    got = c.tree_decode(q, k, v, mask, 1.0).cpu().double()
+    for b, h in ((0, 0), (7, 1), (13, 0), (14, 1), (22, 0), (31, 1)):
+        ref, A, s, l, vmax = weigh(c, b, h, 1, q, k, v, mask, 1.0)
+        n = s.shape[1]
+        kmax = tokens(c, b, c.n_q, c.r)[0][h].abs().amax(0).maximum(k[b, h].cpu().double().abs().amax(0))
+        e_s = (q[b, h].cpu().double().abs() @ kmax[:, None]) * (3 * 2.0 ** -17 + (D + 8) * U)
+        eps = 2 * e_s + 140 * U + n * U + 2.0 ** -11 + 2.0 ** -17
+        tol = 2 * eps * A + 2.0 ** -11 * ref.abs() + n * 2.0 ** -29 / l * vmax + 2.0 ** -17 * vmax
+        # the sums over a range grow by steps of 16 tokens, each cut off by 2^-23 of them
+        tol = tol + 2 * n / 16 * 2.0 ** -23 * A
+        assert (tol <= 0.005 * A).all()  # a tenth, or 1.6 %, of the sum would not pass
+        assert ((got[b, h] - ref).abs() <= tol).all(), (b, h)
+
+
+@pytest.mark.parametrize("scale", [30.0, -30.0, 3.0])
+@pytest.mark.parametrize("N", [7, 70])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_scores_far_apart(dtype, N, scale):
+    """Scores up to 700 log2 units apart that are exact up to binary32: the keys of a group are equal (its
+    scale is 0 and its zero the key, a binary16 number), queries are powers of two in one channel.
+    So a score is off by the roundings of its product with the scale, of that product with log2 e and of
+    the difference, 6 half steps of the largest; the rest is a weight's and the output's rounding."""
+    B, Hkv, D, T = 2, 3, 64, 500
+    g = torch.Generator().manual_seed(N)
+    c = kivi.KiviCache(B, Hkv, D, 4, 1024, R=32, dtype=dtype)
+    level = torch.randint(-256, 257, (B, Hkv, T // 32 + 1), generator=g) / 64.0
+    K = torch.zeros(B, Hkv, T, D)
+    K[..., 5] = level.repeat_interleave(32, 2)[:, :, :T]
+    V = torch.randn(B, Hkv, T, D, generator=g)
+    c.prefill(K.to(dtype).cuda(), V.to(dtype).cuda())
+    q = torch.zeros(B, Hkv, N, D)
+    q[..., 5] = (2.0 ** (torch.arange(N) % 5 - 3)) * (1 - 2 * (torch.arange(N) % 2))
+    k = torch.zeros(B, Hkv, N, D)
+    k[..., 5] = torch.randint(-256, 257, (B, Hkv, N), generator=g) / 64.0
+    v = torch.randn(B, Hkv, N, D, generator=g)
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    mask = kivi.tree_mask((torch.arange(N) - 3).clamp(min=-1).expand(B, N)).cuda()
+    got = c.tree_decode(q, k, v, mask, scale).cpu().double()
+    f16 = dtype == torch.float16
+    for b in range(B):
+        for h in range(Hkv):
+            ref, A, s, l, vmax = weigh(c, b, h, 1, q, k, v, mask, scale)
+            n = s.shape[1]
+            e_s = torch.where(s > -math.inf, s.abs(), 0.0).amax(1, keepdim=True) * 6 * U
+            eps = 2 * e_s + 140 * U + n * U + ((2.0 ** -11 + 2.0 ** -17) if f16 else 0.0)
+            tol = 2 * eps * A + HALF[dtype] * ref.abs() + 2.0 ** -25 * HALF[dtype]
+            if f16:
+                tol = tol + n * 2.0 ** -29 / l * vmax + 2.0 ** -25 + 2.0 ** -17 * vmax
+            assert (tol <= (0.005 if f16 else 0.0005) * A + 2.0 ** -14).all()
+            assert ((got[b, h] - ref).abs() <= tol).all(), (b, h)
+
+
+@pytest.mark.parametrize("gap", [14.0, 17.3, 20.5, 23.4, 25.6, 27.5, 28.8])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_small_weights_at_any_gap(dtype, gap):
+    """Thousands of tokens `gap` log2 units below one: with binary16 operands each keeps its weight to
+    2^-11 of itself and 2^-29 of the largest, as include/kivi.h states, whatever the gap is."""
+    B, Hkv, D, T = 8, 8, 32, 4096
+    c = kivi.KiviCache(B, Hkv, D, 2, T + 32, R=32, dtype=dtype)
+    K = torch.zeros(B, Hkv, T, D, device="cuda", dtype=dtype)
+    K[:, :, 0] = gap * math.log(2) / D
+    V = torch.full_like(K, 64.0)
+    V[:, :, 0] = 0
+    c.prefill(K, V)
+    q = torch.ones(B, Hkv, 3, D, device="cuda", dtype=dtype)
+    none = torch.zeros(B, 3, 1, dtype=torch.int32, device="cuda")
+    got = c.tree_decode(q, q, q, none, 1.0).cpu().double()
+    f16 = dtype == torch.float16
+    for b, h in ((0, 0), (3, 7), (7, 4)):
+        ref, A, s, l, vmax = weigh(c, b, h, 1, q, q, q, none, 1.0)
+        e_s = gap * ((3 * 2.0 ** -17 if f16 else 0.0) + (D + 8) * U)
+        eps = 2 * e_s + (140 + T) * U + (2.0 ** -11 if f16 else 0.0)
+        tol = 2 * eps * A + HALF[dtype] * ref.abs()
+        if f16:
+            tol = tol + T * 2.0 ** -29 / l * vmax + 2 * T / 16 * 2.0 ** -23 * A
+        assert ((got[b, h] - ref).abs() <= tol).all(), (b, h)
+
+
+def words(see):
+    """int32 mask words of bool [B][N][N]."""
+    B, N, _ = see.shape
+    w = torch.zeros(B, N, -(-N // 32) * 32, dtype=torch.int64)
+    w[..., :N] = see
+    w = (w.view(B, N, -1, 32) << torch.arange(32)).sum(-1)
+    return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32).cuda()
+
+
+# ---- largest tree, first call in a capture ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_of_the_largest_size(dtype):
+    """256 nodes of 64 query heads to a KV head: 16384 rows, each against its own reference."""
+    B, Hkv, D, T, gq, N = 1, 1, 32, 300, 64, 256
+    g = torch.Generator().manual_seed(1)
+    c = kivi.KiviCache(B, Hkv, D, 2, 512, R=32, dtype=dtype)
+    c.prefill(*(torch.randn(B, Hkv, T, D, generator=g).to(dtype).cuda() for _ in "kv"))
+    q = torch.randn(B, gq, N, D, generator=g).to(dtype).cuda()
+    k, v = (torch.randn(B, Hkv, N, D, generator=g).to(dtype).cuda() for _ in "kv")
+    mask = words(torch.rand(B, N, N, generator=g) < 0.3)
+    got = c.tree_decode(q, k, v, mask, 0.2).cpu().double()
+    f16 = dtype == torch.float16
+    kmax = torch.cat([tokens(c, 0, c.n_q, c.r)[0][0], k[0, 0].cpu().double()]).abs().amax(0)
+    for h in (0, 1, 31, 63):
+        ref, A, s, l, vmax = weigh(c, 0, h, gq, q, k, v, mask, 0.2)
+        n = s.shape[1]
+        e_s = 0.2 * (q[0, h].cpu().double().abs() @ kmax[:, None]) * ((D + 8) * U + (3 * 2.0 ** -17 if f16 else 0.0))
+        eps = 2 * e_s + 140 * U + n * U + ((2.0 ** -11 + 2.0 ** -17) if f16 else 0.0)
+        tol = 2 * eps * A + HALF[dtype] * ref.abs() + 2.0 ** -25 * HALF[dtype]
+        if f16:
+            tol = tol + n * 2.0 ** -29 / l * vmax + 2.0 ** -25 + 2.0 ** -17 * vmax
+        assert ((got[0, h] - ref).abs() <= tol).all(), h
+
+
+def test_tree_first_call_of_a_cache_in_a_capture():
+    """The workspace made under capture serves the graph and eager calls after it."""
+    c = kivi.KiviCache(1, 2, 64, 2, 2048, R=64)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c.prefill(*(torch.randn(1, 2, 1500, 64, generator=g, device="cuda").half() for _ in "kv"))
+    q, k, v = (torch.randn(1, 2, 6, 64, generator=g, device="cuda").half() for _ in "qkv")
+    mask = kivi.tree_mask((torch.arange(6) - 1)[None]).cuda()
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.tree_decode(q, k, v, mask, 0.125, out=out)
+    graph.replay()
+    eager = c.tree_decode(q, k, v, mask, 0.125)
+    graph.replay()
+    del graph
+    again = c.tree_decode(q, k, v, mask, 0.125)
+    assert torch.equal(out, eager) and torch.equal(out, again)
