@@ -14,7 +14,9 @@ constexpr int kMergeThreads = 32 * kMergeRows;
 // other: bound by their latency (a long cache of few heads has a partial of every CTA;
 // one binary32 head of 20011 tokens, 444 partials, takes 32 us in all, 41 with each
 // partial weighed as it came).  A row that
-// attended to nothing (all l_s = 0) is 0.
+// attended to nothing (all l_s = 0) is 0.  An infinite or NaN accumulator keeps its part
+// where the weight of its segment comes to 0: what a row attends to may not vanish with
+// the way in which the work is split.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, TreePlan p) {
   const long long gpb = (long long)a.Hkv * p.n_rb;
@@ -88,12 +90,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   for (int s = lane / LPR; s < n; s += SPL) {
     const float e = w[s];
     const float4 v = __ldcg(reinterpret_cast<const float4*>(at(s) + 2 * p.rb + (long long)row * D + d));
-    if (e != 0.f) {
-      num.x = fmaf(e, v.x, num.x);
-      num.y = fmaf(e, v.y, num.y);
-      num.z = fmaf(e, v.z, num.z);
-      num.w = fmaf(e, v.w, num.w);
-    }
+    auto join = [e](float x, float sum) {
+      return e != 0.f || isfinite(x) ? fmaf(e, x, sum) : sum + x;
+    };
+    num.x = join(v.x, num.x);
+    num.y = join(v.y, num.y);
+    num.z = join(v.z, num.z);
+    num.w = join(v.w, num.w);
   }
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1) {
@@ -104,11 +107,11 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   }
   if (lane >= LPR) return;
   T* o = static_cast<T*>(a.out) + ((b * a.Hkv + h) * (long long)rows + (long long)rb * p.rb + row) * D + d;
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  o[0] = from_f32<T>(num.x * inv);
-  o[1] = from_f32<T>(num.y * inv);
-  o[2] = from_f32<T>(num.z * inv);
-  o[3] = from_f32<T>(num.w * inv);
+  const float inv = 1.f / den;
+  o[0] = from_f32<T>(den == 0.f ? 0.f : num.x * inv);
+  o[1] = from_f32<T>(den == 0.f ? 0.f : num.y * inv);
+  o[2] = from_f32<T>(den == 0.f ? 0.f : num.z * inv);
+  o[3] = from_f32<T>(den == 0.f ? 0.f : num.w * inv);
 }
 
 template <int D, typename T>

@@ -16,8 +16,6 @@
 // blocks an SM (216 registers a thread hold the tiles), and 32 % of the issue
 // slots are used: each waits for its tile's words (0.9 warps a scheduler's issue) and
 // for shared memory (0.8).
-#include <type_traits>
-
 #include "kivi_dequant.cuh"
 #include "kivi_tree.cuh"
 
@@ -65,6 +63,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) float sm[];
   __shared__ TreeAt s_at;
+  __shared__ int s_odd;  // the segment has infinite or NaN raw values
   const int tid = threadIdx.x;
   const long long W0 = blockIdx.x;
   if (tid < 32) {
@@ -100,6 +99,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     const long long tq = (q.n_q + kTT - 1) / kTT;
 
     __syncthreads();  // the segment before has read its last tile
+    if (tid == 0) s_odd = 0;
     const float* qp = static_cast<const float*>(a.q) + (unit * rows + row0) * D;
     for (int i = tid; i < RB * D; i += kThreads)
       sm[SM::Q + i] = row0 + i / D < rows ? qp[i] * a.qscale : 0.f;
@@ -170,7 +170,13 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             sm[SM::K + (tk + i) * SM::LD + ch + e] = kp ? kp[e] : 0.f;
-            sm[SM::V + (tk + i) * D + ch + e] = vp ? vp[e] : 0.f;
+            // an infinity or a NaN is left out: it joins at the segment's end, for the rows
+            // that attend to it (0 times it would spoil the others, and a later rescaling
+            // by 0 itself)
+            const float x = vp ? vp[e] : 0.f;
+            const bool fin = isfinite(x);
+            if (!fin) s_odd = 1;
+            sm[SM::V + (tk + i) * D + ch + e] = fin ? x : 0.f;
           }
         }
       }
@@ -254,43 +260,34 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
 #pragma unroll
         for (int j = 0; j < OC; ++j) acc[i][j] *= f;
       }
-      auto add = [&](auto guard) {
 #pragma unroll 4
-        for (int tk2 = 0; tk2 < kTT; ++tk2) {
-          float pv[OR], vv[OC];
+      for (int tk2 = 0; tk2 < kTT; ++tk2) {
+        float pv[OR], vv[OC];
 #pragma unroll
-          for (int i = 0; i < OR; i += 4)
-            *reinterpret_cast<float4*>(pv + i) =
-                *reinterpret_cast<const float4*>(sm + SM::P + tk2 * SM::PL + or0 + i);
+        for (int i = 0; i < OR; i += 4)
+          *reinterpret_cast<float4*>(pv + i) =
+              *reinterpret_cast<const float4*>(sm + SM::P + tk2 * SM::PL + or0 + i);
 #pragma unroll
-          for (int g = 0; g < ON; ++g)
+        for (int g = 0; g < ON; ++g)
 #pragma unroll
-            for (int e = 0; e < OV; ++e)
-              vv[g * OV + e] = sm[SM::V + tk2 * D + g * (D / ON) + oc0 + e];
+          for (int e = 0; e < OV; ++e)
+            vv[g * OV + e] = sm[SM::V + tk2 * D + g * (D / ON) + oc0 + e];
 #pragma unroll
-          for (int i = 0; i < OR; ++i) {
-            // a drafted token that the node does not see has weight 0 whatever its
-            // values are: 0 * inf must not reach the sum
-            if (decltype(guard)::value && pv[i] == 0.f) continue;
-            if constexpr (OC % 2 == 0) {
+        for (int i = 0; i < OR; ++i) {
+          if constexpr (OC % 2 == 0) {
 #pragma unroll
-              for (int j = 0; j < OC; j += 2) {
-                const float2 r = fma2(make_float2(pv[i], pv[i]), make_float2(vv[j], vv[j + 1]),
-                                      make_float2(acc[i][j], acc[i][j + 1]));
-                acc[i][j] = r.x;
-                acc[i][j + 1] = r.y;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < OC; ++j) acc[i][j] = fmaf(pv[i], vv[j], acc[i][j]);
+            for (int j = 0; j < OC; j += 2) {
+              const float2 r = fma2(make_float2(pv[i], pv[i]), make_float2(vv[j], vv[j + 1]),
+                                    make_float2(acc[i][j], acc[i][j + 1]));
+              acc[i][j] = r.x;
+              acc[i][j + 1] = r.y;
             }
+          } else {
+#pragma unroll
+            for (int j = 0; j < OC; ++j) acc[i][j] = fmaf(pv[i], vv[j], acc[i][j]);
           }
         }
-      };
-      if (raw)
-        add(std::true_type{});
-      else
-        add(std::false_type{});
+      }
     }
 
     // ---- the segment's end
@@ -311,8 +308,9 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
       }
     }
     __syncthreads();
+    float* dst;  // the block's rows of the output, or the accumulators of its partial
     if (whole) {
-      float* op = static_cast<float*>(a.out) + (unit * rows + row0) * D;
+      dst = static_cast<float*>(a.out) + (unit * rows + row0) * D;
 #pragma unroll
       for (int i = 0; i < OR; ++i) {
         if (row0 + or0 + i >= rows) continue;
@@ -322,19 +320,38 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
         for (int g = 0; g < ON; ++g)
 #pragma unroll
           for (int e = 0; e < OV; ++e)
-            op[(or0 + i) * D + g * (D / ON) + oc0 + e] =
+            dst[(or0 + i) * D + g * (D / ON) + oc0 + e] =
                 lr == 0.f ? 0.f : acc[i][g * OV + e] * inv;
       }
     } else {
       float* pp = a.part + (2 * W0 + (tile0 == 0)) * tree_part(p, D);
       for (int i = tid; i < 2 * RB; i += kThreads) pp[i] = sm[SM::P + i];
+      dst = pp + 2 * RB;
 #pragma unroll
       for (int i = 0; i < OR; ++i)
 #pragma unroll
         for (int g = 0; g < ON; ++g)
 #pragma unroll
           for (int e = 0; e < OV; ++e)
-            pp[2 * RB + (or0 + i) * D + g * (D / ON) + oc0 + e] = acc[i][g * OV + e];
+            dst[(or0 + i) * D + g * (D / ON) + oc0 + e] = acc[i][g * OV + e];
+    }
+    if (s_odd && !poison) {  // infinite or NaN raw values, of the tokens that a row attends to
+      __syncthreads();       // (added to what the block's threads just wrote)
+      const long long i1 = min((tile0 + nt - tq) * kTT, (long long)q.r + a.N);
+#pragma unroll 1
+      for (int i = tid; i < min(RB, rows - row0) * D; i += kThreads) {
+        const int row = i / D;
+        if (whole && sm[SM::P + 2 * row + 1] == 0.f) continue;  // no weight: stays 0
+        const uint32_t* mk = a.mask + (b * a.N + (row0 + row) % a.N) * mw;
+#pragma unroll 1
+        for (long long tok = max(tile0 - tq, 0LL) * kTT; tok < i1; ++tok) {
+          const int node = (int)(tok - q.r);
+          const float v =
+              node < 0 ? static_cast<const float*>(a.c.v_res)[(unit * a.c.R + tok) * D + i % D]
+                       : static_cast<const float*>(a.v)[(unit * a.N + node) * D + i % D];
+          if (!isfinite(v) && (node < 0 || ((mk[node / 32] >> (node % 32)) & 1u))) dst[i] += v;
+        }
+      }
     }
     x += nt;
     rem += nt;

@@ -502,9 +502,12 @@ KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq
  * j / 32; any set is taken (a tree's is the node and its ancestors; a node
  * may leave itself out).  Bits from N on are ignored.  A token that a node
  * does not attend to has no part in its result, even where its key or value
- * is infinite or NaN; a node that attends to nothing (an empty cache and an
- * empty mask) gets 0.  The cache may be empty.  It is only read: see
- * kivi_ragged_tree_commit.
+ * is infinite or NaN.  A value that is infinite or NaN makes its channel so
+ * for every node that attends to it, however small its weight is beside the
+ * largest.  A score of +infinity or NaN makes the node's result NaN; one of
+ * -infinity is a weight of 0, and a node without any other weight (an empty
+ * cache and an empty mask among them) gets 0.  The cache may be empty.  It is
+ * only read: see kivi_ragged_tree_commit.
  * Any element alignment of q, k, v and out is accepted; out overlaps no input.
  * Two launches, capturable in a CUDA graph.
  * Sums, the softmax and its statistics are binary32 for both dtypes; with

@@ -1,5 +1,5 @@
 """Numbers of the attention of drafted tokens: references that rise in the middle of a range, scores
-far apart, weights far below the largest, the largest tree.
+far apart, weights far below the largest, infinite and NaN values.
 Against 64-bit sums over the bytes that the cache holds (draft_testlib.tokens)."""
 import math
 
@@ -144,6 +144,9 @@ def test_tree_small_weights_at_any_gap(dtype, gap):
         assert ((got[b, h] - ref).abs() <= tol).all(), (b, h)
 
 
+# ---- infinite and NaN values and keys of tokens that a node attends to ---------------------------
+
+
 def words(see):
     """int32 mask words of bool [B][N][N]."""
     B, N, _ = see.shape
@@ -151,6 +154,87 @@ def words(see):
     w[..., :N] = see
     w = (w.view(B, N, -1, 32) << torch.arange(32)).sum(-1)
     return torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32).cuda()
+
+
+def same(x, value):
+    return torch.isnan(x) if math.isnan(value) else x == value
+
+
+@pytest.mark.parametrize("where", ["draft", "window"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("B,Hkv,T", [(16, 32, 40), (1, 1, 700), (1, 2, 130), (40, 8, 200)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_attended_values_that_are_not_finite(dtype, B, Hkv, T, value, where):
+    """A value that is infinite or NaN makes its channel so for every node that attends to it, whether
+    its weight is 2^-200 of the largest or not, and however the work is split; it has no part in
+    the other channels and nodes."""
+    D, N, R = 32, 40, 64
+    g = torch.Generator().manual_seed(T)
+    c = kivi.KiviCache(B, Hkv, D, 2, T // R * R + 2 * R, R=R, dtype=dtype)
+    K = torch.zeros(B, Hkv, T, D)
+    V = torch.randn(B, Hkv, T, D, generator=g)
+    r = (T - 1) % R + 1
+    q, k = torch.zeros(B, Hkv, N, D), torch.zeros(B, Hkv, N, D)
+    q[..., 0] = math.log(2)
+    K[:, :, : T - r, 0] = 200.0  # the store's tokens, where there are any: all other weights are 0
+    k[:, :, 33, 0] = 250.0  # and one late node, above them
+    v = torch.randn(B, Hkv, N, D, generator=g)
+    see = torch.zeros(B, N, N, dtype=torch.bool)
+    see[:, ::2, 2] = True
+    see[:, 1::4, 33] = True
+    see[:, 4, 33] = True
+    mask = words(see)
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    K, V = K.to(dtype).cuda(), V.to(dtype).cuda()
+    c.prefill(K, V)
+    clean = c.tree_decode(q, k, v, mask, 1.0)
+    assert torch.isfinite(clean).all()
+    if where == "draft":
+        v[:, :, 2, 1::3] = value
+        rows = see[0, :, 2].cuda()
+    else:
+        c.view("v_res")[:, :, min(3, r - 1), 1::3] = value
+        rows = torch.ones(N, dtype=torch.bool, device="cuda")
+    got = c.tree_decode(q, k, v, mask, 1.0)
+    assert same(got[:, :, rows][..., 1::3], value).all()
+    rest = torch.ones(D, dtype=torch.bool)
+    rest[1::3] = False
+    assert torch.equal(got[..., rest], clean[..., rest])
+    assert torch.equal(got[:, :, ~rows], clean[:, :, ~rows])
+
+
+@pytest.mark.parametrize("T", [0, 40, 700])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_attended_keys_that_are_infinite(dtype, T):
+    """A score of -inf is a weight of 0, and a node with no other gets 0; +inf and NaN give NaN.  The
+    other nodes keep their results."""
+    B, Hkv, D, N = 2, 2, 32, 40
+    c = kivi.KiviCache(B, Hkv, D, 2, 1024, R=64, dtype=dtype)
+    g = torch.Generator().manual_seed(T)
+    if T:
+        c.prefill(*(torch.randn(B, Hkv, T, D, generator=g).to(dtype).cuda() for _ in "kv"))
+    q, k, v = (torch.randn(B, Hkv, N, D, generator=g).to(dtype).cuda() for _ in "qkv")
+    q[..., 0] = 1.0
+    mask = words(torch.eye(N, dtype=torch.bool).expand(B, N, N))
+    none = torch.zeros_like(mask)
+    clean, alone = c.tree_decode(q, k, v, mask, 0.5), c.tree_decode(q, k, v, none, 0.5)
+    low, high, odd = (3, 35), (5, 36), (7, 39)
+    for n in low:
+        k[:, :, n, 0] = -math.inf
+    for n in high:
+        k[:, :, n, 0] = math.inf
+    for n in odd:
+        k[:, :, n, 0] = math.nan
+    got = c.tree_decode(q, k, v, mask, 0.5)
+    touched = torch.zeros(N, dtype=torch.bool)
+    touched[list(low + high + odd)] = True
+    assert torch.equal(got[:, :, ~touched], clean[:, :, ~touched])
+    assert torch.isnan(got[:, :, list(high + odd)]).all()
+    assert torch.equal(got[:, :, list(low)], alone[:, :, list(low)])
+    if not T:
+        assert (got[:, :, list(low)] == 0).all()
+        v[:, :, list(low)] = math.inf  # no weight is left: still 0
+        assert (c.tree_decode(q, k, v, mask, 0.5)[:, :, list(low)] == 0).all()
 
 
 # ---- largest tree, first call in a capture ---------------------------------------------------------
