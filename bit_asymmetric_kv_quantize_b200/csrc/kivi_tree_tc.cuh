@@ -21,8 +21,8 @@
 //   c' s = c' s_hi + c' s_lo, s_hi the leading 7 bits of s: c' s_hi is exact in
 //   binary16, c' s_lo is rounded at 2^-18 of c' s; two products;
 //   sum_d q_d z'_d, the same for the 32 tokens of a group, is formed apart (z'
-//   as the sum of two binary16 numbers) by mma.sync and joins the score in
-//   binary32.
+//   as the sum of two binary16 numbers, off by 2^-22 of it at most) by mma.sync and
+//   joins the score in binary32.
 // Values alike: sum_t p_t z'_t of each value group apart.  With them, as one
 // more column of ones, the sum of the weights.
 // Why the codes are centered: the tensor cores cut each accumulation off toward

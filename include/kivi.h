@@ -513,9 +513,10 @@ KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq
  * Sums, the softmax and its statistics are binary32 for both dtypes; with
  * fp16 inputs the stored codes' products and the weights p_t pass through
  * binary16 matrix operands as the kernel's comments say: a stored number is
- * carried to 2^-17 of its group's range and to 2^-21 absolutely (values of the
- * size of binary16's subnormals lose part of their bits), a weight to 2^-11 of
- * itself and to 2^-29 of the largest.
+ * carried to 2^-17 of its group's range, 2^-22 of its group's middle (minimum
+ * plus half the range, which is more where a narrow group lies far from zero)
+ * and 2^-21 absolutely (values of the size of binary16's subnormals lose part
+ * of their bits), a weight to 2^-11 of itself and to 2^-29 of the largest.
  * Errors: KIVI_ERR_ARG (null or misaligned pointer, N < 1, Hq not a multiple
  * of Hkv), KIVI_ERR_UNSUPPORTED (N > 256, Hq/Hkv > 64, a dense-and-sparse
  * cache), KIVI_ERR_STATE (a ragged or paged cache),

@@ -1,5 +1,5 @@
 """Numbers of the attention of drafted tokens: references that rise in the middle of a range, scores
-far apart, weights far below the largest, infinite and NaN values.
+far apart, weights far below the largest, narrow groups far from zero, infinite and NaN values.
 Against 64-bit sums over the bytes that the cache holds (draft_testlib.tokens)."""
 import math
 
@@ -142,6 +142,37 @@ def test_tree_small_weights_at_any_gap(dtype, gap):
         if f16:
             tol = tol + T * 2.0 ** -29 / l * vmax + 2 * T / 16 * 2.0 ** -23 * A
         assert ((got[b, h] - ref).abs() <= tol).all(), (b, h)
+
+
+@pytest.mark.parametrize("bits", [1, 2, 4])
+@pytest.mark.parametrize("meta", [torch.float32, torch.float16])
+def test_tree_narrow_groups_far_from_zero(bits, meta):
+    """Groups of keys a unit wide around 1400, where a group's middle is most of what is carried: a stored
+    key is off by 2^-17 of its group's range, 2^-22 of its middle and 2^-21, as include/kivi.h states.
+    One channel of q is not 0, so a score has 6 roundings to binary32 more."""
+    B, Hkv, D, T, N = 2, 2, 64, 600, 5
+    g = torch.Generator().manual_seed(bits)
+    c = kivi.KiviCache(B, Hkv, D, bits, 1024, R=32, meta=meta)
+    mid = 1400 + torch.randint(0, 8, (B, Hkv, T // 32 + 1, 1), generator=g).float()
+    K = (mid.repeat_interleave(32, 2)[:, :, :T] + torch.rand(B, Hkv, T, D, generator=g))
+    V = torch.randn(B, Hkv, T, D, generator=g)
+    c.prefill(K.half().cuda(), V.half().cuda())
+    q = torch.zeros(B, Hkv, N, D)
+    q[..., 9] = 1.0
+    k, v = torch.full((B, Hkv, N, D), 1404.0), torch.randn(B, Hkv, N, D, generator=g)
+    q, k, v = (x.half().cuda() for x in (q, k, v))
+    mask = kivi.tree_mask(torch.full((B, N), -1)).cuda()
+    for scale in (1.0, 4.0):
+        got = c.tree_decode(q, k, v, mask, scale).cpu().double()
+        for b in range(B):
+            for h in range(Hkv):
+                ref, A, s, l, vmax = weigh(c, b, h, 1, q, k, v, mask, scale)
+                n = s.shape[1]
+                e_s = scale * (2.0 ** -17 + 1409 * 2.0 ** -22 + 2.0 ** -21) + scale * 1409 * 6 * U
+                eps = 2 * e_s + 140 * U + n * U + 2.0 ** -11 + 2.0 ** -17
+                tol = (2 * eps * A + 2.0 ** -11 * ref.abs() + n * 2.0 ** -29 / l * vmax + 2.0 ** -25
+                       + 2.0 ** -17 * vmax)
+                assert ((got[b, h] - ref).abs() <= tol).all(), (scale, b, h)
 
 
 # ---- infinite and NaN values and keys of tokens that a node attends to ---------------------------
