@@ -33,7 +33,7 @@ __device__ __forceinline__ void store_row(T* p, const float (&x)[CH], bool wide)
 // Bound by the stores' traffic to DRAM, next to the unpacking's integer work (64 % of
 // its pipe): 8 x 32 heads of 4096 tokens at 2 bits take 93 us, 5.0 TB/s of codes read
 // and numbers written (a copy reaches 6.5), 117 us when each row's loads waited for the
-// stores before them; 2 sequences' last 5001 tokens 3 us.
+// stores before them; the last 401 of 5001 tokens of 2 sequences x 8 heads 3 us.
 template <int D, int BITS, typename T, typename M>
 __global__ void __launch_bounds__(D / (16 / (int)sizeof(T)) * 8)
     read_kernel(CacheView c, int Hkv, long long n_q, int r, const DevState* st, long long t0,

@@ -27,7 +27,6 @@ struct TreePlan {
   int tt;      // tokens of a tile
   int n_rb;    // row blocks of a KV head
   int ctas;    // CTAs of the split kernel
-  int min_w;   // shortest range
   int parts;   // tensor cores: groups of four warps in a block
 };
 
@@ -102,9 +101,10 @@ __device__ __forceinline__ TreeAt tree_find(const TreeArgs& a, const TreePlan& p
   o.total = sum;
   return o;
 }
+// Tiles of a CTA's range: one at least (every group has a tile); longer ones leave SMs
+// idle where a cache is short.
 __device__ __forceinline__ long long tree_range(const TreePlan& p, long long total) {
-  const long long w = (total + p.ctas - 1) / p.ctas;
-  return w < p.min_w ? p.min_w : w;
+  return (total + p.ctas - 1) / p.ctas;
 }
 
 // Lets `kernel` have `bytes` of dynamic shared memory on the current device; asked for

@@ -143,8 +143,7 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 // The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all fit
 // (four blocks on an SM instead of three).  Tensor cores: up to 64 rows two blocks of
 // threads on an SM, more in row blocks of equal size up to 128 rows, one block on an SM
-// (both sides measured: kivi_tree_tc.cuh).  The shortest range is one tile: longer ones
-// leave SMs idle where a cache is short.
+// (both sides measured: kivi_tree_tc.cuh).
 static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
   const int rows = gq * N;
   TreePlan p;
@@ -153,7 +152,6 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 32;
     p.ctas = sms * (p.rb == 16 ? 4 : 3);
-    p.min_w = 1;
     p.parts = 0;
   } else {
     p.parts = rows <= 64 ? 2 : 4;
@@ -163,7 +161,6 @@ static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
     p.n_rb = (rows + p.rb - 1) / p.rb;
     p.tt = 128;
     p.ctas = p.parts == 2 ? 2 * sms : sms;
-    p.min_w = 1;
   }
   return p;
 }

@@ -4,7 +4,7 @@
 //
 // The work is split as kivi_tree.cuh says, in tiles of 128 tokens; a row is a
 // (query head of the group, node) pair, `nr` rows (a multiple of 16, at most
-// 64) at a time.  Both products are taken transposed, so that the cache's side
+// 128) at a time.  Both products are taken transposed, so that the cache's side
 // fills the 128 rows of the matrix instruction whatever the tree's size is:
 //   S^T [128 tokens x nr]  = K^ [128 x D]      . Q^T   (A = K^, B = Q)
 //   O^T [128 (D) x nr]    += V^^T [D x 128]    . P^T   (A = V^^T, B = P)
