@@ -237,9 +237,7 @@ class KiviCache:
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
         self._staging: Optional[torch.Tensor] = None
-        self._ws_tree: Optional[torch.Tensor] = None
-        self._ws_tree_kept: list = []  # outgrown ones, which captured graphs may still use
-        self._tree_need: dict = {}  # workspace bytes by (N, Hq)
+        self._init_tree()
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         self.shapes = {
@@ -481,6 +479,33 @@ class KiviCache:
         return out
 
     # -- drafted tokens (speculative decoding)
+    def _init_tree(self):
+        self._ws_tree: Optional[torch.Tensor] = None
+        self._ws_tree_streams: set = set()  # streams that the allocator knows it to be used on
+        self._ws_tree_captured = False  # a graph has it
+        self._ws_tree_kept: list = []  # outgrown ones that graphs have
+        self._tree_need: dict = {}  # workspace bytes by (N, Hq)
+
+    def _tree_ws(self, N: int, Hq: int, stream: int) -> torch.Tensor:
+        """The tree calls' workspace, with the cache's device current.  An outgrown one goes back to
+        the allocator once the streams that used it are done, unless a capture took it."""
+        need = self._tree_need.get((N, Hq))
+        if need is None:
+            need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
+            self._tree_need[N, Hq] = need
+        if self._ws_tree is None or self._ws_tree.numel() < need:
+            if self._ws_tree_captured:
+                self._ws_tree_kept.append(self._ws_tree)
+            self._ws_tree = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+            self._ws_tree_streams = {stream}
+            self._ws_tree_captured = False
+        if torch.cuda.is_current_stream_capturing():
+            self._ws_tree_captured = True
+        elif stream not in self._ws_tree_streams:
+            self._ws_tree.record_stream(torch.cuda.current_stream(self.device))
+            self._ws_tree_streams.add(stream)
+        return self._ws_tree
+
     def _tree_args(self, q, k, v, mask, out):
         if q.dim() != 4:
             raise ValueError(f"q: expected shape (B, Hq, N, D), got {tuple(q.shape)}")
@@ -496,15 +521,6 @@ class KiviCache:
         if out is None:
             out = torch.empty_like(q)
         po = self._arg(out, (self.B, Hq, N, self.D), "out")
-        need = self._tree_need.get((N, Hq))
-        if need is None:
-            with _on(self.device):
-                need = int(lib().kivi_tree_workspace_bytes(ctypes.byref(self._c), N, Hq))
-            self._tree_need[N, Hq] = need
-        if self._ws_tree is None or self._ws_tree.numel() < need:
-            if self._ws_tree is not None:
-                self._ws_tree_kept.append(self._ws_tree)
-            self._ws_tree = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
         return (pq, pk, pv, mask.data_ptr(), N, Hq), po, out
 
     def tree_decode(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor,
@@ -515,9 +531,10 @@ class KiviCache:
         share one workspace: on several streams at a time they take one cache object each."""
         args, po, out = self._tree_args(q, k, v, mask, out)
         with _on(self.device):
+            stream = _raw_stream(self.device)
+            ws = self._tree_ws(*args[-2:], stream)
             _check(lib().kivi_tree_decode(ctypes.byref(self._c), *args, float(softmax_scale), po,
-                                          self._ws_tree.data_ptr(), self._ws_tree.numel(),
-                                          _raw_stream(self.device)), "kivi_tree_decode")
+                                          ws.data_ptr(), ws.numel(), stream), "kivi_tree_decode")
         return out
 
     def ragged_tree_decode(self, st: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -526,10 +543,11 @@ class KiviCache:
         """tree_decode of a ragged batch, every sequence over its own tokens."""
         args, po, out = self._tree_args(q, k, v, mask, out)
         with _on(self.device):
+            stream = _raw_stream(self.device)
+            ws = self._tree_ws(*args[-2:], stream)
             _check(lib().kivi_ragged_tree_decode(ctypes.byref(self._c), self._state_arg(st), *args,
-                                                 float(softmax_scale), po,
-                                                 self._ws_tree.data_ptr(), self._ws_tree.numel(),
-                                                 _raw_stream(self.device)), "kivi_ragged_tree_decode")
+                                                 float(softmax_scale), po, ws.data_ptr(), ws.numel(),
+                                                 stream), "kivi_ragged_tree_decode")
         return out
 
     def _state_arg(self, st: torch.Tensor) -> int:
@@ -624,9 +642,7 @@ class PagedKiviCache(KiviCache):
                                            pages_per_seq, num_pages), "kivi_paged_cache_init")
         self._ws: Optional[torch.Tensor] = None
         self._ws_dev: Optional[torch.Tensor] = None
-        self._ws_tree: Optional[torch.Tensor] = None
-        self._ws_tree_kept: list = []  # outgrown ones, which captured graphs may still use
-        self._tree_need: dict = {}  # workspace bytes by (N, Hq)
+        self._init_tree()
         E, WB = _code_block(bits)
         self.B, self.Hkv, self.D, self.bits, self.R, self.capacity = B, Hkv, D, bits, R, capacity
         P = num_pages
