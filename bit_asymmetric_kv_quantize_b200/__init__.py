@@ -575,8 +575,11 @@ class KiviCache:
                                                  N, path.data_ptr(), count.data_ptr(), P,
                                                  _raw_stream(self.device)), "kivi_ragged_tree_commit")
 
-    def _read_out(self, T: int, K, V):
-        shape = (self.B, self.Hkv, max(int(T), 0), self.D)
+    def _read_out(self, what: str, t0: int, T: int, K, V):
+        # no room is made for a range that no fill of this cache has
+        if t0 < 0 or T < 0 or t0 > self.capacity or T > self.capacity - t0:
+            raise KiviError(1, what)
+        shape = (self.B, self.Hkv, T, self.D)
         make = lambda: torch.zeros(shape, dtype=self.dtype, device=self.device)  # noqa: E731
         K, V = make() if K is None else K, make() if V is None else V
         return self._arg(K, shape, "K"), self._arg(V, shape, "V"), K, V
@@ -584,7 +587,7 @@ class KiviCache:
     def read_tokens(self, t0: int, T: int, K: Optional[torch.Tensor] = None,
                     V: Optional[torch.Tensor] = None):
         """Tokens t0 .. t0+T-1 as numbers: (K, V), each [B][Hkv][T][D] (kivi_read_tokens)."""
-        pk, pv, K, V = self._read_out(T, K, V)
+        pk, pv, K, V = self._read_out("kivi_read_tokens", t0, T, K, V)
         with _on(self.device):
             _check(lib().kivi_read_tokens(ctypes.byref(self._c), t0, T, pk, pv, _raw_stream(self.device)),
                    "kivi_read_tokens")
@@ -594,7 +597,7 @@ class KiviCache:
                            K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None):
         """read_tokens of a ragged batch; tokens that a sequence does not have are left as they
         were in K and V (zeros in those made here)."""
-        pk, pv, K, V = self._read_out(T, K, V)
+        pk, pv, K, V = self._read_out("kivi_ragged_read_tokens", t0, T, K, V)
         with _on(self.device):
             _check(lib().kivi_ragged_read_tokens(ctypes.byref(self._c), self._state_arg(st), t0, T,
                                                  pk, pv, _raw_stream(self.device)),

@@ -66,3 +66,18 @@ def test_workspace_given_back_while_another_stream_uses_it():
     others = [torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and all(bool((o == 0xA5).all()) for o in others)
+
+
+@pytest.mark.parametrize("t0,T", [(0, 1 << 40), (-1, 1), (0, -1), (4096, 1), (1 << 50, 1)])
+def test_read_refuses_a_range_before_it_makes_room_for_it(t0, T):
+    c, _ = filled()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(kivi.KiviError):
+        c.read_tokens(t0, T)
+    r = kivi.KiviCache(1, 1, 64, 2, 4096, R=64)
+    x = torch.zeros(1, 1, 100, 64, dtype=torch.float16, device="cuda")
+    st = r.ragged_prefill(x, x, torch.tensor([100], device="cuda"))
+    with pytest.raises(kivi.KiviError):
+        r.ragged_read_tokens(st, t0, T)
+    del r, x, st
+    assert torch.cuda.memory_allocated() == before
