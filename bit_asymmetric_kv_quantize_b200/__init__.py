@@ -665,8 +665,10 @@ def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     """The mask of tree_decode for trees given by parents: int [B][N], the parent node of each
     node (a lower number), or -1 for one that follows the cache's last token.  Each node attends
     to itself and its ancestors.  Returned on the device of `parents`, made on the host."""
+    if parents.dtype not in (torch.int8, torch.uint8, torch.int16, torch.int32, torch.int64):
+        raise ValueError(f"parents: expected an int tensor, got {parents.dtype}")
     p = parents.detach().cpu().to(torch.int64)
-    if p.dim() != 2:
+    if p.dim() != 2 or p.numel() == 0:
         raise ValueError(f"parents: expected shape (B, N), got {tuple(p.shape)}")
     B, N = p.shape
     if bool((p >= torch.arange(N)).any()) or bool((p < -1).any()):
