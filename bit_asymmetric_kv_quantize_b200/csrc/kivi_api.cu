@@ -67,6 +67,11 @@ int check_cache(const kivi_cache* c) {
 }
 
 size_t elem_bytes(int dtype) { return dtype == KIVI_F32 ? 4 : 2; }
+// Whether pointers (null among them) are aligned to elements of a cache's type.
+template <typename... P>
+bool aligned(int dtype, P... p) {
+  return ((... | (uintptr_t)p) & (elem_bytes(dtype) - 1)) == 0;
+}
 size_t meta_bytes(int meta) { return meta == KIVI_META_F16 ? 2 : 4; }
 
 CacheView view(const kivi_cache* c) {
@@ -349,7 +354,7 @@ int tree_decode(const kivi_cache* c, const void* state, const void* q, const voi
   if (rc) return rc;
   if (ragged && (!state || ((uintptr_t)state & 15))) return KIVI_ERR_ARG;
   if (!q || !k || !v || !mask || ((uintptr_t)mask & 3) || !out || Hq <= 0 ||
-      Hq % c->dims.Hkv != 0 || N < 1)
+      Hq % c->dims.Hkv != 0 || N < 1 || !aligned(c->dims.dtype, q, k, v, out))
     return KIVI_ERR_ARG;
   const int gq = Hq / c->dims.Hkv;
   if (N > kMaxNodes || gq > kMaxTreeGq || sparse(c->dims)) return KIVI_ERR_UNSUPPORTED;
@@ -867,7 +872,8 @@ int kivi_ragged_tree_commit(const kivi_cache* cache, void* state, const void* k,
   int rc = check_cache(cache);
   if (rc) return rc;
   if (!state || ((uintptr_t)state & 15) || !k || !v || !path || ((uintptr_t)path & 3) || !count ||
-      ((uintptr_t)count & 3) || N < 1 || P < 1 || P > cache->dims.R)
+      ((uintptr_t)count & 3) || N < 1 || P < 1 || P > cache->dims.R ||
+      !aligned(cache->dims.dtype, k, v))
     return KIVI_ERR_ARG;
   if (N > kMaxNodes) return KIVI_ERR_UNSUPPORTED;
   if (!is_ragged(cache)) return KIVI_ERR_STATE;
@@ -885,7 +891,9 @@ int kivi_read_tokens(const kivi_cache* cache, long long t0, long long T, void* K
   if (rc) return rc;
   if (device_counted(cache)) return KIVI_ERR_STATE;
   const long long n = cache->n_q + cache->r;
-  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V))) return KIVI_ERR_ARG;
+  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V)) ||
+      !aligned(cache->dims.dtype, K, V))
+    return KIVI_ERR_ARG;
   return read_tokens(cache, nullptr, t0, T, K, V, stream);
 }
 
@@ -896,7 +904,9 @@ int kivi_ragged_read_tokens(const kivi_cache* cache, const void* state, long lon
   if (!state || ((uintptr_t)state & 15)) return KIVI_ERR_ARG;
   if (!is_ragged(cache)) return KIVI_ERR_STATE;
   const long long n = cache->dims.capacity;
-  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V))) return KIVI_ERR_ARG;
+  if (t0 < 0 || T < 0 || t0 > n || T > n - t0 || (T > 0 && (!K || !V)) ||
+      !aligned(cache->dims.dtype, K, V))
+    return KIVI_ERR_ARG;
   return read_tokens(cache, state, t0, T, K, V, stream);
 }
 

@@ -508,7 +508,7 @@ KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq
  * -infinity is a weight of 0, and a node without any other weight (an empty
  * cache and an empty mask among them) gets 0.  The cache may be empty.  It is
  * only read: see kivi_ragged_tree_commit.
- * Any element alignment of q, k, v and out is accepted; out overlaps no input.
+ * q, k, v and out are aligned to their elements, no more; out overlaps no input.
  * Two launches, capturable in a CUDA graph.
  * Sums, the softmax and its statistics are binary32 for both dtypes; with
  * fp16 inputs the stored codes' products and the weights p_t pass through
@@ -558,9 +558,9 @@ KIVI_API int kivi_ragged_tree_commit(const kivi_cache *cache, void *state, const
  * dims.dtype, [B][Hkv][T][D].  A quantized token is c * s + z (kept entries of
  * a dense-and-sparse cache: their value), computed in binary32 by one fused
  * multiply-add and rounded to dims.dtype; a window token is its stored value.
- * Any element alignment of K and V is accepted.  T = 0 does nothing.
- * Errors: KIVI_ERR_ARG (null pointer, a range that is not within the
- * n_q + r tokens), KIVI_ERR_STATE (a ragged or paged cache), KIVI_ERR_CUDA. */
+ * K and V are aligned to their elements, no more.  T = 0 does nothing.
+ * Errors: KIVI_ERR_ARG (null or misaligned pointer, a range that is not within
+ * the n_q + r tokens), KIVI_ERR_STATE (a ragged or paged cache), KIVI_ERR_CUDA. */
 KIVI_API int kivi_read_tokens(const kivi_cache *cache, long long t0, long long T, void *K,
                               void *V, void *stream);
 
