@@ -960,10 +960,10 @@ int kivi_qk_norm_rope(const kivi_rope* p, const void* qkv, long long stride,
   a.interleaved = p->interleaved != 0;
   a.dtype = p->dtype;
   a.eps = p->eps;
-  a.sms = device_sms();
-  if (a.sms <= 0) return KIVI_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms <= 0) return KIVI_ERR_CUDA;
   touch_noalloc_scratch();
-  return kivi::launch_rope(a, (cudaStream_t)stream) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
+  return kivi::launch_rope(a, sms, (cudaStream_t)stream) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -53,8 +53,8 @@ struct RopeArgs {
   int B, N, Hq, Hkv, D, rot, axes, interleaved, dtype;
   int section_end[kRopeMaxAxes];  // pair i turns by axis a: i < section_end[a]
   float eps;
-  int sms;                  // of the device
 };
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+// sms: of the device
+cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t s);
 
 }  // namespace kivi

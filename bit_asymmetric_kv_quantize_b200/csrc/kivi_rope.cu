@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a, int TB) 
 }
 
 template <int D, typename T>
-cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
+cudaError_t rope_t(const RopeArgs& a, int sms, cudaStream_t s) {
   const int tokens = a.B * a.N;
   constexpr int RPB = kRopeThreads * 8 / D;
   // As many tokens a block (of 8, 4, 2) as leave every SM a block, since a block's table
@@ -200,7 +200,7 @@ cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
   // those 10.2 / 6.8 / 7.8 / 12.0; 16 of them 4.8 / 5.3 / 7.5 / 11.7.  At a step itself wide
   // rows would do a little better with the number before (592 tokens of 48 heads: 6.9 with two, 7.9 with
   // four), narrow ones with the one after.
-  const int TB = tokens >= 8 * a.sms ? 8 : tokens >= 4 * a.sms ? 4 : tokens >= 2 * a.sms ? 2 : 1;
+  const int TB = tokens >= 8 * sms ? 8 : tokens >= 4 * sms ? 4 : tokens >= 2 * sms ? 2 : 1;
   const int spread = (a.Hq + RPB - 1) / RPB;
   const dim3 grid((unsigned)((tokens + TB - 1) / TB), TB > 1 ? 1 : (unsigned)min(spread, 65535));
   const size_t bytes = TB * (a.rot / 2) * sizeof(float2);
@@ -212,19 +212,19 @@ cudaError_t rope_t(const RopeArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t rope_d(const RopeArgs& a, cudaStream_t s) {
+cudaError_t rope_d(const RopeArgs& a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 32: return rope_t<32, T>(a, s);
-    case 64: return rope_t<64, T>(a, s);
-    case 128: return rope_t<128, T>(a, s);
+    case 32: return rope_t<32, T>(a, sms, s);
+    case 64: return rope_t<64, T>(a, sms, s);
+    case 128: return rope_t<128, T>(a, sms, s);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
-  return a.dtype == 1 ? rope_d<float>(a, s) : rope_d<__half>(a, s);
+cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t s) {
+  return a.dtype == 1 ? rope_d<float>(a, sms, s) : rope_d<__half>(a, sms, s);
 }
 
 }  // namespace kivi
