@@ -10,10 +10,11 @@
 // tiles, end to end, are cut into equal ranges of W, one per CTA, whatever the
 // lengths are, so a ragged batch keeps all CTAs busy.  A group that falls into
 // one range is written out at once; of any other, each CTA leaves a partial
-// (max, sum, accumulators of RB rows) in one of its two slots -- slot 1: the
-// segment begins the group, slot 0: it does not -- and tree_merge_kernel joins
-// them.  Nothing is counted or kept between calls, so calls may be captured
-// and replayed in any order on one workspace.
+// (max, sum, accumulators of RB rows; the sums negative where raw values of the
+// segment are infinite or NaN) in one of its two slots -- slot 1: the segment
+// begins the group, slot 0: it does not -- and tree_merge_kernel joins them.
+// Nothing is counted or kept between calls, so calls may be captured and replayed
+// in any order on one workspace.
 #pragma once
 
 #include <atomic>

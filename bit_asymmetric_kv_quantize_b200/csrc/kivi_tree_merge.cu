@@ -8,15 +8,36 @@ namespace {
 constexpr int kMergeRows = 8;
 constexpr int kMergeThreads = 32 * kMergeRows;
 
+// The sum of a lane's share of the partials (P: the first one's piece were it a slot 0) where
+// some may not be finite: one with a weight of 0 is added as it is.
+__device__ __noinline__ float4 merge_odd(const float* P, long long stride, const float* w, int s,
+                                         int n, int step) {
+  auto join = [](float e, float x, float sum) {
+    return e != 0.f || isfinite(x) ? fmaf(e, x, sum) : sum + x;
+  };
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (; s < n; s += step) {
+    const float e = w[s];
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(P + (s == 0 ? 1 : 2LL * s) * stride));
+    num.x = join(e, v.x, num.x);
+    num.y = join(e, v.y, num.y);
+    num.z = join(e, v.z, num.z);
+    num.w = join(e, v.w, num.w);
+  }
+  return num;
+}
+
 // Block (group, 8 rows of it), a warp for each row: of the segments' partials (m_s,
 // l_s, acc_s), M = max m_s and weights 2^(m_s - M) first, then
 // out = sum 2^(m_s - M) acc_s / sum 2^(m_s - M) l_s with all loads independent of each
 // other: bound by their latency (a long cache of few heads has a partial of every CTA;
-// one binary32 head of 20011 tokens, 444 partials, takes 32 us in all, 41 with each
-// partial weighed as it came).  A row that
+// 9 rows of one binary32 head of 20011 tokens, 313 partials, take 30 us in all at D 64 and
+// 48 at D 128; with each partial weighed as it came the first took 41).  A row that
 // attended to nothing (all l_s = 0) is 0.  An infinite or NaN accumulator keeps its part
 // where the weight of its segment comes to 0: what a row attends to may not vanish with
-// the way in which the work is split.
+// the way in which the work is split.  The split kernels say by the sign of l_s where
+// there may be any (asking each accumulator here took the 48 us to 107, and a second
+// walk behind the first, by its registers, to 54).
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, TreePlan p) {
   const long long gpb = (long long)a.Hkv * p.n_rb;
@@ -69,34 +90,38 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a, T
   extern __shared__ float w_s[];  // [8 rows][partials]
   float* w = w_s + warp * n;
   float M = -__builtin_huge_valf();
+  bool odd = false;
   for (int s = lane; s < n; s += 32) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(s)) + row);
     if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    odd |= __float_as_int(ml.y) < 0;
   }
   M = warp_max(M);
+  odd = __any_sync(0xffffffffu, odd);
   float den = 0.f;
   for (int s = lane; s < n; s += 32) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(at(s)) + row);
     const float e = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
     w[s] = e;
-    den = fmaf(e, ml.y, den);
+    den = fmaf(e, fabsf(ml.y), den);
   }
   den = warp_sum(den);
   __syncwarp();
   constexpr int LPR = D / 4, SPL = 32 / LPR;  // lanes of a row, and how many share the partials
   const int d = lane % LPR * 4;
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (odd) {
+    num = merge_odd(P + 2 * p.rb + (long long)row * D + d, stride, w, lane / LPR, n, SPL);
+  } else {
 #pragma unroll 8
-  for (int s = lane / LPR; s < n; s += SPL) {
-    const float e = w[s];
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(at(s) + 2 * p.rb + (long long)row * D + d));
-    auto join = [e](float x, float sum) {
-      return e != 0.f || isfinite(x) ? fmaf(e, x, sum) : sum + x;
-    };
-    num.x = join(v.x, num.x);
-    num.y = join(v.y, num.y);
-    num.z = join(v.z, num.z);
-    num.w = join(v.w, num.w);
+    for (int s = lane / LPR; s < n; s += SPL) {
+      const float e = w[s];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(at(s) + 2 * p.rb + (long long)row * D + d));
+      num.x = fmaf(e, v.x, num.x);
+      num.y = fmaf(e, v.y, num.y);
+      num.z = fmaf(e, v.z, num.z);
+      num.w = fmaf(e, v.w, num.w);
+    }
   }
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1) {

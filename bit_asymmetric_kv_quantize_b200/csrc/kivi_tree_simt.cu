@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
       }
     } else {
       float* pp = a.part + (2 * W0 + (tile0 == 0)) * tree_part(p, D);
-      for (int i = tid; i < 2 * RB; i += kThreads) pp[i] = sm[SM::P + i];
+      // (the sum's sign: whether there were infinite or NaN raw values)
+      for (int i = tid; i < 2 * RB; i += kThreads)
+        pp[i] = s_odd && (i & 1) ? -sm[SM::P + i] : sm[SM::P + i];
       dst = pp + 2 * RB;
 #pragma unroll
       for (int i = 0; i < OR; ++i)

@@ -1258,7 +1258,8 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
       {
         const int ch_d = q * 32 + lane;
         const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
-        const int i1 = s_odd ? min((g.t1 - g.tq) * kTcTile, n_raw) : 0;
+        const bool odd = s_odd != 0;  // infinite or NaN raw values
+        const int i1 = odd ? min((g.t1 - g.tq) * kTcTile, n_raw) : 0;
         float* pt = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
         __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
 #pragma unroll 1
@@ -1295,7 +1296,7 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
               pt[2 * nr + row * D + ch_d] = o;
               if (ch_d == 0) {
                 pt[2 * row] = m;
-                pt[2 * row + 1] = l;
+                pt[2 * row + 1] = odd ? -l : l;
               }
             }
           }
