@@ -81,3 +81,38 @@ def test_read_refuses_a_range_before_it_makes_room_for_it(t0, T):
         r.ragged_read_tokens(st, t0, T)
     del r, x, st
     assert torch.cuda.memory_allocated() == before
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_cache_that_is_all_window(dtype):
+    """capacity == R: no store, and no flush that could have room."""
+    R, D = 32, 64
+    c = kivi.KiviCache(2, 2, D, 2, R, R=R, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, V = (torch.randn(2, 2, 30, D, generator=g, device="cuda").to(dtype) for _ in "kv")
+    st = c.ragged_prefill(K, V, torch.tensor([30, 7], device="cuda"))
+    k, v = (torch.randn(2, 2, 4, D, generator=g, device="cuda").to(dtype) for _ in "kv")
+    q = torch.randn(2, 4, 4, D, generator=g, device="cuda").to(dtype)
+    mask = kivi.tree_mask((torch.arange(4) - 1).expand(2, 4)).cuda()
+    see = torch.tril(torch.ones(4, 4, dtype=torch.bool))
+    out = c.ragged_tree_decode(st, q, k, v, mask, 0.125).cpu().double()
+    for b, n in ((0, 30), (1, 7)):
+        for h in range(4):
+            ks = torch.cat([K[b, h // 2, :n], k[b, h // 2]]).cpu().double()
+            vs = torch.cat([V[b, h // 2, :n], v[b, h // 2]]).cpu().double()
+            s = q[b, h].cpu().double() @ ks.T * 0.125
+            s = s.masked_fill(torch.cat([torch.zeros(4, n).bool(), ~see], 1), -float("inf"))
+            ref = torch.softmax(s, -1) @ vs
+            # raw keys and values lose nothing, weights and the output are rounded to the type:
+            # 2 half steps of sum p |V| (numerator and denominator), one of the output, and the
+            # binary32 sums of D and n products
+            half = torch.finfo(dtype).eps / 2
+            A = torch.softmax(s, -1) @ vs.abs()
+            top = (q[b, h].cpu().double().abs() @ ks.abs().T).amax(1, keepdim=True) * 0.125
+            tol = 2 * (half + (2 * top * (D + 8) + 140 + n) * 2.0 ** -24) * A + half * ref.abs() + 2.0 ** -25
+            assert ((out[b, h] - ref).abs() <= tol).all()
+    path = torch.arange(4, dtype=torch.int32, device="cuda").expand(2, 4).contiguous()
+    c.ragged_tree_commit(st, k, v, path, torch.tensor([3, 4], dtype=torch.int32, device="cuda"))
+    assert kivi.ragged_lengths(st) == ([0, 0], [30, 11], [1, 0])
+    Kr, Vr = c.ragged_read_tokens(st, 0, R)
+    assert (Kr[0] == 0).all() and torch.equal(Kr[1, :, 7:11], k[1]) and torch.equal(Vr[1, :, :7], V[1, :, :7])
