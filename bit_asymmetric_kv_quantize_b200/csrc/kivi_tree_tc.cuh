@@ -28,7 +28,12 @@
 // Why the codes are centered: the tensor cores cut each accumulation off toward
 // zero.  With c itself all addends of a sum over tokens are positive, and the cuts
 // add up (the results of a 16384-token GQA layer were off by 1.3e-4 on average, as
-// much as a binary16 output's rounding); the sums of c' stay near zero.
+// much as a binary16 output's rounding); the sums of c' stay near zero, unless a
+// channel's codes are mostly on one side.  Then, and for the sums of z' and of the weights,
+// each of the n / 16 additions cuts off up to 2^-23 of the sum so far: 2^20 tokens of one
+// sign in one range came out 6.4e-3 too small.  So a range takes a group in segments of
+// kTcMost tiles at most, 1024 additions a plane, whose partials are joined in binary32 in
+// the range's slot (131072 tokens a group: 0.9 % more time with 3 rows, 3.4 % with 64).
 // A scale below binary16's normal range keeps fewer bits: c' s is off by at most
 // 15 * 2^-25 < 2^-21 there.
 // s is halved (a binary16 s_hi of a 1-bit group of the widest range would
@@ -100,6 +105,7 @@ constexpr int kTcThreads = (4 * PARTS + 2) * 32;
 constexpr float kTcSlack = 15.0f;   // log2 units a score may exceed m by
 constexpr float kTcBelow = 4.0f;    // and those by which a rise leaves m below the maximum
 constexpr float kTcNone = -1.0e30f; // reference of a row that has seen nothing
+constexpr int kTcMost = 128;        // tiles of a segment at most
 
 // ---- layouts ---------------------------------------------------------------
 template <int D, int BITS, int MB, int PARTS>
@@ -699,6 +705,26 @@ __device__ __forceinline__ uint32_t tc_seen(const uint32_t* mask_s, int node, in
   return bits;
 }
 
+// An accumulator at its weight; an infinite or NaN one is kept where that comes to 0 (as in
+// tree_merge_kernel).
+__device__ __forceinline__ float tc_part(float f, float x) {
+  return f != 0.f || isfinite(x) ? f * x : x;
+}
+// The infinite and NaN values of raw tokens i0 .. i1 - 1 that row `row` of the KV head attends to,
+// added up (w, d: one channel of the window and of the drafted tokens).
+template <int D>
+__device__ __noinline__ float tc_odd(const __half* w, const __half* d, const uint32_t* mask_s, int i0,
+                                     int i1, int r, int row, int N) {
+  float o = 0.f;
+  for (int i = i0; i < i1; ++i) {
+    const __half x = i < r ? w[i * D] : d[(i - r) * D];
+    if ((__half_as_ushort(x) & 0x7C00u) == 0x7C00u &&
+        (i < r || (tc_seen(mask_s, i - r, row, N) & 1u)))
+      o += __half2float(x);
+  }
+  return o;
+}
+
 // Tensor-memory columns: two planes of keys; two of values (the same ones where two
 // blocks share tensor memory); S^T; O^T.
 template <int PARTS>
@@ -713,13 +739,13 @@ struct TcBar {
   static constexpr int raw = 0, scores = 5, values = 6, N = 7;  // raw: [stage]
 };
 
-// One segment of a group.
+// One segment of a group: what of it falls into the block's range, or kTcMost tiles of that.
 struct TcSeg {
   long long b, unit, n_q;
   int t0, t1, tq;      // tiles [t0, t1); of the group, tq of quantized tokens
   int t1s;             // the segment's end of those
   int r, row0, nrows;  // nrows: rows of this block that exist
-  bool whole, ok;
+  bool ends, ok;       // ends: with the group
 };
 // A block's walk over its range: sequence, KV head, row block, tile, tiles left.
 struct TcWalk {
@@ -741,6 +767,7 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
   __shared__ TcWalk s_walk;
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_odd;
+  __shared__ int s_first;       // the tile of the group at which the range meets it
   __shared__ int s_poison[2];   // [segment parity]
   volatile int* dead = &s_dead;
   const uint32_t bar0 = tc_smem(s_bars), sm0 = tc_smem(sm);
@@ -794,15 +821,16 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
   float* lz_s = reinterpret_cast<float*>(sm + Ge::S_LZ);  // [part][ROWS][8]
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Ge::S_MASK);
 
-  // A range ends within a group at most at its own end: segments after the first
-  // begin with a group.
+  // A range ends within a group at most at its own end: the first segment of a group after
+  // the range's first group begins with it.
   auto next_seg = [&](TcWalk& w) -> TcSeg {
     // what steers the warp is broadcast: without that the compiler takes it for
     // divergent and guards each tensor-memory access (some 50 instructions each)
     const TreeSeq q = tree_seq(a, p, w.b);
     TcSeg g;
     g.t0 = w.t;
-    g.t1 = w.t + (int)min(q.ut - w.t, w.left);
+    const int end = w.t + (int)min(q.ut - w.t, w.left);
+    g.t1 = min(end, w.t + kTcMost);
     g.b = w.b;
     g.unit = w.b * a.Hkv + w.h;
     g.row0 = w.rb * nr;
@@ -812,7 +840,8 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
     g.ok = q.ok;
     g.tq = q.ok ? (int)((q.n_q + kTcTile - 1) / kTcTile) : 0;
     g.t1s = min(g.t1, g.tq);
-    g.whole = w.t == 0 && g.t1 == q.ut;
+    g.ends = g.t1 == q.ut;
+    const bool more = g.t1 < end;
     w.left -= g.t1 - g.t0;
     g.t0 = __shfl_sync(0xffffffffu, g.t0, 0);
     g.t1 = __shfl_sync(0xffffffffu, g.t1, 0);
@@ -821,13 +850,16 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
     g.r = __shfl_sync(0xffffffffu, g.r, 0);
     g.nrows = __shfl_sync(0xffffffffu, g.nrows, 0);
     g.ok = __shfl_sync(0xffffffffu, (int)g.ok, 0) != 0;
-    g.whole = __shfl_sync(0xffffffffu, (int)g.whole, 0) != 0;
-    w.t = 0;
-    if (++w.rb == p.n_rb) {
-      w.rb = 0;
-      if (++w.h == a.Hkv) {
-        w.h = 0;
-        ++w.b;
+    g.ends = __shfl_sync(0xffffffffu, (int)g.ends, 0) != 0;
+    w.t = g.t1;
+    if (!more) {
+      w.t = 0;
+      if (++w.rb == p.n_rb) {
+        w.rb = 0;
+        if (++w.h == a.Hkv) {
+          w.h = 0;
+          ++w.b;
+        }
       }
     }
     return g;
@@ -938,7 +970,10 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
       const __half* dv = static_cast<const __half*>(a.v) + g.unit * a.N * D;
       const int n_raw = g.r + a.N;
       // ---- start of a segment: queries, mask, references, pages
-      if (tid == 0) s_odd = 0;
+      if (tid == 0) {
+        s_odd = 0;
+        if (seg == 0 || g.t0 == 0) s_first = g.t0;
+      }
       if (!g.ok) s_poison[seg & 1] = 1;
       if (a.c.bt != nullptr && g.ok) {  // a page outside the pool poisons the group
         const long long i1 = min(g.t1 * 4LL, g.n_q / kTile);
@@ -1254,14 +1289,37 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
       }
       tc_sync_workers<PARTS>();
 
-      // ---- end of a segment: lane = channel, rows 4 part .. of each 4 PARTS
+      // ---- end of a segment: rows first (reference and sum joined with those of the segments
+      // before it, and the weights of both), then lane = channel, rows 4 part .. of each 4 PARTS
       {
         const int ch_d = q * 32 + lane;
-        const bool poison = s_poison[seg & 1] != 0 || *dead != 0;
         const bool odd = s_odd != 0;  // infinite or NaN raw values
         const int i1 = odd ? min((g.t1 - g.tq) * kTcTile, n_raw) : 0;
-        float* pt = a.part + (2 * (long long)blockIdx.x + (g.t0 == 0)) * tree_part(p, D);
+        const int first = s_first;
+        const bool whole = first == 0 && g.ends, cont = g.t0 != first;
+        float* pt = a.part + (2 * (long long)blockIdx.x + (first == 0)) * tree_part(p, D);
         __half* out = static_cast<__half*>(a.out) + (g.unit * rows + g.row0) * (long long)D + ch_d;
+        if (tid < g.nrows) {
+          float l = s_poison[seg & 1] != 0 || *dead != 0 ? kNaN : 0.f, m = m_s[tid];
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) l += lz_s[(i * ROWS + tid) * 8 + 4];
+          bool mark = odd;
+          if (cont) {
+            const float m0 = pt[2 * tid], l0 = pt[2 * tid + 1], top = fmaxf(m0, m);
+            const float f0 = tc_ex2(m0 - top), f = tc_ex2(m - top);
+            mark |= __float_as_int(l0) < 0;
+            l = fmaf(f0, fabsf(l0), f * l);
+            m = top;
+            wmax_s[tid] = f;
+            wmax_s[ROWS + tid] = f0;
+          }
+          f_s[tid] = l;
+          if (!whole) {
+            pt[2 * tid] = m;
+            pt[2 * tid + 1] = mark ? -l : l;
+          }
+        }
+        tc_sync_workers<PARTS>();
 #pragma unroll 1
         for (int e4 = 4 * part; e4 < g.nrows && q < NJ; e4 += 4 * PARTS) {
           float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1270,34 +1328,19 @@ __global__ void __launch_bounds__(kTcThreads<PARTS>, PARTS == 2 ? 2 : 1)
           for (int e = 0; e < 4; ++e) {
             const int row = e4 + e;
             if (row >= g.nrows) break;
-            const float* z = lz_s + row * 8;
-            float l = z[4], m = m_s[row], zs = z[q];
+            float zs = 0.f;
 #pragma unroll
-            for (int i = 1; i < PARTS; ++i) {
-              l += z[i * ROWS * 8 + 4];
-              zs += z[i * ROWS * 8 + q];
-            }
+            for (int i = 0; i < PARTS; ++i) zs += lz_s[(i * ROWS + row) * 8 + q];
             float o = fmaf(2.0f, v[e], zs);
-            // infinite or NaN raw values, of the tokens that the row attends to
-#pragma unroll 1
-            for (int i = max(g.t0 - g.tq, 0) * kTcTile; i < i1; ++i) {
-              const __half w = i < g.r ? wv[i * D + ch_d] : dv[(i - g.r) * D + ch_d];
-              if ((__half_as_ushort(w) & 0x7C00u) == 0x7C00u &&
-                  (i < g.r || (tc_seen(mask_s, i - g.r, g.row0 + row, a.N) & 1u)))
-                o += __half2float(w);
-            }
-            if (poison) {
-              o = m = 0.f;
-              l = kNaN;
-            }
-            if (g.whole) {
+            float* po = pt + 2 * nr + row * D + ch_d;
+            if (odd)
+              o += tc_odd<D>(wv + ch_d, dv + ch_d, mask_s, max(g.t0 - g.tq, 0) * kTcTile, i1, g.r, g.row0 + row, a.N);
+            if (cont) o = tc_part(wmax_s[row], o) + tc_part(wmax_s[ROWS + row], *po);
+            if (whole) {
+              const float l = f_s[row];
               out[row * D] = __float2half_rn(l == 0.f ? 0.f : __fdividef(o, l));
             } else {
-              pt[2 * nr + row * D + ch_d] = o;
-              if (ch_d == 0) {
-                pt[2 * row] = m;
-                pt[2 * row + 1] = odd ? -l : l;
-              }
+              *po = o;
             }
           }
         }

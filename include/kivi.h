@@ -516,7 +516,10 @@ KIVI_API size_t kivi_tree_workspace_bytes(const kivi_cache *cache, int N, int Hq
  * carried to 2^-17 of its group's range, 2^-22 of its group's middle (minimum
  * plus half the range, which is more where a narrow group lies far from zero)
  * and 2^-21 absolutely (values of the size of binary16's subnormals lose part
- * of their bits), a weight to 2^-11 of itself and to 2^-29 of the largest.
+ * of their bits), a weight to 2^-11 of itself and to 2^-29 of the largest; the
+ * matrix instructions cut sums off toward zero, which takes at most 2^-11 of
+ * sum_t p_t |Vhat_t| / sum_t p_t (2^-12 where the weights are spread evenly),
+ * however long the cache is.
  * Errors: KIVI_ERR_ARG (null or misaligned pointer, N < 1, Hq not a multiple
  * of Hkv), KIVI_ERR_UNSUPPORTED (N > 256, Hq/Hkv > 64, a dense-and-sparse
  * cache), KIVI_ERR_STATE (a ragged or paged cache),

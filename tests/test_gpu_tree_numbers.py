@@ -268,6 +268,108 @@ def test_tree_attended_keys_that_are_infinite(dtype, T):
         assert (c.tree_decode(q, k, v, mask, 0.5)[:, :, list(low)] == 0).all()
 
 
+def long_groups(N):
+    """Groups of which a CTA has about one (tensor cores; rows = N)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return 2 * sms + 4 if N <= 64 else sms + 2
+
+
+@pytest.mark.parametrize("N", [3, 80])
+def test_tree_sums_of_one_sign_over_a_million_tokens(N):
+    """Equal weights and, in each channel, equal values: partial sums only grow, and the tensor cores cut each
+    addition off toward zero.  A segment has 128 tiles at most, 1024 steps of 16 tokens: its sums of c' s
+    (two planes) lose up to 2 * 1024 * 2^-23 / 2 of themselves (a step 2^-23 of the sum so far, which
+    grows evenly), those of z' and of the weights 1024 * 2^-23 / 2; the segments are joined in binary32 (64
+    of them, 3 roundings each); a stored value is carried to 2^-17; the output is rounded."""
+    D, T, H = 32, 1 << 20, long_groups(N)
+    c = kivi.KiviCache(1, H, D, 2, T + 32, R=32)
+    for n in ("k_codes", "k_scale", "k_zero", "v_zero", "k_res", "v_res"):
+        c.buffers[n].zero_()
+    code = torch.arange(D) % 4  # of channel d, for every token
+    w = torch.tensor([0, 0x55555555, 0xAAAAAAAA - (1 << 32), -1])[code].to(torch.int32).cuda()
+    c.view("v_codes").copy_(w.expand(c.view("v_codes").shape))
+    c._c.n_q, c._c.r = T, 32
+    q = torch.zeros(1, H, N, D, dtype=torch.float16, device="cuda")
+    none = torch.zeros(1, N, -(-N // 32), dtype=torch.int32, device="cuda")
+    for s, z in ((2 / 3, -1.0), (0.0, 1.0), (2 / 3, 1.0)):
+        c.view("v_scale").fill_(s)
+        c.view("v_zero").fill_(z)
+        want = code.double() * float(torch.tensor(s)) + z
+        c.view("v_res").copy_(want.half().cuda().expand(c.view("v_res").shape))
+        got = c.tree_decode(q, q, q, none, 1.0)[0].cpu().double()
+        part = (code - 1.5).abs() * s + abs(z + 1.5 * s)
+        tol = (2.0 ** -13 + 2 * 2.0 ** -14 + 3 * 64 * U + 2.0 ** -17) * part + 2.0 ** -11 * want.abs()
+        assert ((got - want).abs() <= tol).all(), (s, z, float(((got - want).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("N", [9, 80])
+def test_tree_ranges_of_several_segments(N):
+    """Ranges of more than 128 tiles, whose segments are joined in the kernel: references that rise or fall
+    from one to the next, whole groups and parts of groups, an infinite value, each against its own
+    sums.  Bound as in test_tree_reference_rises_within_a_range."""
+    D, T, H = 32, 20011, long_groups(N)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    c = kivi.KiviCache(1, H, D, 2, 20096, R=32)
+    K = torch.zeros(1, H, T, D, device="cuda")
+    K[..., 0] = 0.1 * torch.rand(1, H, T, generator=g, device="cuda") - 0.05
+    ramp = torch.linspace(0, 16, T, device="cuda")
+    K[:, ::2, :, 1] = ramp
+    K[:, 1::2, :, 1] = ramp.flip(0)
+    V = 0.25 * torch.randn(1, H, T, D, generator=g, device="cuda") + torch.linspace(-1, 1, T, device="cuda")[:, None]
+    c.prefill(K.half(), V.half())
+    assert split_of(c, N, N) > 128
+    q = torch.zeros(1, H, N, D, device="cuda")
+    q[..., 0] = 1.0
+    q[:, :, ::2, 1] = 0.25 * math.log(2)
+    q[:, :, 1::4, 1] = 2 * math.log(2)
+    q = q.half()
+    k, v = (0.3 * torch.randn(1, H, N, D, generator=g, device="cuda").half() for _ in "kv")
+    mask = kivi.tree_mask((torch.arange(N) - 2).clamp(min=-1)[None]).cuda()
+    got = c.tree_decode(q, k, v, mask, 1.0)
+    for h in (0, 1, 2, 51, 100, H // 2, H // 2 + 1, H - 2, H - 1):
+        ref, A, s, l, vmax = weigh(c, 0, h, 1, q, k, v, mask, 1.0)
+        n = s.shape[1]
+        kmax = torch.cat([K[0, h].half(), k[0, h]]).abs().amax(0).cpu().double()
+        e_s = (q[0, h].cpu().double().abs() @ kmax[:, None]) * (3 * 2.0 ** -17 + (D + 8) * U)
+        eps = 2 * e_s + 140 * U + 2.0 ** -11 + 2.0 ** -17 + 2.0 ** -13 + 2 * 2.0 ** -14
+        tol = 2 * eps * A + 2.0 ** -11 * ref.abs() + n * 2.0 ** -29 / l * vmax + 2.0 ** -17 * vmax
+        assert (tol <= 0.006 * A).all()
+        assert ((got[0, h].cpu().double() - ref).abs() <= tol).all(), h
+    v[:, :, 2, 1::3] = math.inf
+    sees2 = sees(mask, N)[0, :, 2].cuda()
+    odd = c.tree_decode(q, k, v, mask, 1.0)
+    assert (odd[:, :, sees2][..., 1::3] == math.inf).all()
+    assert torch.equal(odd[:, :, ~sees2], got[:, :, ~sees2])
+    rest = torch.ones(D, dtype=torch.bool)
+    rest[1::3] = False
+    assert torch.equal(odd[..., rest], got[..., rest])
+    assert torch.equal(c.tree_decode(q, k, v, mask, 1.0), odd)
+
+
+def test_tree_bad_pages_in_ranges_of_several_segments():
+    """A page outside the pool in any segment of a sequence makes all of it NaN, and no other."""
+    D, R, N = 32, 128, 5
+    B = long_groups(N)
+    pages = 160
+    g = torch.Generator(device="cuda").manual_seed(1)
+    bt = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+    c = kivi.PagedKiviCache(B, 1, D, 2, pages, B * pages, bt, R=R)
+    K = torch.randn(B, 1, 20400, D, generator=g, device="cuda").half()
+    st = c.ragged_prefill(K, K, torch.full((B,), 20400, device="cuda"))
+    q, k, v = (torch.randn(B, 1, N, D, generator=g, device="cuda").half() for _ in "qkv")
+    mask = kivi.tree_mask((torch.arange(N) - 1).expand(B, N)).cuda()
+    clean = c.ragged_tree_decode(st, q, k, v, mask, 0.2)
+    bad = {0: 0, 5: 3, 6: 150, 100: 70, B - 1: 158}
+    for b, p in bad.items():
+        c.block_table[b, p] = -1
+    got = c.ragged_tree_decode(st, q, k, v, mask, 0.2)
+    rows = torch.tensor(list(bad), device="cuda")
+    good = torch.ones(B, dtype=torch.bool, device="cuda")
+    good[rows] = False
+    assert torch.isnan(got[rows]).all() and torch.isfinite(clean).all()
+    assert torch.equal(got[good], clean[good])
+
+
 # ---- largest tree, first call in a capture ---------------------------------------------------------
 
 
