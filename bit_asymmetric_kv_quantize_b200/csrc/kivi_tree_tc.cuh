@@ -77,17 +77,19 @@
 // are unpacked while the score products run.  Measured on 8 sequences x 32 heads of 4096
 // tokens at 2 bits, two blocks against one of 16 workers: 8 rows 119 and 174 us, 32
 // rows 139 and 185, 64 rows 180 and 217; 80 rows (2 x 48) 295 and 249, 128 rows (2 x 64)
-// 338 and 293, 160 rows (3 x 64, 2 x 80) 507 and 498.  (Wider loads and stores of words
-// and scales have since taken 2 to 4 % from both.)
+// 338 and 293, 160 rows (3 x 64, 2 x 80) 507 and 498.  (Both have since got faster, wider
+// loads and stores and a shorter segment's end: 114, 130, 167, 240, 283 and 484 us for those
+// row counts in the form that is taken.)
 //
-// What bounds it: neither DRAM (5 to 15 % of its rate) nor the matrix instructions (8
-// to 26 % of their pipe), but the unpacking of codes into tensor memory and the
-// barriers between a tile's steps: half of the issue slots are used, most stalls are
-// waits at barriers (1.8 to 2.6 of the 8 to 9 warps a scheduler's issue waits for).
-// A 4096-token layer of 8 x 32 heads with 16 nodes takes 118 us (1.3 TB/s of the cache,
-// 73 TFLOP/s of the products), a 16384-token GQA layer of 16 x 8 heads, 96 rows,
-// 429 us (240 TFLOP/s), a paged batch of 24 x 8 heads to 6000 tokens at 4 bits, 244
-// rows, 491 us (189 TFLOP/s).
+// What bounds it: neither DRAM (6 to 16 % of its rate) nor the matrix instructions (8
+// to 27 % of their pipe), but instructions and the barriers between a tile's steps, half
+// each: 50 to 53 % of the issue slots are used (7.4 K warp instructions a tile with 16 rows,
+// 13.9 K with 96), and most stalls are waits at barriers (1.8 to 2.7 of the 8 to 9 warps
+// a scheduler's issue waits for).
+// A 4096-token layer of 8 x 32 heads with 16 nodes takes 116 us (1.3 TB/s of the cache,
+// 74 TFLOP/s of the products), a 16384-token GQA layer of 16 x 8 heads, 96 rows,
+// 427 us (241 TFLOP/s), a paged batch of 24 x 8 heads to 6000 tokens at 4 bits, 244
+// rows, 485 us (192 TFLOP/s).
 #pragma once
 
 #include <type_traits>
