@@ -46,8 +46,8 @@
 // exceeds it by more than 15 (in units of log2), and then to 4 below the tile's
 // maximum.  Weights up to 2^15 lose nothing in binary16 or in the binary32 sums.
 // Binary16 takes a weight below 2^-25 for 0, so what is lost lies below 2^-29 of the
-// largest: less than the output's own rounding up to 2^18 such tokens in one range
-// (with the maximum itself for reference it was 2^-25, and 2^14 tokens).  A lower
+// largest: 2^-15 of it for all tokens of a segment, a sixteenth of the output's own
+// rounding (with the maximum itself for reference it was 2^-25, and 2^-11).  A lower
 // reference leaves less room: with 8 below, more tiles raise theirs (16384-token GQA
 // layer of 8 sequences 273 us, against 263 with 4 and 259 with none).
 // The weights of a tile are formed with the references as they are while the excess
