@@ -37,6 +37,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 constexpr int kTT = 32;  // = one key group
+// Tiles of a segment at most.  A sum that grows by equal steps is off by as much as half a
+// unit of its last place at each of them, always to the same side: 16384 equal values in one
+// range came out 4.7e-5 off, 2^20 of them 3e-3.  So a range takes a group in segments of
+// 512 tokens, whose partials are joined in the range's slot (2e-6 and 6e-6; 3 to 5 % more
+// time where ranges are that long).
+constexpr int kSimtMost = 16;
+
+// An accumulator at its weight; an infinite or NaN one is kept where that comes to 0 (as in
+// tree_merge_kernel).
+__device__ __forceinline__ float simt_part(float f, float x) {
+  return f != 0.f || isfinite(x) ? f * x : x;
+}
 
 template <int D, int RB>
 struct SimtSmem {
@@ -83,6 +95,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
   const int rows = a.gq * a.N, mw = (a.N + 31) / 32;
   const float kInf = __builtin_huge_valf();
 
+  bool begins = false;  // the range has the group's first tile
   while (x < end) {
     const TreeSeq q = tree_seq(a, p, b);
     const long long gpb = (long long)a.Hkv * p.n_rb;
@@ -93,7 +106,10 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     }
     const long long grp = rem / q.ut, tile0 = rem % q.ut;
     const long long left = end - x;
-    const long long nt = q.ut - tile0 < left ? q.ut - tile0 : left;
+    const long long most = left < kSimtMost ? left : kSimtMost;
+    const long long nt = q.ut - tile0 < most ? q.ut - tile0 : most;
+    const bool cont = x != W0 * W && tile0 != 0;  // joins the segment before
+    if (!cont) begins = tile0 == 0;
     const int h = (int)(grp / p.n_rb), row0 = (int)(grp % p.n_rb) * RB;
     const long long unit = b * a.Hkv + h;
     const long long tq = (q.n_q + kTT - 1) / kTT;
@@ -291,7 +307,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
     }
 
     // ---- the segment's end
-    const bool whole = tile0 == 0 && nt == q.ut;
+    const bool whole = begins && tile0 + nt == q.ut;
+    float* pp = a.part + (2 * W0 + begins) * tree_part(p, D);
     if (poison) {  // refused sequence, or a page outside the pool
 #pragma unroll
       for (int i = 0; i < SR; ++i) {
@@ -308,13 +325,40 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
       }
     }
     __syncthreads();
+    if (cont) {
+      // joined with the segments so far: rows first (a sum's sign only marks partials with
+      // infinite or NaN raw values), then the accumulators at the weights of both
+      float* f_s = sm + SM::P + 2 * RB;
+      if (tid < RB) {
+        const float m0 = pp[2 * tid], l0 = pp[2 * tid + 1], m1 = sm[SM::P + 2 * tid];
+        const float top = fmaxf(m0, m1), base = top == -kInf ? 0.f : top;
+        const float f0 = exp2f(m0 - base), f1 = exp2f(m1 - base);
+        const float lr = fmaf(f0, fabsf(l0), f1 * sm[SM::P + 2 * tid + 1]);
+        sm[SM::P + 2 * tid] = top;
+        sm[SM::P + 2 * tid + 1] = __float_as_int(l0) < 0 ? -lr : lr;
+        f_s[tid] = f0;
+        f_s[RB + tid] = f1;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < OR; ++i) {
+        const float f0 = f_s[or0 + i], f1 = f_s[RB + or0 + i];
+#pragma unroll
+        for (int g = 0; g < ON; ++g)
+#pragma unroll
+          for (int e = 0; e < OV; ++e)
+            acc[i][g * OV + e] =
+                simt_part(f0, pp[2 * RB + (or0 + i) * D + g * (D / ON) + oc0 + e]) +
+                simt_part(f1, acc[i][g * OV + e]);
+      }
+    }
     float* dst;  // the block's rows of the output, or the accumulators of its partial
     if (whole) {
       dst = static_cast<float*>(a.out) + (unit * rows + row0) * D;
 #pragma unroll
       for (int i = 0; i < OR; ++i) {
         if (row0 + or0 + i >= rows) continue;
-        const float lr = sm[SM::P + 2 * (or0 + i) + 1];
+        const float lr = fabsf(sm[SM::P + 2 * (or0 + i) + 1]);
         const float inv = 1.f / lr;
 #pragma unroll
         for (int g = 0; g < ON; ++g)
@@ -324,10 +368,8 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(TreeArgs a, TreePla
                 lr == 0.f ? 0.f : acc[i][g * OV + e] * inv;
       }
     } else {
-      float* pp = a.part + (2 * W0 + (tile0 == 0)) * tree_part(p, D);
-      // (the sum's sign: whether there were infinite or NaN raw values)
       for (int i = tid; i < 2 * RB; i += kThreads)
-        pp[i] = s_odd && (i & 1) ? -sm[SM::P + i] : sm[SM::P + i];
+        pp[i] = s_odd && (i & 1) ? -fabsf(sm[SM::P + i]) : sm[SM::P + i];
       dst = pp + 2 * RB;
 #pragma unroll
       for (int i = 0; i < OR; ++i)

@@ -2,6 +2,7 @@
 far apart, weights far below the largest, narrow groups far from zero, infinite and NaN values.
 Against 64-bit sums over the bytes that the cache holds (draft_testlib.tokens)."""
 import math
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -26,6 +27,11 @@ def weigh(c, b, h, gq, q, k, v, mask, scale):
     l = p.sum(1, keepdim=True)
     p = p / l
     return p @ V, p @ V.abs(), s, l, V.abs().max()
+
+
+def head_of(c, h):
+    """KV head h of a cache, for weigh."""
+    return SimpleNamespace(bits=c.bits, D=c.D, R=c.R, n_q=c.n_q, r=c.r, view=lambda n: c.view(n)[:, h:h + 1])
 
 
 def split_of(c, rows, N):
@@ -268,9 +274,11 @@ def test_tree_attended_keys_that_are_infinite(dtype, T):
         assert (c.tree_decode(q, k, v, mask, 0.5)[:, :, list(low)] == 0).all()
 
 
-def long_groups(N):
-    """Groups of which a CTA has about one (tensor cores; rows = N)."""
+def long_groups(N, dtype=torch.float16):
+    """Groups of which a CTA has about one (rows = N)."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if dtype == torch.float32:
+        return 4 * sms + 4 if N <= 16 else 3 * sms + 4
     return 2 * sms + 4 if N <= 64 else sms + 2
 
 
@@ -302,38 +310,70 @@ def test_tree_sums_of_one_sign_over_a_million_tokens(N):
         assert ((got - want).abs() <= tol).all(), (s, z, float(((got - want).abs() / tol).max()))
 
 
-@pytest.mark.parametrize("N", [9, 80])
-def test_tree_ranges_of_several_segments(N):
-    """Ranges of more than 128 tiles, whose segments are joined in the kernel: references that rise or fall
-    from one to the next, whole groups and parts of groups, an infinite value, each against its own
-    sums.  Bound as in test_tree_reference_rises_within_a_range."""
-    D, T, H = 32, 20011, long_groups(N)
+@pytest.mark.parametrize("N", [3, 20])
+def test_tree_binary32_sums_of_one_sign(N):
+    """The same in binary32, where an addition is off by half a unit of the sum's last place, to one side for
+    equal steps: 512 of them in a segment, whose sum grows evenly (512 / 2 half steps); 3 roundings for each
+    of T / 512 joins; the value itself, the quotient, and the window's tile 8 more."""
+    D, T, H = 32, 1 << 17, long_groups(N, torch.float32)
+    c = kivi.KiviCache(1, H, D, 2, T + 32, R=32, dtype=torch.float32)
+    for n in ("k_codes", "k_scale", "k_zero", "v_zero", "k_res", "v_res"):
+        c.buffers[n].zero_()
+    code = torch.arange(D) % 4
+    w = torch.tensor([0, 0x55555555, 0xAAAAAAAA - (1 << 32), -1])[code].to(torch.int32).cuda()
+    c.view("v_codes").copy_(w.expand(c.view("v_codes").shape))
+    c._c.n_q, c._c.r = T, 32
+    q = torch.zeros(1, H, N, D, device="cuda")
+    none = torch.zeros(1, N, 1, dtype=torch.int32, device="cuda")
+    for s, z in ((2 / 3, -1.0), (0.1, 0.7), (1 / 3, 1.0)):
+        c.view("v_scale").fill_(s)
+        c.view("v_zero").fill_(z)
+        want = code.double() * float(torch.tensor(s)) + float(torch.tensor(z))
+        c.view("v_res").copy_(want.float().cuda().expand(c.view("v_res").shape))
+        got = c.tree_decode(q, q, q, none, 1.0)[0].cpu().double()
+        tol = (512 / 2 + 3 * T / 512 + 8) * U * want.abs()
+        assert ((got - want).abs() <= tol).all(), (s, z, float(((got - want).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("N,dtype", [(9, torch.float16), (80, torch.float16), (9, torch.float32),
+                                     (50, torch.float32)])
+def test_tree_ranges_of_several_segments(N, dtype):
+    """Ranges of more than 128 tiles (16 in binary32), whose segments are joined in the kernel: references
+    that rise or fall from one to the next, whole groups and parts of groups, an infinite value, each
+    against its own sums.  Bound as in test_tree_reference_rises_within_a_range; binary32: a
+    segment's sums are off by 512 half steps at most, the joins (40) by 3 each."""
+    D, T, H = 32, 20011, long_groups(N, dtype)
+    f16 = dtype == torch.float16
     g = torch.Generator(device="cuda").manual_seed(N)
-    c = kivi.KiviCache(1, H, D, 2, 20096, R=32)
+    c = kivi.KiviCache(1, H, D, 2, 20096, R=32, dtype=dtype)
     K = torch.zeros(1, H, T, D, device="cuda")
     K[..., 0] = 0.1 * torch.rand(1, H, T, generator=g, device="cuda") - 0.05
     ramp = torch.linspace(0, 16, T, device="cuda")
     K[:, ::2, :, 1] = ramp
     K[:, 1::2, :, 1] = ramp.flip(0)
     V = 0.25 * torch.randn(1, H, T, D, generator=g, device="cuda") + torch.linspace(-1, 1, T, device="cuda")[:, None]
-    c.prefill(K.half(), V.half())
-    assert split_of(c, N, N) > 128
+    c.prefill(K.to(dtype), V.to(dtype))
+    assert not f16 or split_of(c, N, N) > 128
     q = torch.zeros(1, H, N, D, device="cuda")
     q[..., 0] = 1.0
     q[:, :, ::2, 1] = 0.25 * math.log(2)
     q[:, :, 1::4, 1] = 2 * math.log(2)
-    q = q.half()
-    k, v = (0.3 * torch.randn(1, H, N, D, generator=g, device="cuda").half() for _ in "kv")
+    q = q.to(dtype)
+    k, v = ((0.3 * torch.randn(1, H, N, D, generator=g, device="cuda")).to(dtype) for _ in "kv")
     mask = kivi.tree_mask((torch.arange(N) - 2).clamp(min=-1)[None]).cuda()
     got = c.tree_decode(q, k, v, mask, 1.0)
     for h in (0, 1, 2, 51, 100, H // 2, H // 2 + 1, H - 2, H - 1):
-        ref, A, s, l, vmax = weigh(c, 0, h, 1, q, k, v, mask, 1.0)
+        ref, A, s, l, vmax = weigh(head_of(c, h), 0, 0, 1, *(x[:, h:h + 1] for x in (q, k, v)), mask, 1.0)
         n = s.shape[1]
-        kmax = torch.cat([K[0, h].half(), k[0, h]]).abs().amax(0).cpu().double()
-        e_s = (q[0, h].cpu().double().abs() @ kmax[:, None]) * (3 * 2.0 ** -17 + (D + 8) * U)
-        eps = 2 * e_s + 140 * U + 2.0 ** -11 + 2.0 ** -17 + 2.0 ** -13 + 2 * 2.0 ** -14
-        tol = 2 * eps * A + 2.0 ** -11 * ref.abs() + n * 2.0 ** -29 / l * vmax + 2.0 ** -17 * vmax
-        assert (tol <= 0.006 * A).all()
+        kmax = torch.cat([K[0, h].to(dtype), k[0, h]]).abs().amax(0).cpu().double()
+        e_s = (q[0, h].cpu().double().abs() @ kmax[:, None]) * ((3 * 2.0 ** -17 if f16 else 0.0) + (D + 8) * U)
+        eps = 2 * e_s + (140 + 512 + 3 * 40) * U
+        if f16:
+            eps = 2 * e_s + 140 * U + 2.0 ** -11 + 2.0 ** -17 + 2.0 ** -13 + 2 * 2.0 ** -14
+        tol = 2 * eps * A + HALF[dtype] * ref.abs()
+        if f16:
+            tol = tol + n * 2.0 ** -29 / l * vmax + 2.0 ** -17 * vmax
+        assert (tol <= (0.006 if f16 else 0.0005) * A).all()  # (2 * 2 e_s = 4 * 22 * 40 u = 2.1e-4 for q = 2 ln 2)
         assert ((got[0, h].cpu().double() - ref).abs() <= tol).all(), h
     v[:, :, 2, 1::3] = math.inf
     sees2 = sees(mask, N)[0, :, 2].cuda()
@@ -346,17 +386,18 @@ def test_tree_ranges_of_several_segments(N):
     assert torch.equal(c.tree_decode(q, k, v, mask, 1.0), odd)
 
 
-def test_tree_bad_pages_in_ranges_of_several_segments():
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_tree_bad_pages_in_ranges_of_several_segments(dtype):
     """A page outside the pool in any segment of a sequence makes all of it NaN, and no other."""
     D, R, N = 32, 128, 5
-    B = long_groups(N)
+    B = long_groups(N, dtype)
     pages = 160
     g = torch.Generator(device="cuda").manual_seed(1)
     bt = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
-    c = kivi.PagedKiviCache(B, 1, D, 2, pages, B * pages, bt, R=R)
-    K = torch.randn(B, 1, 20400, D, generator=g, device="cuda").half()
+    c = kivi.PagedKiviCache(B, 1, D, 2, pages, B * pages, bt, R=R, dtype=dtype)
+    K = torch.randn(B, 1, 20400, D, generator=g, device="cuda").to(dtype)
     st = c.ragged_prefill(K, K, torch.full((B,), 20400, device="cuda"))
-    q, k, v = (torch.randn(B, 1, N, D, generator=g, device="cuda").half() for _ in "qkv")
+    q, k, v = (torch.randn(B, 1, N, D, generator=g, device="cuda").to(dtype) for _ in "qkv")
     mask = kivi.tree_mask((torch.arange(N) - 1).expand(B, N)).cuda()
     clean = c.ragged_tree_decode(st, q, k, v, mask, 0.2)
     bad = {0: 0, 5: 3, 6: 150, 100: 70, B - 1: 158}
