@@ -13,8 +13,8 @@
 // What bounds it: latency.  6 x 4 heads of up to 2999 tokens at 3 bits, 39 rows,
 // take 43 us; the arithmetic alone (39 rows in a block of 64) would take 11 us at 75
 // TFLOP/s, but a block has four warps, three blocks an SM (168 registers a thread hold
-// the tiles; at D 128 some 240, two blocks), and 38 % of the issue slots are used:
-// each waits for its tile's words (1.0 warps a scheduler's issue) and for shared memory
+// the tiles; at D 128 some 240, two blocks), and 39 % of the issue slots are used:
+// each waits for its tile's words (0.9 warps a scheduler's issue) and for shared memory
 // (1.2).
 #include "kivi_dequant.cuh"
 #include "kivi_tree.cuh"
