@@ -193,13 +193,13 @@ cudaError_t rope_t(const RopeArgs& a, int sms, cudaStream_t s) {
   const int tokens = a.B * a.N;
   constexpr int RPB = kRopeThreads * 8 / D;
   // As many tokens a block (of 8, 4, 2) as leave every SM a block, since a block's table
-  // and its rounds of rows (RPB * kRopeRows at a time) serve all of them; else one token, its heads
-  // spread over blocks that take one round each (each makes the table again).  With
+  // and its rounds of rows (RPB * kRopeRows at a time) serve all of them; else one token,
+  // its heads spread over blocks that take one round each (each makes the table again).  With
   // 1 / 2 / 4 / 8 tokens a block (148 SMs, warm, us): 3102 tokens of 20 heads (binary32,
   // D 64) 37 / 21 / 13 / 8.5; 8191 of 48 heads (binary16, D 128) 174 / 74 / 58 / 53; 420 of
   // those 10.2 / 6.8 / 7.8 / 12.0; 16 of them 4.8 / 5.3 / 7.5 / 11.7.  At a step itself wide
-  // rows would do a little better with the number before (592 tokens of 48 heads: 6.9 with two, 7.9 with
-  // four), narrow ones with the one after.
+  // rows would do a little better with the number before (592 tokens of 48 heads: 6.9 with
+  // two, 7.9 with four), narrow ones with the one after.
   const int TB = tokens >= 8 * sms ? 8 : tokens >= 4 * sms ? 4 : tokens >= 2 * sms ? 2 : 1;
   const int spread = (a.Hq + RPB - 1) / RPB;
   const dim3 grid((unsigned)((tokens + TB - 1) / TB), TB > 1 ? 1 : (unsigned)min(spread, 65535));

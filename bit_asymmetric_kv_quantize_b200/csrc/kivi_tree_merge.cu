@@ -166,9 +166,10 @@ cudaError_t merge_d(const TreeArgs& a, const TreePlan& p, cudaStream_t s) {
 }  // namespace
 
 // The plan of a call.  CUDA cores (binary32): 64 rows a block, or 16 where all fit
-// (four blocks on an SM instead of three; at D 128 of two, whose ranges are cut for three).  Tensor cores: up to 64 rows two blocks of
-// threads on an SM, more in row blocks of equal size up to 128 rows, one block on an SM
-// (both sides measured: kivi_tree_tc.cuh).
+// (four blocks on an SM instead of three; at D 128 of two, whose ranges are cut for
+// three).  Tensor cores: up to 64 rows two blocks of threads on an SM, more in row blocks
+// of equal size up to 128 rows, one block on an SM (both sides measured:
+// kivi_tree_tc.cuh).
 static TreePlan tree_plan(int gq, int N, int dtype, int sms) {
   const int rows = gq * N;
   TreePlan p;
